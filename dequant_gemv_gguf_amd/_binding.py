@@ -1,9 +1,12 @@
-"""ctypes marshalling for libkqgemv.so (see include/kqgemv.h for semantics)."""
+"""ctypes marshalling for libkqgemv.so (see include/kqgemv.h and include/kqkv.h
+for semantics)."""
 import ctypes
 import os
 
 KQ_TYPE_Q4_0, KQ_TYPE_Q8_0, KQ_TYPE_Q2_K, KQ_TYPE_Q3_K = 2, 8, 10, 11
 KQ_TYPE_Q4_K, KQ_TYPE_Q5_K, KQ_TYPE_Q6_K = 12, 13, 14
+KQKV_F16, KQKV_Q8_0 = 1, 8
+KQKV_ROPE_HALVES, KQKV_ROPE_PAIRS = 0, 1
 
 STATUS = {
     0: "KQ_OK", -1: "KQ_ERR_TYPE", -2: "KQ_ERR_SHAPE", -3: "KQ_ERR_M", -4: "KQ_ERR_NULL",
@@ -22,6 +25,34 @@ class GGUFTensor(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char_p), ("type", ctypes.c_int), ("n_dims", ctypes.c_int),
                 ("dims", ctypes.c_int64 * 4), ("offset", ctypes.c_uint64), ("nbytes", ctypes.c_uint64),
                 ("data", ctypes.c_void_p)]
+
+
+class KVCache(ctypes.Structure):
+    """struct kqkv_cache (include/kqkv.h).  k and v: tensors (kept alive by
+    this object) or int addresses."""
+    _fields_ = [("type", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("page_tokens", ctypes.c_int), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p)]
+
+    def __init__(self, type, kv_heads, head_dim, page_tokens, n_pages, k, v):
+        super().__init__(int(type), int(kv_heads), int(head_dim), int(page_tokens), int(n_pages), _addr(k), _addr(v))
+        self.tensors = (k, v)
+        self.ref = ctypes.byref(self)
+
+
+class KVRope(ctypes.Structure):
+    """struct kqkv_rope (include/kqkv.h).  sections: the pairs of each axis;
+    freq_factors: a tensor (kept alive by this object), an int address or
+    None."""
+    _fields_ = [("style", ctypes.c_int), ("rot_dims", ctypes.c_int), ("base", ctypes.c_float),
+                ("n_axes", ctypes.c_int), ("sections", ctypes.c_int * 4), ("freq_factors", ctypes.c_void_p)]
+
+    def __init__(self, style, rot_dims, base, sections=None, freq_factors=None):
+        sections = [int(rot_dims) // 2] if sections is None else [int(n) for n in sections]
+        padded = (ctypes.c_int * 4)(*sections[:4])
+        super().__init__(int(style), int(rot_dims), float(base), len(sections), padded, _addr(freq_factors))
+        self.tensors = (freq_factors,)
+        self.ref = ctypes.byref(self)
 
 
 class KQError(RuntimeError):
@@ -82,6 +113,15 @@ def lib():
         L.kq_streamer_sync.argtypes = [P]
         L.kq_stream_qgemv_multi.argtypes = [P, I, P, P, P, I64, P, I, P]
         L.kq_stream_qgemv.argtypes = [P, I, P, I64, I64, P, I, P]
+        L.kqkv_page_bytes.argtypes = [I, I, I, I]
+        L.kqkv_page_bytes.restype = I64
+        L.kqkv_plan.argtypes = [I, P, P, I, P, I64, P, P, P, I64, P, P, I, P, P, P, P, P, P]
+        L.kqkv_rope_store.argtypes = [P, P, I, P, I64, P, I, P, I64, P, I64, P, I64, P, I64, P]
+        L.kqkv_load.argtypes = [P, I, P, P, P, P]
+        L.kqkv_attn_workspace_bytes.argtypes = [P, I, I, I64, I]
+        L.kqkv_attn_workspace_bytes.restype = ctypes.c_size_t
+        L.kqkv_attn.argtypes = [P, I, I, I64, P, P, P, I64, I, I, P, I64, ctypes.c_float, I, P, I64, P,
+                                ctypes.c_size_t, P, P]
         _lib = L
     return _lib
 
@@ -342,3 +382,60 @@ def kq_stream_qgemv_multi(h, types, Ws, Ns, K, x, M, ys):
 def kq_stream_qgemv(h, qtype, W, N, K, x, M, y):
     _check("kq_stream_qgemv", lib().kq_stream_qgemv(h, int(qtype), _ptr(W), int(N), int(K), _ptr(x), int(M),
                                                     _ptr(y)))
+
+
+# ---- paged key-value cache (include/kqkv.h) -------------------------------------
+# cache: a KVCache, rope: a KVRope (or None).  Tensors or int addresses.  A call
+# goes to the device that its tensors are on, on that device's current stream.
+
+def _device_call(fn, like, stream, *args):
+    """Calls lib().fn(*args, stream) with the tensor `like`'s device current."""
+    f = getattr(_lib or lib(), fn)
+    if stream is None and like is not None and not isinstance(like, int) and like.is_cuda:
+        import torch
+        if like.device.index != torch.cuda.current_device():
+            with torch.cuda.device(like.device):
+                _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+            return
+        stream = torch.cuda.current_stream().cuda_stream
+    elif stream is not None and not isinstance(stream, int):
+        stream = stream.cuda_stream
+    _check(fn, f(*args, stream))
+
+
+def kqkv_page_bytes(qtype, kv_heads, head_dim, page_tokens):
+    r = int(lib().kqkv_page_bytes(int(qtype), int(kv_heads), int(head_dim), int(page_tokens)))
+    if r < 0:
+        raise KQError("kqkv_page_bytes", r)
+    return r
+
+
+def kqkv_plan(B, ctx_len, new_len, page_tokens, table, table_stride, held, held_out, free_pages, n_pages, n_free,
+              n_free_out, T, slots, pos, seq_start, ctx_out, err_flag=None, stream=None):
+    _device_call("kqkv_plan", ctx_len, stream, B, _addr(ctx_len), _addr(new_len), page_tokens, _addr(table),
+                 table_stride, _addr(held), _addr(held_out), _addr(free_pages), n_pages, _addr(n_free),
+                 _addr(n_free_out), T, _addr(slots), _addr(pos), _addr(seq_start), _addr(ctx_out), _addr(err_flag))
+
+
+def kqkv_rope_store(cache, rope, T, pos, pos_stride, slots, q_heads, q, ldq, q_out, ldq_out, k, ldk, v, ldv,
+                    stream=None):
+    _device_call("kqkv_rope_store", q if q is not None else k, stream, cache.ref if cache is not None else None,
+                 rope.ref if rope is not None else None, T, _addr(pos), pos_stride, _addr(slots), q_heads, _addr(q),
+                 ldq, _addr(q_out), ldq_out, _addr(k), ldk, _addr(v), ldv)
+
+
+def kqkv_load(cache, T, slots, k=None, v=None, stream=None):
+    _device_call("kqkv_load", slots, stream, cache.ref if cache is not None else None, T, _addr(slots), _addr(k),
+                 _addr(v))
+
+
+def kqkv_attn_workspace_bytes(cache, B, max_q, max_ctx, q_heads):
+    return int(lib().kqkv_attn_workspace_bytes(cache.ref if cache is not None else None, int(B), int(max_q),
+                                               int(max_ctx), int(q_heads)))
+
+
+def kqkv_attn(cache, B, max_q, max_ctx, ctx_len, seq_start, table, table_stride, q_heads, T, q, ldq, scale, window,
+              out, ldo, workspace=None, workspace_bytes=0, err_flag=None, stream=None):
+    _device_call("kqkv_attn", q, stream, cache.ref if cache is not None else None, B, max_q, max_ctx, _addr(ctx_len),
+                 _addr(seq_start), _addr(table), table_stride, q_heads, T, _addr(q), ldq, scale, window, _addr(out),
+                 ldo, _addr(workspace), workspace_bytes, _addr(err_flag))

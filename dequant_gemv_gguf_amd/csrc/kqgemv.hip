@@ -44,7 +44,7 @@ int launch_mixed_t(int ta, int tb, const std::vector<int> &ia, size_t *pa, const
 // built for), looked up once per device.
 constexpr int CHECKED_DEVICES = 64;
 static std::atomic<int> device_state[CHECKED_DEVICES];   // 0 unknown, 1 gfx950, 2 other
-static int device_check() {
+__attribute__((visibility("hidden"))) int device_check() {
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= CHECKED_DEVICES) return KQ_ERR_DEVICE;
     int st = device_state[dev].load(std::memory_order_acquire);
