@@ -3,7 +3,7 @@
 The library is several objects compiled in parallel: the C ABI
 (csrc/kqgemv.hip), the GGUF reader and the host-streamed calls (csrc/kq_gguf.cpp,
 csrc/kq_stream.cpp, host code), the paged key-value cache (csrc/kq_kv.hip,
-csrc/kq_attn.hip), and csrc/kq_inst.hip once per block format and once per
+csrc/kq_attn.hip, and csrc/kq_attn_inst.hip once per head size), and csrc/kq_inst.hip once per block format and once per
 pair of K-quant formats served by one mixed launch (each instantiates the
 launchers and kernels of its format or pair).  They are linked with
 --no-undefined, so an instantiation missing from the lists below fails the
@@ -57,6 +57,7 @@ def units():
     out = [("kqgemv", "kqgemv.hip", []), ("kq_gguf", "kq_gguf.cpp", []), ("kq_stream", "kq_stream.cpp", []),
            ("kq_mc", "kq_mc.hip", []), ("kq_kv", "kq_kv.hip", []), ("kq_attn", "kq_attn.hip", []),
            ("kq_probe", "kq_probe.hip", []), ("kq_stamps", "kq_stamps.hip", [])]
+    out += [("kq_attn%d" % n, "kq_attn_inst.hip", ["-DKQ_ATTN_NB=%d" % n]) for n in range(1, 9)]
     out += [("kq_type%d" % t, "kq_inst.hip", ["-DKQ_INST_TYPE=%d" % t]) for t in TYPES]
     out += [("kq_mixed%d_%d" % p, "kq_inst.hip", ["-DKQ_INST_A=%d" % p[0], "-DKQ_INST_B=%d" % p[1]])
             for p in PAIRS]

@@ -396,7 +396,7 @@ int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const
                     const float *k, int64_t ldk, const float *v, int64_t ldv, void *stream) {
     int r = cache_check(cache);
     if (r) return r;
-    if (T < 0 || T >= (1 << 27) || q_heads < 0 || q_heads > 1024) return KQ_ERR_SHAPE;
+    if (T < 0 || T >= (1 << 24) || q_heads < 0 || q_heads > 1024) return KQ_ERR_SHAPE;
     Rope ra = {};
     if (rope) {
         if (rope->style != KQKV_ROPE_HALVES && rope->style != KQKV_ROPE_PAIRS) return KQ_ERR_ARG;
@@ -446,7 +446,7 @@ int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const
 int kqkv_load(const kqkv_cache *cache, int T, const int32_t *slots, float *k, float *v, void *stream) {
     const int r = cache_check(cache);
     if (r) return r;
-    if (T < 0 || T >= (1 << 27)) return KQ_ERR_SHAPE;
+    if (T < 0 || T >= (1 << 24)) return KQ_ERR_SHAPE;
     if (T == 0 || (!k && !v)) return KQ_OK;
     if (!slots) return KQ_ERR_NULL;
     if (!aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16)) return KQ_ERR_ALIGN;
