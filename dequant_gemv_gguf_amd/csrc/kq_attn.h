@@ -7,7 +7,7 @@
 // for any m_r: the keys are cut into tiles of 32, each wave keeps a running m,
 // sum l and accumulator o of its tiles, and two such states join as
 //   m = max(m', m''), l = l' 2^(m' - m) + l'' 2^(m'' - m), o likewise.
-// m follows the running maximum only when a score exceeds it by 2^8 (weights
+// m follows the running maximum (Q8_0: see below) only when a score exceeds it by 2^8 (weights
 // stay below 2^14 with the offset below): then o and l are rescaled; most tiles
 // need neither the maximum over the lanes of a row nor a rescaling.
 //
@@ -30,13 +30,21 @@
 // Precision.  A row's q is scaled by a power of two that brings its largest
 // element to [2^10, 2^11) and enters as two fp16 limbs (22 bits); cached values
 // enter as they are (int8 quants are whole fp16 numbers, a block's scale is
-// applied to its 32-element partial score in fp32).  Weights: fp16 cache, two
-// fp16 limbs of 2^6 times the weight; Q8_0 cache, the weight times the value's
-// scale as three bf16 limbs (any magnitude of a scale fits).
+// applied to its 32-element partial score in fp32).  Weights, times 2^6, enter
+// as two fp16 limbs too, in a Q8_0 cache multiplied by the value's scale: m then
+// follows the score plus the exponent of the tile's largest scale, so that the
+// products stay below 2^14 whatever the scales are.  The limbs end at 2^-25, 2^-31
+// of the largest product.
 #pragma once
 
 #include "kq_kv.h"
 
+#ifndef DEPTH_
+#define DEPTH_ 1
+#endif
+#ifndef OCC_
+#define OCC_ (NB <= 4 ? 3 : NB <= 6 ? 2 : 1)
+#endif
 namespace kq {
 namespace kv {
 
@@ -49,6 +57,7 @@ struct Attn {
     const int32_t *ctx_len, *seq_start, *table;
     const float *q;
     float *out, *part;         // part: [item][kv head][row][dim], then [item][kv head][row] (m, l)
+    int4 *info;                // [request] first whole piece, rest (-1: none), pieces
     int32_t *err;
     int64_t stride, ldq, ldo;
     int B, T, max_q, group, window;
@@ -71,178 +80,276 @@ struct Req1 {
     int first, n, ctx, tiles, lo;
 };
 __device__ __forceinline__ Req1 attn_req(const Cache &c, const Attn &a, int b) {
-    Req1 r = {0, 0, 0, 0, 0};
-    if (b >= a.B) return r;
-    r.first = a.seq_start[b];
-    r.n = a.seq_start[b + 1] - r.first;
-    r.ctx = max(a.ctx_len[b], 0);
-    if (r.n <= 0) {
-        r.n = 0;
-        return r;
-    }
-    const int hi = min(r.ctx, attn_room(c, a));
-    const int64_t lo = a.window ? (int64_t)r.ctx - r.n - a.window + 1 : 0;
+    const bool in = b < a.B;
+    const int i = in ? b : 0;
+    const int first = a.seq_start[i], end = a.seq_start[i + 1], ctx = max(a.ctx_len[i], 0);
+    Req1 r;
+    r.first = first;
+    r.n = in ? max(end - first, 0) : 0;
+    r.ctx = ctx;
+    const int hi = min(ctx, attn_room(c, a));
+    const int64_t lo = a.window ? (int64_t)ctx - r.n - a.window + 1 : 0;
     r.lo = (int)(max(min(lo, (int64_t)hi), (int64_t)0) / TILE);
-    r.tiles = (hi + TILE - 1) / TILE - r.lo;
-    if (r.tiles < 0) r.tiles = 0;
+    r.tiles = r.n ? max((hi + TILE - 1) / TILE - r.lo, 0) : 0;
     return r;
 }
 
-// How the requests are cut: `chunk` tiles a piece, so that there are at most
-// a.items pieces (sum of max(1, ceil(tiles / chunk)) <= B + total / chunk).
-__device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, int lane) {
-    if (a.items <= a.B) return INT32_MAX;
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) total += attn_req(c, a, b0 + lane).tiles;
-#pragma unroll
-    for (int s = 32; s; s >>= 1) total += __shfl_xor(total, s);
-    const int64_t extra = a.items - a.B;
-    return (int)max((total + extra - 1) / extra, (int64_t)a.min_tiles);
+// Inclusive prefix sums over the wave, in registers (row shifts, then the row
+// broadcasts).
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_or_0(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ int attn_pieces(const Req1 &r, int chunk) {
-    if (r.n == 0) return 0;
-    return chunk == INT32_MAX || r.tiles <= chunk ? 1 : (r.tiles + chunk - 1) / chunk;
+__device__ __forceinline__ int wave_scan(int x) {
+    x += dpp_or_0<0x111, 0xF>(x);
+    x += dpp_or_0<0x112, 0xF>(x);
+    x += dpp_or_0<0x114, 0xF>(x);
+    x += dpp_or_0<0x118, 0xF>(x);
+    x += dpp_or_0<0x142, 0xA>(x);
+    return x + dpp_or_0<0x143, 0xC>(x);
+}
+__device__ __forceinline__ float wave_sum(float x) {
+    auto add = [](float v, int o) { return v + __builtin_bit_cast(float, o); };
+    auto bits = [](float v) { return __builtin_bit_cast(int, v); };
+    x = add(x, dpp_or_0<0x111, 0xF>(bits(x)));
+    x = add(x, dpp_or_0<0x112, 0xF>(bits(x)));
+    x = add(x, dpp_or_0<0x114, 0xF>(bits(x)));
+    x = add(x, dpp_or_0<0x118, 0xF>(bits(x)));
+    x = add(x, dpp_or_0<0x142, 0xA>(bits(x)));
+    x = add(x, dpp_or_0<0x143, 0xC>(bits(x)));
+    return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(x), 63));
+}
+
+// How the requests are cut: `chunk` tiles a piece, and a rest, so that there
+// are at most a.items pieces (sum of floor(tiles / chunk) <= total / chunk <=
+// items - B, and a rest each).  The sum of up to 4096 counts is taken in fp32 and
+// raised by 2^-16, more than its rounding.  All whole pieces come before all
+// rests: the work-groups that start last are the short ones.
+// (r0: the lane's request of the first 64.)
+__device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, const Req1 &r0, int lane) {
+    if (a.items <= a.B) return INT32_MAX;
+    float total = wave_sum((float)r0.tiles);
+    for (int b0 = 64; b0 < a.B; b0 += 64) total += wave_sum((float)attn_req(c, a, b0 + lane).tiles);
+    const float each = total * (1.f + 1.f / 65536.f) / (float)(a.items - a.B);
+    return max((int)fminf(each, 1e9f) + 1, a.min_tiles);
 }
 
 // Piece `item` (b -1 when there are fewer).  All results are uniform.
 struct Piece {
-    int b, index, of;          // request, which of its pieces
+    int b, index, of;          // request, which of its pieces (the rest is the last)
+    int whole, rest;           // its first whole piece's item, its rest's (-1: none)
     Req1 r;
 };
-__device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, int chunk, int item, int lane) {
-    int before = 0, found = -1, index = 0, of = 0, first = 0, rn = 0, ctx = 0, tiles = 0, lo = 0;
-    for (int b0 = 0; b0 < a.B && found < 0; b0 += 64) {
-        const Req1 r = attn_req(c, a, b0 + lane);
-        const int n = attn_pieces(r, chunk);
-        int s = n;
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(s, d);
-            if (lane >= d) s += o;
+__device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, const Req1 &r0, int chunk, int item,
+                                            int lane) {
+    int found = -1, index = 0, of = 0, w0 = 0, rest0 = 0, first = 0, rn = 0, ctx = 0, tiles = 0, lo = 0;
+    int wholes = 0;
+    auto cut = [&](const Req1 &r, int *w, int *rest) {
+        *w = r.n ? (int)((u32)r.tiles / (u32)chunk) : 0;
+        *rest = r.n && (r.tiles == 0 || r.tiles > *w * chunk) ? 1 : 0;
+    };
+    if (a.B > 64)
+        for (int b0 = 0; b0 < a.B; b0 += 64) {
+            int w, rest;
+            cut(attn_req(c, a, b0 + lane), &w, &rest);
+            wholes += __builtin_amdgcn_readlane(wave_scan(w), 63);
         }
-        const int at = item - before - (s - n);
-        const uint64_t hit = __ballot(at >= 0 && at < n);
+    int wbefore = 0, rbefore = 0;
+    for (int b0 = 0; b0 < a.B && found < 0; b0 += 64) {
+        const Req1 r = b0 ? attn_req(c, a, b0 + lane) : r0;
+        int w, rest;
+        cut(r, &w, &rest);
+        const int ws = wave_scan(w), rs = wave_scan(rest);
+        if (a.B <= 64) wholes = __builtin_amdgcn_readlane(ws, 63);
+        const int wf = wbefore + ws - w, rf = wholes + rbefore + rs - rest;
+        const bool in_w = item >= wf && item < wf + w, in_r = rest && item == rf;
+        const uint64_t hit = __ballot(in_w || in_r);
         const int l = hit ? __builtin_ctzll(hit) : 0;
         if (hit) found = b0 + l;
-        index = __builtin_amdgcn_readlane(at, l);
-        of = __builtin_amdgcn_readlane(n, l);
+        index = __builtin_amdgcn_readlane(in_r ? w : item - wf, l);
+        of = __builtin_amdgcn_readlane(w + rest, l);
+        w0 = __builtin_amdgcn_readlane(wf, l);
+        rest0 = __builtin_amdgcn_readlane(rest ? rf : -1, l);
         first = __builtin_amdgcn_readlane(r.first, l);
         rn = __builtin_amdgcn_readlane(r.n, l);
         ctx = __builtin_amdgcn_readlane(r.ctx, l);
         tiles = __builtin_amdgcn_readlane(r.tiles, l);
         lo = __builtin_amdgcn_readlane(r.lo, l);
-        before += __builtin_amdgcn_readlane(s, 63);
+        wbefore += __builtin_amdgcn_readlane(ws, 63);
+        rbefore += __builtin_amdgcn_readlane(rs, 63);
     }
-    return Piece{found, index, of, Req1{first, rn, ctx, tiles, lo}};
+    return Piece{found, index, of, w0, rest0, Req1{first, rn, ctx, tiles, lo}};
 }
 
-typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef u32 u2 __attribute__((ext_vector_type(2)));
+typedef unsigned short us8 __attribute__((ext_vector_type(8)));
+typedef unsigned short us4 __attribute__((ext_vector_type(4)));
+typedef unsigned short us2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ f4 mma(b8 a, b8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 
-// 8 int8 as fp16: 0x6400 + u is 1024 + u for a byte u.
-__device__ __forceinline__ h8 quants_h8(u2 x) {
+// 8 int8 q as fp16: 0x6400 + u is 1024 + u for the byte u = q + 128.
+__device__ __forceinline__ h8 quants_h8(u32 x0, u32 x1) {
     u4 w;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const u32 u = x[i] ^ 0x80808080u;
+        const u32 u = (i ? x1 : x0) ^ 0x80808080u;
         w[2 * i] = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u);
         w[2 * i + 1] = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
     }
-    h8 h = __builtin_bit_cast(h8, w);
-    return h - (_Float16)1152;
+    return __builtin_bit_cast(h8, w) - (_Float16)1152;
 }
-// 8 int8 as bf16: the upper halves of their fp32 forms (7 bits at most).
-__device__ __forceinline__ b8 quants_b8(u2 x) {
+// (q + 128) 2^-24: the bytes as fp16 subnormals, which the matrix instructions
+// take as they are; two operations less per four quants where the 128 comes
+// off elsewhere.
+__device__ __forceinline__ h8 biased_h8(u32 x0, u32 x1) {
     u4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int v = (int)(x[i / 2] >> (16 * (i % 2)));
-        const float lo = (float)(int8_t)v, hi = (float)(int8_t)(v >> 8);
-        w[i] = __builtin_amdgcn_perm(__builtin_bit_cast(u32, hi), __builtin_bit_cast(u32, lo), 0x07060302u);
+    for (int i = 0; i < 2; ++i) {
+        const u32 u = (i ? x1 : x0) ^ 0x80808080u;
+        w[2 * i] = __builtin_amdgcn_perm(0u, u, 0x0C010C00u);
+        w[2 * i + 1] = __builtin_amdgcn_perm(0u, u, 0x0C030C02u);
     }
-    return __builtin_bit_cast(b8, w);
+    return __builtin_bit_cast(h8, w);
+}
+// x minus a half of h, exactly, in one operation (written as a difference it is
+// a conversion and a subtraction).
+__device__ __forceinline__ float minus_lo(u32 h, float x) {
+    float r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(x));
+    return r;
+}
+__device__ __forceinline__ float minus_hi(u32 h, float x) {
+    float r;
+    asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(x));
+    return r;
 }
 // x = hi + lo to 22 bits: hi rounded to zero, lo the rest.
 __device__ __forceinline__ void limbs(const float *x, h8 *hi, h8 *lo) {
     u4 a, b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const auto h = __builtin_amdgcn_cvt_pkrtz(x[2 * i], x[2 * i + 1]);
-        const auto l = __builtin_amdgcn_cvt_pkrtz(x[2 * i] - (float)h[0], x[2 * i + 1] - (float)h[1]);
-        a[i] = __builtin_bit_cast(u32, h);
-        b[i] = __builtin_bit_cast(u32, l);
+        a[i] = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(x[2 * i], x[2 * i + 1]));
+        b[i] = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(minus_lo(a[i], x[2 * i]), minus_hi(a[i], x[2 * i + 1])));
     }
     *hi = __builtin_bit_cast(h8, a);
     *lo = __builtin_bit_cast(h8, b);
 }
-// x = l[0] + l[1] + l[2] to 24 bits, each limb the upper half of the rest.
-__device__ __forceinline__ void limbs3(const float *x, b8 *l) {
-    float r[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = x[i];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        u4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const u32 a = __builtin_bit_cast(u32, r[2 * i]), b = __builtin_bit_cast(u32, r[2 * i + 1]);
-            w[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-            if (k < 2) {
-                r[2 * i] -= __builtin_bit_cast(float, a & 0xFFFF0000u);
-                r[2 * i + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
-            }
-        }
-        l[k] = __builtin_bit_cast(b8, w);
-    }
+
+// A tile's K and V of a lane as loaded (16 bytes an instruction and lane
+// wherever the rows allow it).  NB = dim / 32.
+template <bool Q8, int NB> struct Tile {
+    static constexpr int W = Q8 ? 2 : 4;   // dwords of one operand
+    u32 k[2][NB * W], v[2 * NB * W];
+    h8 s;                      // Q8_0: 16 bytes of the tile's scales
+    u32 wrong;                 // bit u: group u lies in a page that is none
+};
+
+// A K operand of 16 rows wants 4 pieces of every row at once, but a load that
+// takes 64 bytes of 16 rows asks the cache for twice as many lines as one that
+// takes 128 bytes of 8 rows, and those requests are what the stream waits for.
+// So a unit of 128 bytes of a row (two fp16 operands, or four int8 ones) is
+// loaded for rows 0..7 (the tile's first 16-token group) by one instruction and
+// for rows 8..15 (the second) by another, lane (m, g) taking 16-byte piece
+// 4 (m / 8) + g of row m % 8; half of the lanes' registers then change places
+// across the row of 16 lanes.
+constexpr int ROW_ROR8 = 0x128;
+__device__ __forceinline__ void swap_rows(u32 &x, u32 &y) {
+    const int p = __builtin_amdgcn_update_dpp((int)x, (int)y, ROW_ROR8, 0xF, 0xC, false);
+    const int q = __builtin_amdgcn_update_dpp((int)y, (int)x, ROW_ROR8, 0xF, 0x3, false);
+    x = (u32)p;
+    y = (u32)q;
+}
+// Lanes 32..63 of x change places with lanes 0..31 of y; odd rows of 16 lanes
+// of x with even ones of y.
+__device__ __forceinline__ void swap_halves(u32 &x, u32 &y) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, y, false, false);
+    x = r[0];
+    y = r[1];
+}
+__device__ __forceinline__ void swap_odd_rows(u32 &x, u32 &y) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+    x = r[0];
+    y = r[1];
 }
 
-// One tile of a lane as loaded.  NB = dim / 32.
-template <bool Q8, int NB> struct KTile;
-template <int NB> struct KTile<false, NB> { u4 x[2][NB]; };
-template <int NB> struct KTile<true, NB> { u2 x[2][NB]; h8 s[NB]; };
-template <bool Q8, int NB> struct VTile;
-template <int NB> struct VTile<false, NB> { u4 x[2 * NB]; };
-template <int NB> struct VTile<true, NB> { u2 x[2 * NB]; h8 s[NB]; };
-
-// lane (m, g): K rows 8 (m / 4) + 4 t + m % 4 of the tile, elements 32 s + 8 g ..;
-// `at` is the 16-token group of the lane's rows.
+// Row of K that lane m's operand stands for in subtile t, within its group:
+// 8 (m / 4 % 2) + 4 t + m % 4 (keys 8 (m / 4) + 4 t + m % 4 of the tile).
+// k0, k1: the head's rows of the tile's two groups.
 template <bool Q8, int NB>
-__device__ __forceinline__ void load_k(KTile<Q8, NB> &k, const uint8_t *mine, const uint8_t *scales, int lane) {
-    constexpr int D = 32 * NB;
-    const int m = lane & 15, g = lane >> 4, row = (8 * (m >> 2) + (m & 3)) & 15;
-    constexpr int E = Q8 ? 1 : 2;
-    const uint8_t *p = mine + row * D * E + g * 8 * E;
+__device__ __forceinline__ void load_k(Tile<Q8, NB> &to, const uint8_t *k0, const uint8_t *k1, int lane) {
+    constexpr int E = Q8 ? 1 : 2, RB = 32 * NB * E, UNITS = RB / 128, W = Tile<Q8, NB>::W;
+    const int m = lane & 15, g = lane >> 4, row = 8 * ((m >> 2) & 1) + (m & 3);
+    const u32 at = row * RB + ((m >> 3) * 4 + g) * 16;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int s = 0; s < NB; ++s) {
-            if constexpr (Q8) k.x[t][s] = *(const u2 *)(p + (4 * t * D + 32 * s));
-            else k.x[t][s] = *(const u4 *)(p + (4 * t * D + 32 * s) * 2);
-        }
-    if constexpr (Q8) {
-        const uint8_t *q = scales + (g & 1) * 16;
+        for (int u = 0; u < UNITS; ++u) {
+            const u4 a = *(const u4 *)(k0 + at + (4 * t * RB + 128 * u)), b = *(const u4 *)(k1 + at + (4 * t * RB + 128 * u));
 #pragma unroll
-        for (int s = 0; s < NB; ++s) k.s[s] = *(const h8 *)(q + s * 32);
+            for (int i = 0; i < 4; ++i) {
+                to.k[t][8 * u + i] = a[i];
+                to.k[t][8 * u + 4 + i] = b[i];
+            }
+        }
+    // what is left of a row: 64 bytes as they are, then (int8) 32
+    if constexpr (RB % 128 != 0) {
+        const u64 step = (u64)(k1 - k0);
+        const uint8_t *p = k0 + ((m & 8) ? step : 0) + row * RB + 128 * UNITS;
+        constexpr int DONE = 8 * UNITS;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            if constexpr (RB % 128 >= 64) {
+                const u4 a = *(const u4 *)(p + 16 * g + 4 * t * RB);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) to.k[t][DONE + i] = a[i];
+            }
+            if constexpr (RB % 64 != 0) {
+                const u2 a = *(const u2 *)(p + (RB % 128 - 32) + 16 * (g & 1) + 8 * (g >> 1) + 4 * t * RB);
+                to.k[t][NB * W - 2] = a[0];
+                to.k[t][NB * W - 1] = a[1];
+            }
+        }
     }
 }
-// lane (m, g): dims 16 n + m, keys 8 g .. 8 g + 7.
-template <bool Q8, int NB>
-__device__ __forceinline__ void load_v(VTile<Q8, NB> &v, const uint8_t *mine, const uint8_t *scales, int lane) {
-    const int m = lane & 15, g = lane >> 4;
-    constexpr int E = Q8 ? 1 : 2;
-    const uint8_t *p = mine + (m * 16 + (g & 1) * 8) * E;
+// The loaded registers as operands: block b's in k[t][b * W ..], whose lane group
+// g holds elements 8 g .. (fp16), or 16 (g % 2) + 8 (g / 2) .. (int8).
+template <bool Q8, int NB> __device__ __forceinline__ void order_k(Tile<Q8, NB> &T) {
+    constexpr int RB = 32 * NB * (Q8 ? 1 : 2), UNITS = RB / 128;
 #pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) {
-        if constexpr (Q8) v.x[n] = *(const u2 *)(p + n * 256);
-        else v.x[n] = *(const u4 *)(p + n * 512);
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int u = 0; u < UNITS; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) swap_rows(T.k[t][8 * u + i], T.k[t][8 * u + 4 + i]);
+        if constexpr (Q8) {
+#pragma unroll
+            for (int h = 0; h < RB / 64; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) swap_halves(T.k[t][4 * h + i], T.k[t][4 * h + 2 + i]);
+        }
     }
-    if constexpr (Q8) {
-        const uint8_t *q = scales + (g & 1) * 16;
+}
+
+// lane (m, g): dims 16 n + m, keys 8 g .. 8 g + 7.  int8: one load brings the 16
+// tokens of dim 16 n + m for n even in lanes g % 2 == 0 and odd in the others,
+// which then change halves.
+template <bool Q8, int NB>
+__device__ __forceinline__ void load_v(Tile<Q8, NB> &to, const uint8_t *mine, int lane) {
+    const int m = lane & 15, g = lane >> 4;
+    const uint8_t *p = Q8 ? mine + (16 * (g & 1) + m) * 16 : mine + (m * 16 + (g & 1) * 8) * 2;
 #pragma unroll
-        for (int s = 0; s < NB; ++s) v.s[s] = *(const h8 *)(q + s * 32);
+    for (int n = 0; n < (Q8 ? NB : 2 * NB); ++n) {
+        const u4 a = *(const u4 *)(p + n * 512);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to.v[4 * n + i] = a[i];
+    }
+}
+template <bool Q8, int NB> __device__ __forceinline__ void order_v(Tile<Q8, NB> &T) {
+    if constexpr (Q8) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) swap_odd_rows(T.v[4 * n + i], T.v[4 * n + 2 + i]);
     }
 }
 
@@ -260,9 +367,15 @@ __device__ __forceinline__ float across_groups_sum(float x) {
 // w / row_tiles + i * (4 / row_tiles) of the piece (waves that share a key tile
 // read it through the caches); the waves of a row tile join through LDS.
 template <bool Q8, int NB>
-__global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cache c, Attn a) {
+__global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn a) {
     constexpr int D = 32 * NB, LD = D + 4;
-    __shared__ float lds[ATTN_WAVES * 16 * (LD + 2)];   // [wave][16][LD], then [wave][16] (m, l)
+    // While the tiles go by, a wave's part holds its q limbs (operands as lanes read them), the blocks' sums of
+    // q and two tiles' scales; at the
+    // end, [wave][16][LD] outputs, then [wave][16] (m, l).
+    constexpr int QB = NB * 2 * 1024, OB = Q8 ? NB * 256 : 0, SB = Q8 ? NB * 128 : 0, PART = QB + OB + 2 * SB;
+    constexpr int JOIN = 16 * (LD + 2) * 4;
+    __shared__ __align__(16) uint8_t lds_[ATTN_WAVES * (PART > JOIN ? PART : JOIN)];
+    float *lds = (float *)lds_;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int groups = (a.rows_cap + 16 * a.row_tiles - 1) / (16 * a.row_tiles);
     // pieces that read the same keys (row groups) lie 8 blocks apart: one L2
@@ -270,9 +383,12 @@ __global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cac
     const int unit = oct * 8 + (in & 7), rgroup = in >> 3;
     if (unit >= a.items * c.kv_heads) return;
     const int item = unit / c.kv_heads, head = unit - item * c.kv_heads;
-    const int chunk = attn_chunk(c, a, lane);
-    const Piece pc = attn_piece(c, a, chunk, item, lane);
+    const Req1 r0 = attn_req(c, a, lane);
+    const int chunk = attn_chunk(c, a, r0, lane);
+    const Piece pc = attn_piece(c, a, r0, chunk, item, lane);
     if (pc.b < 0) return;
+    if (a.items > a.B && pc.index == 0 && head == 0 && rgroup == 0 && threadIdx.x == 0)
+        a.info[pc.b] = int4{pc.whole, pc.rest, pc.of, 0};
     const int rows = min(pc.r.n, a.max_q) * a.group;
     const int row0 = rgroup * 16 * a.row_tiles;
     if (row0 >= rows) return;
@@ -294,38 +410,21 @@ __global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cac
     const int lo = a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0;
     if ((int64_t)pc.r.ctx > room && a.err && threadIdx.x == 0) a.err[0] = 1;
 
-    const int t0 = pc.r.lo + pc.index * (pc.of == 1 ? 0 : chunk);
-    const int t1 = pc.of == 1 ? pc.r.lo + pc.r.tiles : min(t0 + chunk, pc.r.lo + pc.r.tiles);
+    const int t0 = pc.r.lo + (pc.index ? pc.index * chunk : 0);
+    const int t1 = pc.index == pc.of - 1 ? pc.r.lo + pc.r.tiles : t0 + chunk;
     const int first = t0 + kw, N = first < t1 ? (t1 - first + kws - 1) / kws : 0;
 
-    // q as two fp16 limbs
-    h8 qh_[NB], ql_[NB];
-    float unscale;
+    // the row's q (its loads go out first, the limbs are made while the first tile's are on their way)
+    f4 x[2 * NB];
     {
-        float x[NB][8], top = 0.f;
-        const float *qp = a.q + (live ? trow : 0) * a.ldq + (int64_t)qh * D + 8 * g;
+        const float *qp = a.q + (live ? trow : 0) * a.ldq + (int64_t)qh * D + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
 #pragma unroll
         for (int s = 0; s < NB; ++s)
 #pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                f4 v = {0.f, 0.f, 0.f, 0.f};
-                if (live) v = *(const f4 *)(qp + 32 * s + e);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[s][e + i] = v[i] * a.scale;
-                    top = fmaxf(top, fabsf(x[s][e + i]));
-                }
+            for (int e = 0; e < 2; ++e) {
+                x[2 * s + e] = f4{0.f, 0.f, 0.f, 0.f};
+                if (live) x[2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
             }
-        top = across_groups_max(top);
-        int ex = 0;
-        if (top > 0.f && top < INFINITY) ex = min(11 - ilogbf(top) - 1, 120);
-        unscale = ldexpf(1.f, -ex);
-#pragma unroll
-        for (int s = 0; s < NB; ++s) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[s][e] = ldexpf(x[s][e], ex);
-            limbs(x[s], &qh_[s], &ql_[s]);
-        }
     }
 
     f4 o[2 * NB];
@@ -335,82 +434,152 @@ __global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cac
 
     const u32 gp = c.page_tokens >> 4, quants = c.page_tokens * D;
     const uint8_t *kb = c.k + (u64)head * c.head_bytes, *vb = c.v + (u64)head * c.head_bytes;
-    // pages of the wave's next 32 tiles: lane i holds group i % 2 of tile i / 2, page << 4 | group in page
-    u32 ids = 0;
+    // Pages of 32 tiles of the wave: lane i holds group i % 2 of tile i / 2, page << 4 | group in page.  The next 32 tiles'
+    // table entries are asked for when these are taken up.
+    u32 ids = 0, raw = 0;
     uint64_t bad = 0;
-    auto fetch_ids = [&](int n) {
+    auto group_of = [&](int n, bool *in) {
         const int grp = 2 * (first + kws * (n + (lane >> 1))) + (lane & 1);
-        const bool in = n + (lane >> 1) < N && grp * 16 < hi_all && grp * 16 + 16 > lo_all;
-        u32 id = 0;
-        bool wrong = false;
-        if (in) {
-            const u32 page = (u32)grp / gp;
-            id = (u32)a.table[pc.b * a.stride + page];
-            wrong = id >= c.n_pages;
-            id = wrong ? 0 : (id << 4 | ((u32)grp - page * gp));
-        }
-        ids = id;
+        *in = n + (lane >> 1) < N && grp * 16 < hi_all && grp * 16 + 16 > lo_all;
+        return grp;
+    };
+    auto ask_ids = [&](int n) {
+        bool in;
+        const int grp = group_of(n, &in);
+        if (in) raw = (u32)a.table[pc.b * a.stride + (u32)grp / gp];
+    };
+    auto take_ids = [&](int n) {
+        bool in;
+        const int grp = group_of(n, &in);
+        const bool wrong = in && raw >= c.n_pages;
+        ids = in && !wrong ? raw << 4 | ((u32)grp % gp) : 0;
         bad = __ballot(wrong);
         if (wrong && a.err) a.err[0] = 1;
     };
-    // byte offsets of the tile's two 16-token groups in K and V alike: quants or halves, and scales
-    struct Where { u64 x0, x1, s0, s1; };
+    // Byte offsets of the tile's first 16-token group in K and V alike (quants or halves, and scales), and of the second
+    // from there.  (A lane's group is an offset times 0 or 1: chosen between two members of a struct, the compiler put the
+    // struct in scratch memory.)
+    struct Where { u64 x0, dx, s0, ds; };
     auto where = [&](int n) {
         Where w;
         const u32 i0 = (u32)__builtin_amdgcn_readlane((int)ids, 2 * (n & 31));
         const u32 i1 = (u32)__builtin_amdgcn_readlane((int)ids, 2 * (n & 31) + 1);
         const u64 p0 = (u64)(i0 >> 4) * (u64)c.page_bytes, p1 = (u64)(i1 >> 4) * (u64)c.page_bytes;
         w.x0 = p0 + (i0 & 15) * (16 * D * (Q8 ? 1 : 2));
-        w.x1 = p1 + (i1 & 15) * (16 * D * (Q8 ? 1 : 2));
+        w.dx = p1 + (i1 & 15) * (16 * D * (Q8 ? 1 : 2)) - w.x0;
         w.s0 = p0 + quants + (i0 & 15) * (NB * 32);
-        w.s1 = p1 + quants + (i1 & 15) * (NB * 32);
+        w.ds = p1 + quants + (i1 & 15) * (NB * 32) - w.s0;
         return w;
     };
-    KTile<Q8, NB> kt;
-    VTile<Q8, NB> vt;
-    // K rows of lane m are in group m / 8, its scales and V keys in group g / 2
-    auto get_k = [&](const Where &w) { load_k<Q8, NB>(kt, kb + ((m & 8) ? w.x1 : w.x0), kb + ((g & 2) ? w.s1 : w.s0), lane); };
-    auto get_v = [&](const Where &w) { load_v<Q8, NB>(vt, vb + ((g & 2) ? w.x1 : w.x0), vb + ((g & 2) ? w.s1 : w.s0), lane); };
+    // V keys of lane (m, g) are in group g / 2; of the scales [K, V][group][block][16] a lane takes the
+    // 16 bytes at 16 * (lane % 8 NB)
+    const int sl = lane % (8 * NB);
+    const uint8_t *sb = (sl / (4 * NB) ? vb : kb) + (sl % (2 * NB)) * 16;
+    const bool second = (sl / (2 * NB)) & 1;
+    auto get_k = [&](Tile<Q8, NB> &to, const Where &w) {
+        load_k<Q8, NB>(to, kb + w.x0, kb + w.x0 + w.dx, lane);
+        if constexpr (Q8) to.s = *(const h8 *)(sb + w.s0 + (second ? w.ds : 0));
+    };
+    auto get_v = [&](Tile<Q8, NB> &to, const Where &w) { load_v<Q8, NB>(to, vb + w.x0 + ((g & 2) ? w.dx : 0), lane); };
+    auto wrong_of = [&](int n) { return (u32)(bad >> (2 * (n & 31))) & 3; };
 
+    constexpr int DEPTH = DEPTH_;
+    Tile<Q8, NB> tiles[DEPTH];
     if (N > 0) {
-        fetch_ids(0);
-        const Where w = where(0);
-        get_k(w);
-        get_v(w);
+        ask_ids(0);
+        take_ids(0);
+#pragma unroll
+        for (int u = 0; u < DEPTH; ++u) {
+            const int n = min(u, N - 1);
+            const Where w = where(n);
+            get_k(tiles[u], w);
+            get_v(tiles[u], w);
+            tiles[u].wrong = wrong_of(n);
+        }
+        ask_ids(32);
     }
-    for (int n = 0; n < N; ++n) {
+    // q as two fp16 limbs, in LDS: read again for every tile, they leave their registers to tiles on the way
+    uint8_t *part = lds_ + wave * PART;
+    float unscale;
+    {
+        float top = 0.f;
+#pragma unroll
+        for (int s = 0; s < 2 * NB; ++s) {
+            x[s] *= a.scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[s][i]));
+        }
+        top = across_groups_max(top);
+        int ex = 0;
+        if (top > 0.f && top < INFINITY) ex = min(10 - ilogbf(top), 120);
+        unscale = ldexpf(1.f, (Q8 ? 24 : 0) - ex);
+#pragma unroll
+        for (int s = 0; s < NB; ++s) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[2 * s + e / 4][e % 4], ex);
+            h8 hi8, lo8;
+            limbs(y, &hi8, &lo8);
+            if constexpr (Q8) {
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += (float)hi8[e] + (float)lo8[e];
+                // -128 2^-24 times the sum of q's block
+                *(float *)(part + QB + s * 256 + lane * 4) = across_groups_sum(sum) * (-128.f / 16777216.f);
+            }
+            *(h8 *)(part + (2 * s) * 1024 + lane * 16) = hi8;
+            *(h8 *)(part + (2 * s + 1) * 1024 + lane * 16) = lo8;
+        }
+    }
+    u32 qat = (u32)lane * 16;
+    auto tile_step = [&](Tile<Q8, NB> &T, int n, int stage) __attribute__((always_inline)) {
+        // (q's address is made anew for each tile, so that the reads stay here)
+        asm volatile("" : "+v"(qat));
+        uint8_t *scales = part + QB + OB + stage * SB;
+        if constexpr (Q8) *(h8 *)(scales + sl * 16) = T.s;
         // scores of the lane's 8 keys, times 1 / unscale
+        order_k<Q8, NB>(T);
         float s[8];
+        f4 d[2], d2[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            f4 d = {0.f, 0.f, 0.f, 0.f}, d2 = d;
+        for (int t = 0; t < 2; ++t) d[t] = d2[t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                if constexpr (Q8) {
-                    const h8 k = quants_h8(kt.x[t][b]);
-                    const f4 z = {0.f, 0.f, 0.f, 0.f};
-                    const f4 x = mma(k, qh_[b], mma(k, ql_[b], z));
+        for (int b = 0; b < NB; ++b) {
+            const h8 qh8 = *(const h8 *)(part + (2 * b) * 1024 + qat), ql8 = *(const h8 *)(part + (2 * b + 1) * 1024 + qat);
+            if constexpr (Q8) {
+                const float off = *(const float *)(part + QB + b * 256 + (qat >> 2));
+                const h8 ks = *(const h8 *)(scales + ((g >> 1) * NB + b) * 32 + (g & 1) * 16);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[i] = fmaf(x[i], (float)kt.s[b][4 * t + i], d[i]);
-                } else {
-                    const h8 k = __builtin_bit_cast(h8, kt.x[t][b]);
-                    d = mma(k, qh_[b], d);
-                    d2 = mma(k, ql_[b], d2);
+                for (int t = 0; t < 2; ++t) {
+                    const h8 k = biased_h8(T.k[t][2 * b], T.k[t][2 * b + 1]);
+                    const f4 y = mma(k, qh8, mma(k, ql8, f4{off, off, off, off}));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[t][i] = fmaf(y[i], (float)ks[4 * t + i], d[t][i]);
+                }
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const h8 k = __builtin_bit_cast(h8, u4{T.k[t][4 * b], T.k[t][4 * b + 1], T.k[t][4 * b + 2], T.k[t][4 * b + 3]});
+                    d[t] = mma(k, qh8, d[t]);
+                    d2[t] = mma(k, ql8, d2[t]);
                 }
             }
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[4 * t + i] = Q8 ? d[i] : d[i] + d2[i];
-        }
-        const uint64_t wrong = (bad >> (2 * (n & 31))) & 3;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[4 * t + i] = Q8 ? d[t][i] : d[t][i] + d2[t][i];
+        const u32 wrong = T.wrong;
         const int tile = first + kws * n;
-        // the next tile's keys (the last tile's again behind it)
-        Where next;
-        {
-            const int nn = n + 1 < N ? n + 1 : n;
-            if (nn != n && (nn & 31) == 0) fetch_ids(nn);
-            next = where(nn);
-            get_k(next);
+        // the keys of the tile after the next (behind the last, the last tile's again)
+        const int nn = min(n + DEPTH, N - 1);
+        if (nn == n + DEPTH && (nn & 31) == 0) {
+            take_ids(nn);
+            ask_ids(nn + 32);
         }
+        const Where next = where(nn);
+        get_k(T, next);
+        T.wrong = wrong_of(nn);
         const bool edge = wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min;
         uint32_t gone = 0;                       // keys of the lane that no row may touch
         if (edge) {
@@ -422,10 +591,29 @@ __global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cac
                 s[e] = out || key >= hi || key < lo ? -INFINITY : s[e];
             }
         }
+        [[maybe_unused]] h8 vs[Q8 ? NB : 1];
         float top = s[0];
 #pragma unroll
         for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
         top *= unscale;
+        if constexpr (Q8) {
+            // weights are multiplied by the values' scales before they are rounded: m follows the product
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                vs[b] = *(const h8 *)(scales + ((2 + (g >> 1)) * NB + b) * 32 + (g & 1) * 16);
+            if (edge) {
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) vs[b][e] = (gone >> e) & 1 ? (_Float16)0 : vs[b][e];
+            }
+            us8 big = __builtin_bit_cast(us8, vs[0]);    // (scales are not negative: they order like integers)
+#pragma unroll
+            for (int b = 1; b < NB; ++b) big = __builtin_elementwise_max(big, __builtin_bit_cast(us8, vs[b]));
+            const us4 b4 = __builtin_elementwise_max(__builtin_shufflevector(big, big, 0, 1, 2, 3), __builtin_shufflevector(big, big, 4, 5, 6, 7));
+            const us2 b2 = __builtin_elementwise_max(__builtin_shufflevector(b4, b4, 0, 1), __builtin_shufflevector(b4, b4, 2, 3));
+            top += (float)__builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, b2[0] > b2[1] ? b2[0] : b2[1]));
+        }
         if (__any(top > mx + SLACK)) {
             const float now = fmaxf(mx, across_groups_max(top));
             const float keep = __builtin_amdgcn_exp2f(mx - now);
@@ -440,44 +628,44 @@ __global__ __launch_bounds__(ATTN_THREADS, NB <= 4 ? 2 : 1) void attn_kernel(Cac
             p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], unscale, LIFT - mx));
             l += p[e];
         }
+        order_v<Q8, NB>(T);
         if constexpr (Q8) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float x[8];
+                float w[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = p[e] * (float)vt.s[b][e];
-                if (edge) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] = (gone >> e) & 1 ? 0.f : x[e];
-                }
-                b8 w[3];
-                limbs3(x, w);
-                const b8 v0 = quants_b8(vt.x[2 * b]), v1 = quants_b8(vt.x[2 * b + 1]);
-#pragma unroll
-                for (int k = 2; k >= 0; --k) {
-                    o[2 * b] = mma(v0, w[k], o[2 * b]);
-                    o[2 * b + 1] = mma(v1, w[k], o[2 * b + 1]);
-                }
+                for (int e = 0; e < 8; ++e) w[e] = fmaf(p[e], (float)vs[b][e], 0.f);   // (one operation on the half as it is)
+                h8 ph, pl;
+                limbs(w, &ph, &pl);
+                const h8 v0 = quants_h8(T.v[4 * b], T.v[4 * b + 1]), v1 = quants_h8(T.v[4 * b + 2], T.v[4 * b + 3]);
+                o[2 * b] = mma(v0, ph, mma(v0, pl, o[2 * b]));
+                o[2 * b + 1] = mma(v1, ph, mma(v1, pl, o[2 * b + 1]));
             }
         } else {
             if (edge) {
-                u4 keep;
+                u32 keep[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     keep[i] = ((gone >> (2 * i)) & 1 ? 0u : 0xFFFFu) | ((gone >> (2 * i + 1)) & 1 ? 0u : 0xFFFF0000u);
 #pragma unroll
-                for (int k = 0; k < 2 * NB; ++k) vt.x[k] &= keep;
+                for (int k = 0; k < 8 * NB; ++k) T.v[k] &= keep[k & 3];
             }
             h8 ph, pl;
             limbs(p, &ph, &pl);
+            auto vop = [&](int k) { return __builtin_bit_cast(h8, u4{T.v[4 * k], T.v[4 * k + 1], T.v[4 * k + 2], T.v[4 * k + 3]}); };
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(__builtin_bit_cast(h8, vt.x[k]), ph, o[k]);
+            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(vop(k), ph, o[k]);
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(__builtin_bit_cast(h8, vt.x[k]), pl, o[k]);
+            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(vop(k), pl, o[k]);
         }
-        get_v(next);
+        get_v(T, next);
+    };
+    for (int n = 0; n < N; n += DEPTH) {
+        tile_step(tiles[0], n, 0);
+        if (DEPTH > 1 && n + 1 < N) tile_step(tiles[DEPTH - 1], n + 1, 1);
     }
     l = across_groups_sum(l);
+    __syncthreads();                            // the q limbs' place is taken by what follows
 
     // join the waves of each row tile
     float *stat = lds + ATTN_WAVES * 16 * LD;
@@ -529,26 +717,15 @@ __global__ __launch_bounds__(ATTN_THREADS) void attn_join_kernel(Cache c, Attn a
     const int lane = threadIdx.x & 63;
     const int b = blockIdx.x / (c.kv_heads * a.rows_cap), left = blockIdx.x - b * (c.kv_heads * a.rows_cap);
     const int head = left / a.rows_cap, row = left - head * a.rows_cap;
-    const int chunk = attn_chunk(c, a, lane);
-    // the request's first piece: the pieces before it
-    int before = 0;
-    Req1 mine = {0, 0, 0, 0, 0};
-    for (int b0 = 0; b0 <= b; b0 += 64) {
-        const Req1 r = attn_req(c, a, b0 + lane);
-        int n = b0 + lane < b ? attn_pieces(r, chunk) : 0;
-#pragma unroll
-        for (int s = 32; s; s >>= 1) n += __shfl_xor(n, s);
-        before += n;
-        if (b < b0 + 64) {
-            mine.first = __builtin_amdgcn_readlane(r.first, b - b0);
-            mine.n = __builtin_amdgcn_readlane(r.n, b - b0);
-            mine.tiles = __builtin_amdgcn_readlane(r.tiles, b - b0);
-        }
-    }
-    const int pieces = attn_pieces(mine, chunk);
-    if (pieces <= 1 || row >= min(mine.n, a.max_q) * a.group) return;
+    const int first = a.seq_start[b], n = a.seq_start[b + 1] - first;
+    const int4 info = a.info[b];                      // (a request without rows has none: left by another call)
+    if (n <= 0 || row >= min(n, a.max_q) * a.group || info.z <= 1) return;
+    const int pieces = info.z, whole = info.x, rest = info.y;
     const float *ml = a.part + (int64_t)a.items * c.kv_heads * a.rows_cap * D;
-    auto at = [&](int i) { return ((int64_t)(before + i) * c.kv_heads + head) * a.rows_cap + row; };
+    auto at = [&](int i) {
+        const int item = i == pieces - 1 && rest >= 0 ? rest : whole + i;
+        return ((int64_t)item * c.kv_heads + head) * a.rows_cap + row;
+    };
     float M = NONE;
     for (int i = lane; i < pieces; i += 64) M = fmaxf(M, ml[at(i) * 2]);
 #pragma unroll
@@ -573,7 +750,7 @@ __global__ __launch_bounds__(ATTN_THREADS) void attn_join_kernel(Cache c, Attn a
             L += ls[w];
         }
         const int j = row / a.group;
-        const int64_t to = (int64_t)mine.first + j;
+        const int64_t to = (int64_t)first + j;
         if (to >= 0 && to < a.T)
             *(f4 *)(a.out + to * a.ldo + (int64_t)(head * a.group + row - j * a.group) * D + d) =
                 L == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : x * (1.f / L);

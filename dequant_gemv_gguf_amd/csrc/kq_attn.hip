@@ -10,7 +10,13 @@ using namespace kq::kv;
 
 // Work-groups that the requests' tokens are cut into (beside one per request
 // and kv head), and the fewest tiles of such a piece.
-constexpr int PIECES = 1024, MIN_TILES = 8;
+#ifndef PIECES_
+#define PIECES_ 1024
+#endif
+#ifndef MINT_
+#define MINT_ 8
+#endif
+constexpr int PIECES = PIECES_, MIN_TILES = MINT_;
 
 // The split of a call: 16-row tiles per work-group (1, 2 or 4: the four waves
 // of a work-group share the rows first, then the keys) and the number of
@@ -24,6 +30,12 @@ static void attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, i
     const int64_t tiles = (max_ctx + TILE - 1) / TILE;
     const int64_t most = (int64_t)B * ((tiles + MIN_TILES - 1) / MIN_TILES);
     a->items = (int)std::min<int64_t>(most, B + std::max(1, PIECES / (c->kv_heads * groups)));
+}
+
+// The pieces' unnormalised outputs with their m and l, then the requests'
+// pieces (a.info), at a multiple of 16 bytes.
+static size_t part_bytes(const kqkv_cache *c, const Attn &a, int q_heads, int max_q) {
+    return ((size_t)a.items * q_heads * max_q * (c->head_dim + 2) * sizeof(float) + 15) & ~(size_t)15;
 }
 
 static int attn_shape(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, int q_heads) {
@@ -42,7 +54,7 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
     if (attn_shape(cache, B, max_q, max_ctx, q_heads)) return 0;
     Attn a;
     attn_split(cache, B, max_q, max_ctx, q_heads, &a);
-    return a.items <= B ? 0 : (size_t)a.items * q_heads * max_q * (cache->head_dim + 2) * sizeof(float);
+    return a.items <= B ? 0 : part_bytes(cache, a, q_heads, max_q) + (size_t)B * sizeof(int4);
 }
 
 int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const int32_t *ctx_len,
@@ -71,6 +83,7 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     a.q = q;
     a.out = out;
     a.part = (float *)workspace;
+    a.info = (int4 *)((char *)workspace + part_bytes(cache, a, q_heads, max_q));
     a.err = err_flag;
     a.stride = table_stride;
     a.ldq = ldq;

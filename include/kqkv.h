@@ -26,7 +26,8 @@
  *   V: groups of 16 tokens, transposed: (t, d) at (t / 16) * 16 * D + d * 16 + t % 16
  * as fp16 (KQKV_F16), or as int8 quants (KQKV_Q8_0) that are followed by their
  * fp16 scales, one per token and 32 elements, for K and V alike at
- * (t / 16) * (D / 32) * 16 + (d / 32) * 16 + t % 16; a value is scale * quant.
+ * (t / 16) * (D / 32) * 16 + (d / 32) * 16 + t % 16; a value is scale * quant, and
+ * no scale is negative.
  * Token t of page p is slot p * P + t.  Memory that holds no token may hold
  * anything, NaN included.
  *
@@ -186,7 +187,8 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
  * A page outside [0, n_pages), or a length past table_stride * P (or 2^31 - 64), takes its
  * tokens out of the sum and sets *err_flag; a negative length counts as 0.
  * Accumulation is fp32; q and the weights enter the matrix instructions as two
- * fp16 limbs (about 22 bits), the cached values as they are.  Reruns are
+ * fp16 limbs (about 22 bits), the cached values as they are; |scale * q| is to
+ * stay below 2^100.  Reruns are
  * bit-identical; a request's bits may depend on the other requests' lengths
  * (they set where its tokens are split).  1 <= B <= 4096, q_heads a multiple
  * of kv_heads, at most 1024, B * q_heads * max_q < 2^24, 0 <= T < 2^24,
