@@ -56,8 +56,8 @@ constexpr float SLACK = 8.f, LIFT = 6.f;       // weights reach 2^(SLACK + LIFT)
 struct Attn {
     const int32_t *ctx_len, *seq_start, *table;
     const float *q;
-    float *out, *part;         // part: [item][kv head][row][dim], then [item][kv head][row] (m, l)
-    int4 *info;                // [request] first whole piece, rest (-1: none), pieces
+    float *out, *part;         // part: [item][kv head][row] of dim outputs, m, l, 2 unused
+    int4 *info;                // [request] items of its first whole piece and of its last one, pieces
     int32_t *err;
     int64_t stride, ldq, ldo;
     int B, T, max_q, group, window;
@@ -65,6 +65,8 @@ struct Attn {
     int items;                 // most pieces that all requests are cut into, >= B
     int min_tiles;             // no piece smaller than this
     int row_tiles;             // 16-row tiles per work-group: 1, 2 or 4
+    u32 group_magic, gp_magic; // ceil(2^32 / d) for d = group and page_tokens / 16: x / d is the upper half of x * magic
+                               // while x * d < 2^32 (x < rows_cap) or, with d <= 16, x < 2^28 (a 16-token group)
     float scale;               // in units of log2
 };
 
@@ -73,6 +75,8 @@ struct Attn {
 __device__ __forceinline__ int attn_room(const Cache &c, const Attn &a) {
     return (int)min(a.stride * (int64_t)c.page_tokens, (int64_t)INT32_MAX - 63);
 }
+
+__device__ __forceinline__ int div_magic(int x, u32 magic) { return magic ? (int)__umulhi((u32)x, magic) : x; }
 
 // One request's share of the step: its rows, and the tiles [lo, lo + tiles) its
 // rows see anything of.
@@ -119,11 +123,12 @@ __device__ __forceinline__ float wave_sum(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(x), 63));
 }
 
-// How the requests are cut: `chunk` tiles a piece, and a rest, so that there
-// are at most a.items pieces (sum of floor(tiles / chunk) <= total / chunk <=
-// items - B, and a rest each).  The sum of up to 4096 counts is taken in fp32 and
-// raised by 2^-16, more than its rounding.  All whole pieces come before all
-// rests: the work-groups that start last are the short ones.
+// How the requests are cut: whole pieces of `chunk` tiles, and a last one of
+// more than chunk / 8 and up to 9 / 8 chunk (a request's only one may be
+// shorter), so that there are at most a.items pieces (sum of whole ones <= total
+// / chunk <= items - B, and a last one each).  The sum of up to 4096 counts is
+// taken in fp32 and raised by 2^-16, more than its rounding.  All whole pieces
+// come before all last ones: the work-groups that start last are the short ones.
 // (r0: the lane's request of the first 64.)
 __device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, const Req1 &r0, int lane) {
     if (a.items <= a.B) return INT32_MAX;
@@ -135,49 +140,48 @@ __device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, const R
 
 // Piece `item` (b -1 when there are fewer).  All results are uniform.
 struct Piece {
-    int b, index, of;          // request, which of its pieces (the rest is the last)
-    int whole, rest;           // its first whole piece's item, its rest's (-1: none)
+    int b, index, of;          // request, which of its pieces
+    int whole, last;           // the items of its first whole piece and of its last one
     Req1 r;
 };
+__device__ __forceinline__ int whole_pieces(const Req1 &r, int chunk) {
+    return r.tiles > chunk / 8 ? (int)((u32)(r.tiles - chunk / 8) / (u32)chunk) : 0;
+}
 __device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, const Req1 &r0, int chunk, int item,
                                             int lane) {
-    int found = -1, index = 0, of = 0, w0 = 0, rest0 = 0, first = 0, rn = 0, ctx = 0, tiles = 0, lo = 0;
+    if (a.items <= a.B) {                            // one piece a request
+        const Req1 r = attn_req(c, a, item);
+        return Piece{r.n ? item : -1, 0, 1, 0, item, r};
+    }
+    int found = -1, index = 0, of = 0, w0 = 0, last0 = 0, first = 0, rn = 0, ctx = 0, tiles = 0, lo = 0;
     int wholes = 0;
-    auto cut = [&](const Req1 &r, int *w, int *rest) {
-        *w = r.n ? (int)((u32)r.tiles / (u32)chunk) : 0;
-        *rest = r.n && (r.tiles == 0 || r.tiles > *w * chunk) ? 1 : 0;
-    };
     if (a.B > 64)
-        for (int b0 = 0; b0 < a.B; b0 += 64) {
-            int w, rest;
-            cut(attn_req(c, a, b0 + lane), &w, &rest);
-            wholes += __builtin_amdgcn_readlane(wave_scan(w), 63);
-        }
-    int wbefore = 0, rbefore = 0;
+        for (int b0 = 0; b0 < a.B; b0 += 64)
+            wholes += __builtin_amdgcn_readlane(wave_scan(whole_pieces(attn_req(c, a, b0 + lane), chunk)), 63);
+    int wbefore = 0, lbefore = 0;
     for (int b0 = 0; b0 < a.B && found < 0; b0 += 64) {
         const Req1 r = b0 ? attn_req(c, a, b0 + lane) : r0;
-        int w, rest;
-        cut(r, &w, &rest);
-        const int ws = wave_scan(w), rs = wave_scan(rest);
+        const int w = whole_pieces(r, chunk), any = r.n ? 1 : 0;
+        const int ws = wave_scan(w), ls = wave_scan(any);
         if (a.B <= 64) wholes = __builtin_amdgcn_readlane(ws, 63);
-        const int wf = wbefore + ws - w, rf = wholes + rbefore + rs - rest;
-        const bool in_w = item >= wf && item < wf + w, in_r = rest && item == rf;
-        const uint64_t hit = __ballot(in_w || in_r);
+        const int wf = wbefore + ws - w, lf = wholes + lbefore + ls - any;
+        const bool in_w = item >= wf && item < wf + w, in_l = any && item == lf;
+        const uint64_t hit = __ballot(in_w || in_l);
         const int l = hit ? __builtin_ctzll(hit) : 0;
         if (hit) found = b0 + l;
-        index = __builtin_amdgcn_readlane(in_r ? w : item - wf, l);
-        of = __builtin_amdgcn_readlane(w + rest, l);
+        index = __builtin_amdgcn_readlane(in_l ? w : item - wf, l);
+        of = __builtin_amdgcn_readlane(w + 1, l);
         w0 = __builtin_amdgcn_readlane(wf, l);
-        rest0 = __builtin_amdgcn_readlane(rest ? rf : -1, l);
+        last0 = __builtin_amdgcn_readlane(lf, l);
         first = __builtin_amdgcn_readlane(r.first, l);
         rn = __builtin_amdgcn_readlane(r.n, l);
         ctx = __builtin_amdgcn_readlane(r.ctx, l);
         tiles = __builtin_amdgcn_readlane(r.tiles, l);
         lo = __builtin_amdgcn_readlane(r.lo, l);
         wbefore += __builtin_amdgcn_readlane(ws, 63);
-        rbefore += __builtin_amdgcn_readlane(rs, 63);
+        lbefore += __builtin_amdgcn_readlane(ls, 63);
     }
-    return Piece{found, index, of, w0, rest0, Req1{first, rn, ctx, tiles, lo}};
+    return Piece{found, index, of, w0, last0, Req1{first, rn, ctx, tiles, lo}};
 }
 
 typedef u32 u2 __attribute__((ext_vector_type(2)));
@@ -272,10 +276,15 @@ __device__ __forceinline__ void swap_odd_rows(u32 &x, u32 &y) {
     y = r[1];
 }
 
+// NT: the cache lines are not to be kept (whole lines are asked for, once).
+template <bool NT> __device__ __forceinline__ u4 load16(const uint8_t *p) {
+    return NT ? __builtin_nontemporal_load((const u4 *)p) : *(const u4 *)p;
+}
+
 // Row of K that lane m's operand stands for in subtile t, within its group:
 // 8 (m / 4 % 2) + 4 t + m % 4 (keys 8 (m / 4) + 4 t + m % 4 of the tile).
 // k0, k1: the head's rows of the tile's two groups.
-template <bool Q8, int NB>
+template <bool Q8, int NB, bool NT>
 __device__ __forceinline__ void load_k(Tile<Q8, NB> &to, const uint8_t *k0, const uint8_t *k1, int lane) {
     constexpr int E = Q8 ? 1 : 2, RB = 32 * NB * E, UNITS = RB / 128, W = Tile<Q8, NB>::W;
     const int m = lane & 15, g = lane >> 4, row = 8 * ((m >> 2) & 1) + (m & 3);
@@ -284,7 +293,7 @@ __device__ __forceinline__ void load_k(Tile<Q8, NB> &to, const uint8_t *k0, cons
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-            const u4 a = *(const u4 *)(k0 + at + (4 * t * RB + 128 * u)), b = *(const u4 *)(k1 + at + (4 * t * RB + 128 * u));
+            const u4 a = load16<NT>(k0 + at + (4 * t * RB + 128 * u)), b = load16<NT>(k1 + at + (4 * t * RB + 128 * u));
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 to.k[t][8 * u + i] = a[i];
@@ -333,13 +342,13 @@ template <bool Q8, int NB> __device__ __forceinline__ void order_k(Tile<Q8, NB> 
 // lane (m, g): dims 16 n + m, keys 8 g .. 8 g + 7.  int8: one load brings the 16
 // tokens of dim 16 n + m for n even in lanes g % 2 == 0 and odd in the others,
 // which then change halves.
-template <bool Q8, int NB>
+template <bool Q8, int NB, bool NT>
 __device__ __forceinline__ void load_v(Tile<Q8, NB> &to, const uint8_t *mine, int lane) {
     const int m = lane & 15, g = lane >> 4;
     const uint8_t *p = Q8 ? mine + (16 * (g & 1) + m) * 16 : mine + (m * 16 + (g & 1) * 8) * 2;
 #pragma unroll
     for (int n = 0; n < (Q8 ? NB : 2 * NB); ++n) {
-        const u4 a = *(const u4 *)(p + n * 512);
+        const u4 a = load16<NT>(p + n * 512);
 #pragma unroll
         for (int i = 0; i < 4; ++i) to.v[4 * n + i] = a[i];
     }
@@ -366,7 +375,7 @@ __device__ __forceinline__ float across_groups_sum(float x) {
 // 16 * row_tiles of its rows.  Wave w takes row tile w % row_tiles and the tiles
 // w / row_tiles + i * (4 / row_tiles) of the piece (waves that share a key tile
 // read it through the caches); the waves of a row tile join through LDS.
-template <bool Q8, int NB>
+template <bool Q8, int NB, bool NT>
 __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn a) {
     constexpr int D = 32 * NB, LD = D + 4;
     // While the tiles go by, a wave's part holds its q limbs (operands as lanes read them), the blocks' sums of
@@ -378,24 +387,28 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     float *lds = (float *)lds_;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int groups = (a.rows_cap + 16 * a.row_tiles - 1) / (16 * a.row_tiles);
-    // pieces that read the same keys (row groups) lie 8 blocks apart: one L2
-    const int per = 8 * groups, oct = blockIdx.x / per, in = blockIdx.x - oct * per;
-    const int unit = oct * 8 + (in & 7), rgroup = in >> 3;
-    if (unit >= a.items * c.kv_heads) return;
-    const int item = unit / c.kv_heads, head = unit - item * c.kv_heads;
-    const Req1 r0 = attn_req(c, a, lane);
+    // row groups of a piece (they read the same keys) lie 8 blocks apart: one L2
+    const int head = blockIdx.y;
+    int item = blockIdx.x, rgroup = 0;
+    if (groups > 1) {
+        const int per = 8 * groups, oct = item / per, in = item - oct * per;
+        item = oct * 8 + (in & 7);
+        rgroup = in >> 3;
+        if (item >= a.items) return;
+    }
+    const Req1 r0 = a.items <= a.B ? Req1{0, 0, 0, 0, 0} : attn_req(c, a, lane);
     const int chunk = attn_chunk(c, a, r0, lane);
     const Piece pc = attn_piece(c, a, r0, chunk, item, lane);
     if (pc.b < 0) return;
     if (a.items > a.B && pc.index == 0 && head == 0 && rgroup == 0 && threadIdx.x == 0)
-        a.info[pc.b] = int4{pc.whole, pc.rest, pc.of, 0};
+        a.info[pc.b] = int4{pc.whole, pc.last, pc.of, 0};
     const int rows = min(pc.r.n, a.max_q) * a.group;
     const int row0 = rgroup * 16 * a.row_tiles;
     if (row0 >= rows) return;
 
     const int rt = wave % a.row_tiles, kw = wave / a.row_tiles, kws = ATTN_WAVES / a.row_tiles;
     const int m = lane & 15, g = lane >> 4;
-    const int r = row0 + 16 * rt + m, j = r / a.group, qh = head * a.group + (r - j * a.group);
+    const int r = row0 + 16 * rt + m, j = div_magic(r, a.group_magic), qh = head * a.group + (r - j * a.group);
     const int64_t trow = (int64_t)pc.r.first + j;
     const bool live = r < rows && trow >= 0 && trow < a.T;
     // the row sees keys [lo, hi); hi_all and lo_all: keys that any row sees,
@@ -417,13 +430,12 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     // the row's q (its loads go out first, the limbs are made while the first tile's are on their way)
     f4 x[2 * NB];
     {
-        const float *qp = a.q + (live ? trow : 0) * a.ldq + (int64_t)qh * D + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
+        const float *qp = a.q + (live ? trow * a.ldq + (int64_t)qh * D : 0) + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
 #pragma unroll
         for (int s = 0; s < NB; ++s)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                x[2 * s + e] = f4{0.f, 0.f, 0.f, 0.f};
-                if (live) x[2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
+                x[2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
             }
     }
 
@@ -446,13 +458,13 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     auto ask_ids = [&](int n) {
         bool in;
         const int grp = group_of(n, &in);
-        if (in) raw = (u32)a.table[pc.b * a.stride + (u32)grp / gp];
+        if (in) raw = (u32)a.table[pc.b * a.stride + div_magic(grp, a.gp_magic)];
     };
     auto take_ids = [&](int n) {
         bool in;
         const int grp = group_of(n, &in);
         const bool wrong = in && raw >= c.n_pages;
-        ids = in && !wrong ? raw << 4 | ((u32)grp % gp) : 0;
+        ids = in && !wrong ? raw << 4 | ((u32)grp - (u32)div_magic(grp, a.gp_magic) * gp) : 0;
         bad = __ballot(wrong);
         if (wrong && a.err) a.err[0] = 1;
     };
@@ -477,27 +489,28 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     const uint8_t *sb = (sl / (4 * NB) ? vb : kb) + (sl % (2 * NB)) * 16;
     const bool second = (sl / (2 * NB)) & 1;
     auto get_k = [&](Tile<Q8, NB> &to, const Where &w) {
-        load_k<Q8, NB>(to, kb + w.x0, kb + w.x0 + w.dx, lane);
+        load_k<Q8, NB, NT>(to, kb + w.x0, kb + w.x0 + w.dx, lane);
         if constexpr (Q8) to.s = *(const h8 *)(sb + w.s0 + (second ? w.ds : 0));
     };
-    auto get_v = [&](Tile<Q8, NB> &to, const Where &w) { load_v<Q8, NB>(to, vb + w.x0 + ((g & 2) ? w.dx : 0), lane); };
+    auto get_v = [&](Tile<Q8, NB> &to, const Where &w) { load_v<Q8, NB, NT>(to, vb + w.x0 + ((g & 2) ? w.dx : 0), lane); };
     auto wrong_of = [&](int n) { return (u32)(bad >> (2 * (n & 31))) & 3; };
 
     constexpr int DEPTH = DEPTH_;
     Tile<Q8, NB> tiles[DEPTH];
-    if (N > 0) {
-        ask_ids(0);
-        take_ids(0);
+    // The first tiles' loads, also for a wave without tiles (page 0 then): under a condition, every wait for q behind them
+    // would wait for them too.
+    ask_ids(0);
+    take_ids(0);
 #pragma unroll
-        for (int u = 0; u < DEPTH; ++u) {
-            const int n = min(u, N - 1);
-            const Where w = where(n);
-            get_k(tiles[u], w);
-            get_v(tiles[u], w);
-            tiles[u].wrong = wrong_of(n);
-        }
-        ask_ids(32);
+    for (int u = 0; u < DEPTH; ++u) {
+        const int n = max(min(u, N - 1), 0);
+        const Where w = where(n);
+        get_k(tiles[u], w);
+        get_v(tiles[u], w);
+        tiles[u].wrong = wrong_of(n);
     }
+    ask_ids(32);
+
     // q as two fp16 limbs, in LDS: read again for every tile, they leave their registers to tiles on the way
     uint8_t *part = lds_ + wave * PART;
     float unscale;
@@ -505,7 +518,7 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < 2 * NB; ++s) {
-            x[s] *= a.scale;
+            x[s] *= live ? a.scale : 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[s][i]));
         }
@@ -679,77 +692,92 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     const int todo = min(16 * a.row_tiles, rows - row0) * (D / 4);
     for (int i = threadIdx.x; i < todo; i += ATTN_THREADS) {
         const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
-        float M = NONE, L = 0.f;
-        f4 x = {0.f, 0.f, 0.f, 0.f};
-        for (int w = 0; w < kws; ++w) M = fmaxf(M, stat[((w * a.row_tiles + (rr >> 4)) * 16 + (rr & 15)) * 2]);
-        for (int w = 0; w < kws; ++w) {
-            const int at = (w * a.row_tiles + (rr >> 4)) * 16 + (rr & 15);
-            const float f = __builtin_amdgcn_exp2f(stat[at * 2] - M);
-            L = fmaf(f, stat[at * 2 + 1], L);
-            x += f * *(const f4 *)(lds + at * LD + d);
+        float M = NONE, L = 0.f, mw[ATTN_WAVES], lw[ATTN_WAVES];
+        f4 x = {0.f, 0.f, 0.f, 0.f}, y[ATTN_WAVES];
+#pragma unroll
+        for (int w = 0; w < ATTN_WAVES; ++w) {           // (behind the last wave of the keys, the first one's with no weight)
+            const int at = ((w < kws ? w * a.row_tiles : 0) + (rr >> 4)) * 16 + (rr & 15);
+            mw[w] = w < kws ? stat[at * 2] : NONE;
+            lw[w] = stat[at * 2 + 1];
+            y[w] = *(const f4 *)(lds + at * LD + d);
+            M = fmaxf(M, mw[w]);
+        }
+#pragma unroll
+        for (int w = 0; w < ATTN_WAVES; ++w) {
+            const float f = w < kws ? __builtin_amdgcn_exp2f(mw[w] - M) : 0.f;
+            L = fmaf(f, lw[w], L);
+            x += w < kws ? f * y[w] : f4{0.f, 0.f, 0.f, 0.f};
         }
         const int row = row0 + rr;
         if (pc.of == 1) {
-            const int jj = row / a.group;
+            const int jj = div_magic(row, a.group_magic);
             const int64_t to = (int64_t)pc.r.first + jj;
             if (to >= 0 && to < a.T)
                 *(f4 *)(a.out + to * a.ldo + (int64_t)(head * a.group + row - jj * a.group) * D + d) =
                     L == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : x * (1.f / L);
         } else {
             const int64_t at = ((int64_t)item * c.kv_heads + head) * a.rows_cap + row;
-            *(f4 *)(a.part + at * D + d) = x;
-            if (d == 0) {
-                float *ml = a.part + (int64_t)a.items * c.kv_heads * a.rows_cap * D + at * 2;
-                ml[0] = M;
-                ml[1] = L;
-            }
+            *(f4 *)(a.part + at * LD + d) = x;
+            if (d == 0) *(f4 *)(a.part + at * LD + D) = f4{M, L, 0.f, 0.f};
         }
     }
 }
 
 // Joins the pieces of the requests that were cut: one work-group per row,
-// thread (i, d) the pieces i, i + ways, ... of 4 elements.
-template <int NB>
-__global__ __launch_bounds__(ATTN_THREADS) void attn_join_kernel(Cache c, Attn a) {
-    constexpr int D = 32 * NB, LANES = D / 4, WAYS = ATTN_THREADS / LANES;
-    __shared__ f4 xs[ATTN_THREADS];
-    __shared__ float ls[WAYS];
-    const int lane = threadIdx.x & 63;
-    const int b = blockIdx.x / (c.kv_heads * a.rows_cap), left = blockIdx.x - b * (c.kv_heads * a.rows_cap);
-    const int head = left / a.rows_cap, row = left - head * a.rows_cap;
+// thread (w, d) pieces w, w + WAYS, ... of 4 elements, each with its own running
+// m, then the ways through LDS.  A chain of dependent loads is what it takes its
+// time for: the request's pieces, then everything else at once.
+template <int NB, int THREADS>
+__global__ __launch_bounds__(THREADS) void attn_join_kernel(Cache c, Attn a) {
+    constexpr int D = 32 * NB, LD = D + 4, LANES = D / 4, WAYS = THREADS / LANES, DEEP = 4;
+    __shared__ f4 xs[THREADS];
+    __shared__ float ms[WAYS], ls[WAYS];
+    const int row = blockIdx.x, head = blockIdx.y, b = blockIdx.z;
     const int first = a.seq_start[b], n = a.seq_start[b + 1] - first;
     const int4 info = a.info[b];                      // (a request without rows has none: left by another call)
     if (n <= 0 || row >= min(n, a.max_q) * a.group || info.z <= 1) return;
-    const int pieces = info.z, whole = info.x, rest = info.y;
-    const float *ml = a.part + (int64_t)a.items * c.kv_heads * a.rows_cap * D;
-    auto at = [&](int i) {
-        const int item = i == pieces - 1 && rest >= 0 ? rest : whole + i;
-        return ((int64_t)item * c.kv_heads + head) * a.rows_cap + row;
-    };
-    float M = NONE;
-    for (int i = lane; i < pieces; i += 64) M = fmaxf(M, ml[at(i) * 2]);
-#pragma unroll
-    for (int s = 32; s; s >>= 1) M = fmaxf(M, __shfl_xor(M, s));
+    const int pieces = info.z, whole = info.x, last = info.y;
     const int way = threadIdx.x / LANES, d = (threadIdx.x - way * LANES) * 4;
     f4 x = {0.f, 0.f, 0.f, 0.f};
-    float L = 0.f;
+    float M = NONE, L = 0.f;
     if (way < WAYS) {
-        for (int i = way; i < pieces; i += WAYS) {
-            const int64_t k = at(i);
-            const float f = __builtin_amdgcn_exp2f(ml[k * 2] - M);
-            L = fmaf(f, ml[k * 2 + 1], L);
-            x += f * *(const f4 *)(a.part + k * D + d);
+        for (int i0 = way; i0 < pieces; i0 += DEEP * WAYS) {
+            f4 y[DEEP], ml[DEEP];
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+                const int i = min(i0 + k * WAYS, pieces - 1);
+                const int item = i == pieces - 1 ? last : whole + i;
+                const float *p = a.part + (((int64_t)item * c.kv_heads + head) * a.rows_cap + row) * LD;
+                y[k] = *(const f4 *)(p + d);
+                ml[k] = *(const f4 *)(p + D);
+            }
+#pragma unroll
+            for (int k = 0; k < DEEP; ++k) {
+                if (i0 + k * WAYS >= pieces) break;
+                const float now = fmaxf(M, ml[k][0]);
+                const float f = __builtin_amdgcn_exp2f(M - now), h = __builtin_amdgcn_exp2f(ml[k][0] - now);
+                M = now;
+                L = L * f + ml[k][1] * h;
+                x = x * f + y[k] * h;
+            }
         }
-        if (d == 0) ls[way] = L;
+        if (d == 0) {
+            ms[way] = M;
+            ls[way] = L;
+        }
     }
     xs[threadIdx.x] = x;
     __syncthreads();
     if (way == 0) {
+#pragma unroll 4
         for (int w = 1; w < WAYS; ++w) {
-            x += xs[w * LANES + threadIdx.x];
-            L += ls[w];
+            const float now = fmaxf(M, ms[w]);
+            const float f = __builtin_amdgcn_exp2f(M - now), h = __builtin_amdgcn_exp2f(ms[w] - now);
+            M = now;
+            L = L * f + ls[w] * h;
+            x = x * f + xs[w * LANES + threadIdx.x] * h;
         }
-        const int j = row / a.group;
+        const int j = div_magic(row, a.group_magic);
         const int64_t to = (int64_t)first + j;
         if (to >= 0 && to < a.T)
             *(f4 *)(a.out + to * a.ldo + (int64_t)(head * a.group + row - j * a.group) * D + d) =
@@ -757,7 +785,7 @@ __global__ __launch_bounds__(ATTN_THREADS) void attn_join_kernel(Cache c, Attn a
     }
 }
 
-template <int NB> int launch_attn(bool q8, const Cache &c, const Attn &a, hipStream_t st);
+template <int NB> int launch_attn(bool q8, bool nt, const Cache &c, const Attn &a, hipStream_t st);
 
 } // namespace kv
 } // namespace kq

@@ -10,32 +10,41 @@ using namespace kq::kv;
 
 // Work-groups that the requests' tokens are cut into (beside one per request
 // and kv head), and the fewest tiles of such a piece.
-#ifndef PIECES_
-#define PIECES_ 1024
-#endif
-#ifndef MINT_
-#define MINT_ 8
-#endif
-constexpr int PIECES = PIECES_, MIN_TILES = MINT_;
+// Contexts past this may not be kept by the last-level cache: where no two work-groups or waves share a line (up to 16
+// rows a kv head), lines are then read with the non-temporal hint (one request of 131072 fp16 tokens 110 -> 102 us, 64
+// requests of up to 32768 Q8_0 tokens 354 -> 321; one of 512, kept, 12.5 -> 14.2).
+constexpr double KEPT_BYTES = 256e6;
 
-// The split of a call: 16-row tiles per work-group (1, 2 or 4: the four waves
-// of a work-group share the rows first, then the keys) and the number of
-// pieces.  Contexts of up to MIN_TILES tiles are not cut: one launch.
-static void attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, Attn *a) {
+// The split of a call.
+//  * row_tiles: 16-row tiles per work-group, 1, 2 or 4: its four waves share the rows first, then the keys.
+//  * A piece has at least min_tiles tiles.  A work-group costs about 6 us beside its tiles (a chain of dependent loads,
+//    the join of its waves) and a cut one its share of a second launch, so where requests and heads alone make a
+//    work-group per compute unit, only long contexts are cut (32 requests of 1024 tokens: not cut 28 us, cut in two 37),
+//    and where they do not, contexts past 8 tiles are cut finely (one request of 1024 tokens: not cut 15.4 us, pieces
+//    of 8 tiles 11.5, of 4 10.2).
+//  * As many pieces as work-groups run at once (3 on each of 256 compute units; more of them cost one long request 5 to
+//    25 %), and up to four times that for large batches, 64 tiles a piece, where they even out the requests' lengths (64
+//    requests of up to 32768: 760 pieces 354 us, 3040 315).
+static void attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, int window, Attn *a) {
     a->group = q_heads / c->kv_heads;
     a->rows_cap = a->group * max_q;
     a->row_tiles = a->rows_cap <= 16 ? 1 : a->rows_cap <= 32 ? 2 : 4;
-    a->min_tiles = MIN_TILES;
+    auto magic = [](int d) { return d == 1 ? 0u : (u32)(((1ull << 32) + d - 1) / d); };
+    a->group_magic = magic(a->group);
+    a->gp_magic = magic(c->page_tokens / 16);
     const int groups = (a->rows_cap + 16 * a->row_tiles - 1) / (16 * a->row_tiles);
-    const int64_t tiles = (max_ctx + TILE - 1) / TILE;
-    const int64_t most = (int64_t)B * ((tiles + MIN_TILES - 1) / MIN_TILES);
-    a->items = (int)std::min<int64_t>(most, B + std::max(1, PIECES / (c->kv_heads * groups)));
+    if (window) max_ctx = std::min<int64_t>(max_ctx, (int64_t)window + max_q + 2 * TILE);
+    const int64_t tiles = (max_ctx + TILE - 1) / TILE, base = (int64_t)B * c->kv_heads * groups;
+    a->min_tiles = base < 32 ? 4 : base < 256 ? 8 : 32;
+    const int64_t pieces = std::max<int64_t>(760, std::min<int64_t>(base * tiles / 64, 3040));
+    const int64_t most = tiles <= std::max(8, a->min_tiles * 9 / 8) ? B : B * ((tiles + a->min_tiles - 1) / a->min_tiles);
+    a->items = (int)std::min<int64_t>(most, B + std::max<int64_t>(1, pieces / (c->kv_heads * groups)));
 }
 
 // The pieces' unnormalised outputs with their m and l, then the requests'
-// pieces (a.info), at a multiple of 16 bytes.
+// pieces (a.info).
 static size_t part_bytes(const kqkv_cache *c, const Attn &a, int q_heads, int max_q) {
-    return ((size_t)a.items * q_heads * max_q * (c->head_dim + 2) * sizeof(float) + 15) & ~(size_t)15;
+    return (size_t)a.items * q_heads * max_q * (c->head_dim + 4) * sizeof(float);
 }
 
 static int attn_shape(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, int q_heads) {
@@ -53,7 +62,7 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
     if (!cache || cache_limits(cache->type, cache->kv_heads, cache->head_dim, cache->page_tokens)) return 0;
     if (attn_shape(cache, B, max_q, max_ctx, q_heads)) return 0;
     Attn a;
-    attn_split(cache, B, max_q, max_ctx, q_heads, &a);
+    attn_split(cache, B, max_q, max_ctx, q_heads, 0, &a);
     return a.items <= B ? 0 : part_bytes(cache, a, q_heads, max_q) + (size_t)B * sizeof(int4);
 }
 
@@ -76,7 +85,7 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     if (workspace_bytes < ws) return KQ_ERR_SHAPE;
     if (device_check()) return KQ_ERR_DEVICE;
     Attn a;
-    attn_split(cache, B, max_q, max_ctx, q_heads, &a);
+    attn_split(cache, B, max_q, max_ctx, q_heads, window, &a);
     a.ctx_len = ctx_len;
     a.seq_start = seq_start;
     a.table = table;
@@ -95,16 +104,17 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     a.scale = (float)(scale * 1.4426950408889634);
     const bool q8 = cache->type == KQKV_Q8_0;
     const Cache c = cache_args(cache);
+    const bool nt = a.row_tiles == 1 && (double)B * max_ctx * 2 * c.page_bytes / c.page_tokens > KEPT_BYTES;
     hipStream_t st = (hipStream_t)stream;
     switch (cache->head_dim / 32) {
-    case 1: return launch_attn<1>(q8, c, a, st);
-    case 2: return launch_attn<2>(q8, c, a, st);
-    case 3: return launch_attn<3>(q8, c, a, st);
-    case 4: return launch_attn<4>(q8, c, a, st);
-    case 5: return launch_attn<5>(q8, c, a, st);
-    case 6: return launch_attn<6>(q8, c, a, st);
-    case 7: return launch_attn<7>(q8, c, a, st);
-    default: return launch_attn<8>(q8, c, a, st);
+    case 1: return launch_attn<1>(q8, nt, c, a, st);
+    case 2: return launch_attn<2>(q8, nt, c, a, st);
+    case 3: return launch_attn<3>(q8, nt, c, a, st);
+    case 4: return launch_attn<4>(q8, nt, c, a, st);
+    case 5: return launch_attn<5>(q8, nt, c, a, st);
+    case 6: return launch_attn<6>(q8, nt, c, a, st);
+    case 7: return launch_attn<7>(q8, nt, c, a, st);
+    default: return launch_attn<8>(q8, nt, c, a, st);
     }
 }
 
