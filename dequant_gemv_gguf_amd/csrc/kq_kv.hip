@@ -218,8 +218,19 @@ __global__ __launch_bounds__(SLOT_THREADS) void plan_rows_kernel(Plan p) {
 
 // ---------------------------------------------------------------------------
 // Rotary positions and store
+//
+// Bound: HBM (q is read and written, k and v read, once).  A lane takes 8
+// elements of a head's row, 4 pairs or 8 that do not turn, as two 16-byte loads
+// and stores, so dim / 8 lanes make a row and a wave takes 64 / (dim / 8) rows at
+// a time; a work-group is one token and its waves go through the token's q and k
+// rows, so that the token's angles (64-bit exponentials, sines and cosines) are
+// computed once, while the first rows are on their way.  For few tokens the rows
+// are spread over more work-groups.  v goes into the transposed groups of 16
+// tokens: a wave takes 16 tokens by 32 elements, lane (t, i) elements 4 i .. of
+// token t: 128 bytes of a row a token, and stores in which 16 lanes write
+// neighbours where the tokens have neighbouring slots (no staging in LDS).
 
-constexpr int STORE_THREADS = 256;
+constexpr int STORE_THREADS = 256, STORE_WAVES = STORE_THREADS / 64;
 constexpr int MAX_DIM = 256, MAX_PAIRS = MAX_DIM / 2;
 
 struct Rope {
@@ -234,26 +245,26 @@ struct Rope {
 struct Rows {
     const float *q, *k, *v;
     float *q_out;
+    const int32_t *slots;
     int64_t ldq, ldq_out, ldk, ldv;
     int q_heads, T;
+    int split;             // work-groups a token's q and k rows are spread over
+    int v_wgs;             // work-groups of v, the first ones of the grid
+    u32 lanes_magic;       // ceil(2^16 / (dim / 8)): lane / (dim / 8) = lane * magic >> 16
 };
 
 // Cosine and sine of pair i of token t.  The angle is taken in turns,
 // t / 2 pi, so that its whole part drops out exactly.
 __device__ __forceinline__ double2 rope_turn(const Rope &r, int t, int i) {
     const int axis = (i >= r.end[0]) + (i >= r.end[1]) + (i >= r.end[2]);
+    const double at = (double)r.pos[axis * r.pos_stride + t];
     double f = exp2(-2.0 * i / (2.0 * r.pairs) * r.log2_base);
     if (r.factors) f /= (double)r.factors[i];
-    double turns = (double)r.pos[axis * r.pos_stride + t] * f * 0.15915494309189533577;
+    double turns = at * f * 0.15915494309189533577;
     turns -= rint(turns);
     double2 cs;
     sincospi(2.0 * turns, &cs.y, &cs.x);
     return cs;
-}
-
-__device__ __forceinline__ void rope_pair(const Rope &r, int i, int *a, int *b) {
-    *a = r.style == KQKV_ROPE_HALVES ? i : 2 * i;
-    *b = r.style == KQKV_ROPE_HALVES ? i + r.pairs : 2 * i + 1;
 }
 
 // Orders a wave's LDS writes before its other lanes' reads.
@@ -262,92 +273,279 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// One head's row of one token (in LDS, the wave's own) into the cache.
-template <bool Q8, bool V>
-__device__ __forceinline__ void store_row(const Cache &c, const float *row, u32 slot, int head, int lane) {
-    const u32 page = slot / c.page_tokens, t = slot - page * c.page_tokens;
-    uint8_t *to = (V ? c.v : c.k) + page * c.page_bytes + (u64)head * c.head_bytes;
+// The scale and the quants' divisor of a block whose largest magnitude has the
+// bits m (magnitudes order like integers, NaN on top).
+struct Scale {
+    float s;               // fp16, as stored
+    bool none;             // every quant is 0
+};
+__device__ __forceinline__ Scale block_scale(u32 m) {
+    const bool bad = m >= 0x7F800000u;
+    const float s = (float)(_Float16)fminf(__builtin_bit_cast(float, m) / 127.f, 65504.f);
+    return Scale{bad ? __builtin_nanf("") : s, bad || s == 0.f};
+}
+__device__ __forceinline__ int quant(float x, const Scale &s) {
+    return s.none ? 0 : (int)fmaxf(-127.f, fminf(127.f, rintf(x / s.s)));
+}
+__device__ __forceinline__ u32 magnitude(float x) { return __builtin_bit_cast(u32, x) & 0x7FFFFFFFu; }
+__device__ __forceinline__ u32 magnitude(f4 x) {
+    return max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
+}
+
+// 4 elements at d of one head's row of one token into K.
+template <bool Q8>
+__device__ __forceinline__ void store_k4(const Cache &c, uint8_t *head, u32 t, int d, f4 x, u32 block_max) {
     if (!Q8) {
-        for (int d = lane; d < c.dim; d += 64)
-            ((_Float16 *)to)[V ? v_at(t, d, c.dim) : k_at(t, d, c.dim)] = (_Float16)row[d];
+        *(h4 *)(head + 2 * k_at(t, d, c.dim)) = __builtin_convertvector(x, h4);
         return;
     }
-    _Float16 *scales = (_Float16 *)(to + c.page_tokens * c.dim);
-    for (int d0 = 0; d0 < c.dim; d0 += 64) {           // a block of 32 in each half of the wave
-        const int d = d0 + lane;
-        const float x = d < c.dim ? row[d] : 0.f;
-        u32 m = __builtin_bit_cast(u32, x) & 0x7FFFFFFFu;   // magnitudes order like integers, NaN on top
+    const Scale s = block_scale(block_max);
+    u32 w = 0;
 #pragma unroll
-        for (int s = 16; s; s >>= 1) m = max(m, (u32)__shfl_xor((int)m, s));
-        const bool bad = m >= 0x7F800000u;
-        float s = (float)(_Float16)fminf(__builtin_bit_cast(float, m) / 127.f, 65504.f);
-        const float n = s > 0.f && !bad ? rintf(x / s) : 0.f;
-        if (bad) s = __builtin_nanf("");
-        if (d < c.dim) {
-            to[V ? v_at(t, d, c.dim) : k_at(t, d, c.dim)] = (uint8_t)(int8_t)fmaxf(-127.f, fminf(127.f, n));
-            if ((lane & 31) == 0) scales[scale_at(t, d >> 5, c.dim)] = (_Float16)s;
+    for (int i = 0; i < 4; ++i) w |= ((u32)quant(x[i], s) & 0xFFu) << (8 * i);
+    *(u32 *)(head + k_at(t, d, c.dim)) = w;
+    if ((d & 31) == 0) ((_Float16 *)(head + c.page_tokens * c.dim))[scale_at(t, d >> 5, c.dim)] = (_Float16)s.s;
+}
+
+// 16 tokens by 32 elements of v, for the unit-th (tokens, head, elements).
+template <bool Q8> __device__ __forceinline__ void store_v(const Cache &c, const Rows &x, int64_t unit, int lane) {
+    const int blocks = c.dim >> 5, per = c.kv_heads * blocks;
+    const int tokens = (int)(unit / per), left = (int)(unit - (int64_t)tokens * per), head = left / blocks, b = left - head * blocks;
+    const int t = tokens * 16 + (lane & 15), i = lane >> 4;
+    const u32 slot = t < x.T ? (u32)x.slots[t] : ~0u;
+    const bool in = slot < c.slots;
+    const float *from = x.v + (in ? t : 0) * x.ldv + (int64_t)head * c.dim + b * 32 + 4 * i;
+    const f4 y[2] = {*(const f4 *)from, *(const f4 *)(from + 16)};
+    const u32 page = slot / c.page_tokens, at = slot - page * c.page_tokens;
+    uint8_t *to = c.v + (in ? page : 0) * c.page_bytes + (u64)head * c.head_bytes;
+    u32 m = max(magnitude(y[0]), magnitude(y[1]));
+    if (Q8) {
+        m = max(m, (u32)__shfl_xor((int)m, 16));
+        m = max(m, (u32)__shfl_xor((int)m, 32));
+    }
+    if (!in) return;
+    const Scale s = block_scale(m);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u32 j = v_at(at, b * 32 + 16 * k + 4 * i + e, c.dim);
+            if (Q8) to[j] = (uint8_t)quant(y[k][e], s);
+            else ((_Float16 *)to)[j] = (_Float16)y[k][e];
         }
+    if (Q8 && i == 0) ((_Float16 *)(to + c.page_tokens * c.dim))[scale_at(at, b, c.dim)] = (_Float16)s.s;
+}
+
+// Needs rot_dims a multiple of 8 (all 4 pairs of a lane turn, or none).
+template <bool Q8>
+__global__ __launch_bounds__(STORE_THREADS) void rope_store_kernel(Cache c, Rope r, Rows x) {
+    __shared__ double2 cs[MAX_PAIRS];
+    __shared__ u32 block_max[STORE_WAVES][16 * 8];       // [wave][row of the wave][block of 32]
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if ((int)blockIdx.x < x.v_wgs) {
+        const int64_t units = (int64_t)((x.T + 15) / 16) * c.kv_heads * (c.dim >> 5);
+        for (int64_t u = (int64_t)blockIdx.x * STORE_WAVES + wave; u < units; u += (int64_t)x.v_wgs * STORE_WAVES)
+            store_v<Q8>(c, x, u, lane);
+        return;
+    }
+    const int wg = blockIdx.x - x.v_wgs, t = wg / x.split, part = wg - t * x.split;
+    const int lanes = c.dim >> 3, sub = (int)(((u32)lane * x.lanes_magic) >> 16), j = lane - sub * lanes;
+    const int rows_a_wave = (int)((64 * x.lanes_magic) >> 16);
+    const int rows = x.q_heads + (x.k ? c.kv_heads : 0), step = rows_a_wave * STORE_WAVES * x.split;
+    const bool turns = j < (r.pairs >> 2);
+    const int oa = turns && r.style == KQKV_ROPE_HALVES ? 4 * j : 8 * j, ob = turns && r.style == KQKV_ROPE_HALVES ? r.pairs + 4 * j : 8 * j + 4;
+    const float *qrow = x.q + t * x.ldq, *krow = x.k + t * x.ldk;
+    auto row_at = [&](int h) { return h < x.q_heads ? qrow + (int64_t)h * c.dim : krow + (int64_t)(h - x.q_heads) * c.dim; };
+    int h = (part * STORE_WAVES + wave) * rows_a_wave + sub;
+    const bool lane_in = sub < rows_a_wave;
+    // the first rows are asked for before the angles are computed
+    f4 a = {0.f, 0.f, 0.f, 0.f}, b = a;
+    if (lane_in && h < rows) {
+        const float *p = row_at(h);
+        a = *(const f4 *)(p + oa);
+        b = *(const f4 *)(p + ob);
+    }
+    const u32 slot = x.k ? (u32)x.slots[t] : ~0u;
+    for (int i = threadIdx.x; i < r.pairs; i += STORE_THREADS) cs[i] = rope_turn(r, t, i);
+    __syncthreads();
+    double2 turn[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn[i] = turns ? cs[4 * j + i] : double2{1.0, 0.0};
+    const bool stored = slot < c.slots;
+    const u32 page = stored ? slot / c.page_tokens : 0, at = slot - page * c.page_tokens;
+    uint8_t *kpage = c.k + page * c.page_bytes;
+    u32 *maxes = block_max[wave] + sub * 8;
+    for (int h0 = h - sub; h0 < rows; h0 += step, h += step) {
+        // the next rows, while these are turned
+        f4 na = {0.f, 0.f, 0.f, 0.f}, nb = na;
+        if (lane_in && h + step < rows) {
+            const float *p = row_at(h + step);
+            na = *(const f4 *)(p + oa);
+            nb = *(const f4 *)(p + ob);
+        }
+        const bool mine = lane_in && h < rows, is_k = h >= x.q_heads;
+        f4 ya = a, yb = b;
+        if (turns) {
+            if (r.style == KQKV_ROPE_HALVES) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double va = a[i], vb = b[i];
+                    ya[i] = (float)(va * turn[i].x - vb * turn[i].y);
+                    yb[i] = (float)(va * turn[i].y + vb * turn[i].x);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const double va = i < 2 ? a[2 * i] : b[2 * i - 4], vb = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+                    const float u = (float)(va * turn[i].x - vb * turn[i].y), w = (float)(va * turn[i].y + vb * turn[i].x);
+                    if (i < 2) {
+                        ya[2 * i] = u;
+                        ya[2 * i + 1] = w;
+                    } else {
+                        yb[2 * i - 4] = u;
+                        yb[2 * i - 3] = w;
+                    }
+                }
+            }
+        }
+        if (mine && !is_k) {
+            float *p = x.q_out + t * x.ldq_out + (int64_t)h * c.dim;
+            *(f4 *)(p + oa) = ya;
+            *(f4 *)(p + ob) = yb;
+        }
+        if (h0 + rows_a_wave > x.q_heads && stored) {        // some of the wave's rows are k's
+            u32 ma = 0, mb = 0;
+            if (Q8) {
+                // the blocks' largest magnitudes: 4 elements lie in one block, a lane's two fours in any two
+                for (int i = lane; i < 16 * 8; i += 64) block_max[wave][i] = 0;
+                wave_sync();
+                if (mine) {
+                    atomicMax(&maxes[oa >> 5], magnitude(ya));
+                    atomicMax(&maxes[ob >> 5], magnitude(yb));
+                }
+                wave_sync();
+                if (mine) {
+                    ma = maxes[oa >> 5];
+                    mb = maxes[ob >> 5];
+                }
+                wave_sync();
+            }
+            if (mine && is_k) {
+                uint8_t *head = kpage + (u64)(h - x.q_heads) * c.head_bytes;
+                store_k4<Q8>(c, head, at, oa, ya, ma);
+                store_k4<Q8>(c, head, at, ob, yb, mb);
+            }
+        }
+        a = na;
+        b = nb;
     }
 }
 
+// Any even rot_dims: a pair a lane, q and k only (k through LDS).
 template <bool Q8>
-__global__ __launch_bounds__(STORE_THREADS) void rope_store_kernel(Cache c, Rope r, Rows x, const int32_t *slots) {
+__global__ __launch_bounds__(STORE_THREADS) void rope_store_any_kernel(Cache c, Rope r, Rows x) {
     __shared__ double2 cs[MAX_PAIRS];
-    __shared__ float rows[STORE_THREADS / 64][MAX_DIM];
-    const int t = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __shared__ __align__(16) float rows[STORE_WAVES][MAX_DIM];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if ((int)blockIdx.x < x.v_wgs) {
+        const int64_t units = (int64_t)((x.T + 15) / 16) * c.kv_heads * (c.dim >> 5);
+        for (int64_t u = (int64_t)blockIdx.x * STORE_WAVES + wave; u < units; u += (int64_t)x.v_wgs * STORE_WAVES)
+            store_v<Q8>(c, x, u, lane);
+        return;
+    }
+    const int t = blockIdx.x - x.v_wgs;
     for (int i = threadIdx.x; i < r.pairs; i += STORE_THREADS) cs[i] = rope_turn(r, t, i);
     __syncthreads();
-    const u32 slot = x.k ? (u32)slots[t] : ~0u;
-    const int heads = x.q_heads + (slot < c.slots ? 2 * c.kv_heads : 0);
+    const u32 slot = x.k ? (u32)x.slots[t] : ~0u;
+    const int heads = x.q_heads + (slot < c.slots ? c.kv_heads : 0);
+    const u32 page = slot / c.page_tokens, at = slot - page * c.page_tokens;
     float *row = rows[wave];
-    for (int h = wave; h < heads; h += STORE_THREADS / 64) {
-        const int kh = h - x.q_heads, vh = kh - c.kv_heads;
-        const float *in = kh < 0 ? x.q + t * x.ldq + (int64_t)h * c.dim
-                        : vh < 0 ? x.k + t * x.ldk + (int64_t)kh * c.dim : x.v + t * x.ldv + (int64_t)vh * c.dim;
-        const int pairs = vh < 0 ? r.pairs : 0;
-        for (int i = lane; i < pairs; i += 64) {
-            int a, b;
-            rope_pair(r, i, &a, &b);
+    for (int h = wave; h < heads; h += STORE_WAVES) {
+        const int kh = h - x.q_heads;
+        const float *in = kh < 0 ? x.q + t * x.ldq + (int64_t)h * c.dim : x.k + t * x.ldk + (int64_t)kh * c.dim;
+        for (int i = lane; i < r.pairs; i += 64) {
+            const int a = r.style == KQKV_ROPE_HALVES ? i : 2 * i, b = r.style == KQKV_ROPE_HALVES ? i + r.pairs : 2 * i + 1;
             const double va = in[a], vb = in[b];
             row[a] = (float)(va * cs[i].x - vb * cs[i].y);
             row[b] = (float)(va * cs[i].y + vb * cs[i].x);
         }
-        for (int d = 2 * pairs + lane; d < c.dim; d += 64) row[d] = in[d];
+        for (int d = 2 * r.pairs + lane; d < c.dim; d += 64) row[d] = in[d];
         wave_sync();
         if (kh < 0) {
             for (int d = lane; d < c.dim; d += 64) x.q_out[t * x.ldq_out + (int64_t)h * c.dim + d] = row[d];
-        } else if (vh < 0) {
-            store_row<Q8, false>(c, row, slot, kh, lane);
         } else {
-            store_row<Q8, true>(c, row, slot, vh, lane);
+            uint8_t *head = c.k + page * c.page_bytes + (u64)kh * c.head_bytes;
+            for (int d = 4 * lane; d < c.dim; d += 256) {
+                u32 m = 0;
+                if (Q8)
+                    for (int e = d & ~31; e < (d & ~31) + 32; e += 4) m = max(m, magnitude(*(const f4 *)(row + e)));
+                store_k4<Q8>(c, head, at, d, *(const f4 *)(row + d), m);
+            }
         }
         wave_sync();
     }
 }
 
 // ---------------------------------------------------------------------------
-// Load
+// Load: K by rows, 4 elements a lane, V in the units of the store.
 
-template <bool Q8, bool V>
-__device__ __forceinline__ float cached(const Cache &c, u32 page, u32 t, int head, int d) {
-    const uint8_t *from = (V ? c.v : c.k) + page * c.page_bytes + (u64)head * c.head_bytes;
-    const u32 i = V ? v_at(t, d, c.dim) : k_at(t, d, c.dim);
-    if (!Q8) return (float)((const _Float16 *)from)[i];
-    return (float)((const _Float16 *)(from + c.page_tokens * c.dim))[scale_at(t, d >> 5, c.dim)] *
-           (float)((const int8_t *)from)[i];
+template <bool Q8>
+__device__ __forceinline__ void load_v4(const Cache &c, const int32_t *slots, int T, float *v, int64_t unit, int lane) {
+    const int blocks = c.dim >> 5, per = c.kv_heads * blocks;
+    const int tokens = (int)(unit / per), left = (int)(unit - (int64_t)tokens * per), head = left / blocks, b = left - head * blocks;
+    const int t = tokens * 16 + (lane & 15), i = lane >> 4;
+    const u32 slot = t < T ? (u32)slots[t] : ~0u;
+    if (slot >= c.slots) return;
+    const u32 page = slot / c.page_tokens, at = slot - page * c.page_tokens;
+    const uint8_t *from = c.v + page * c.page_bytes + (u64)head * c.head_bytes;
+    const float s = Q8 ? (float)((const _Float16 *)(from + c.page_tokens * c.dim))[scale_at(at, b, c.dim)] : 1.f;
+    float *to = v + ((int64_t)t * c.kv_heads + head) * c.dim + b * 32 + 4 * i;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        f4 y;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const u32 j = v_at(at, b * 32 + 16 * k + 4 * i + e, c.dim);
+            y[e] = Q8 ? s * (float)((const int8_t *)from)[j] : (float)((const _Float16 *)from)[j];
+        }
+        *(f4 *)(to + 16 * k) = y;
+    }
 }
 
 template <bool Q8>
-__global__ __launch_bounds__(STORE_THREADS) void load_kernel(Cache c, const int32_t *slots, float *k, float *v) {
-    const int t = blockIdx.x, n = c.kv_heads * c.dim;
+__global__ __launch_bounds__(STORE_THREADS) void load_kernel(Cache c, const int32_t *slots, int T, float *k, float *v, int v_wgs) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if ((int)blockIdx.x < v_wgs) {
+        const int64_t units = (int64_t)((T + 15) / 16) * c.kv_heads * (c.dim >> 5);
+        for (int64_t u = (int64_t)blockIdx.x * STORE_WAVES + wave; u < units; u += (int64_t)v_wgs * STORE_WAVES)
+            load_v4<Q8>(c, slots, T, v, u, lane);
+        return;
+    }
+    const int t = blockIdx.x - v_wgs, n = c.kv_heads * c.dim;
     const u32 slot = (u32)slots[t];
     if (slot >= c.slots) return;
     const u32 page = slot / c.page_tokens, at = slot - page * c.page_tokens;
-    for (int i = threadIdx.x; i < n; i += STORE_THREADS) {
+    for (int i = 4 * threadIdx.x; i < n; i += 4 * STORE_THREADS) {
         const int head = i / c.dim, d = i - head * c.dim;
-        if (k) k[(int64_t)t * n + i] = cached<Q8, false>(c, page, at, head, d);
-        if (v) v[(int64_t)t * n + i] = cached<Q8, true>(c, page, at, head, d);
+        const uint8_t *from = c.k + page * c.page_bytes + (u64)head * c.head_bytes;
+        f4 y;
+        if (Q8) {
+            const float s = (float)((const _Float16 *)(from + c.page_tokens * c.dim))[scale_at(at, d >> 5, c.dim)];
+            const u32 w = *(const u32 *)(from + k_at(at, d, c.dim));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = s * (float)(int8_t)(w >> (8 * e));
+        } else {
+            y = __builtin_convertvector(*(const h4 *)(from + 2 * k_at(at, d, c.dim)), f4);
+        }
+        *(f4 *)(k + (int64_t)t * n + i) = y;
     }
+}
+
+// Work-groups for the units of v (16 tokens, head, 32 elements), a wave each as
+// long as the grid allows it.
+static int v_workgroups(const kqkv_cache *c, int T) {
+    const int64_t units = (int64_t)((T + 15) / 16) * c->kv_heads * (c->head_dim / 32);
+    return (int)std::min<int64_t>((units + STORE_WAVES - 1) / STORE_WAVES, 1 << 22);
 }
 
 } // namespace kv
@@ -396,7 +594,7 @@ int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const
                     const float *k, int64_t ldk, const float *v, int64_t ldv, void *stream) {
     int r = cache_check(cache);
     if (r) return r;
-    if (T < 0 || T >= (1 << 24) || q_heads < 0 || q_heads > 1024) return KQ_ERR_SHAPE;
+    if (T < 0 || T >= (1 << 23) || q_heads < 0 || q_heads > 1024) return KQ_ERR_SHAPE;
     Rope ra = {};
     if (rope) {
         if (rope->style != KQKV_ROPE_HALVES && rope->style != KQKV_ROPE_PAIRS) return KQ_ERR_ARG;
@@ -434,28 +632,35 @@ int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const
         ra.pos_stride = pos_stride;
         ra.style = rope->style;
     }
-    const Rows x = {q, k, v, q_out, ldq, ldq_out, ldk, ldv, q_heads, T};
+    Rows x = {q, k, v, q_out, slots, ldq, ldq_out, ldk, ldv, q_heads, T, 1, k ? v_workgroups(cache, T) : 0, 0};
+    const int lanes = cache->head_dim / 8, a_wg = 64 / lanes * STORE_WAVES, rows = q_heads + (k ? cache->kv_heads : 0);
+    x.lanes_magic = (u32)((65536 + lanes - 1) / lanes);
+    const bool q8 = cache->type == KQKV_Q8_0;
     hipStream_t st = (hipStream_t)stream;
-    if (cache->type == KQKV_F16)
-        hipLaunchKernelGGL(rope_store_kernel<false>, dim3(T), dim3(STORE_THREADS), 0, st, cache_args(cache), ra, x, slots);
-    else
-        hipLaunchKernelGGL(rope_store_kernel<true>, dim3(T), dim3(STORE_THREADS), 0, st, cache_args(cache), ra, x, slots);
+    const Cache c = cache_args(cache);
+    if (ra.pairs % 4 == 0) {
+        // up to about 4 work-groups a compute unit, no more than a wave's rows each
+        x.split = std::max(1, std::min((rows + a_wg - 1) / a_wg, 1024 / T));
+        hipLaunchKernelGGL(q8 ? rope_store_kernel<true> : rope_store_kernel<false>, dim3((unsigned)(x.v_wgs + T * x.split)),
+                           dim3(STORE_THREADS), 0, st, c, ra, x);
+    } else {
+        hipLaunchKernelGGL(q8 ? rope_store_any_kernel<true> : rope_store_any_kernel<false>, dim3((unsigned)(x.v_wgs + T)),
+                           dim3(STORE_THREADS), 0, st, c, ra, x);
+    }
     return launched();
 }
 
 int kqkv_load(const kqkv_cache *cache, int T, const int32_t *slots, float *k, float *v, void *stream) {
     const int r = cache_check(cache);
     if (r) return r;
-    if (T < 0 || T >= (1 << 24)) return KQ_ERR_SHAPE;
+    if (T < 0 || T >= (1 << 23)) return KQ_ERR_SHAPE;
     if (T == 0 || (!k && !v)) return KQ_OK;
     if (!slots) return KQ_ERR_NULL;
     if (!aligned(slots, 4) || !aligned(k, 16) || !aligned(v, 16)) return KQ_ERR_ALIGN;
     if (device_check()) return KQ_ERR_DEVICE;
-    hipStream_t st = (hipStream_t)stream;
-    if (cache->type == KQKV_F16)
-        hipLaunchKernelGGL(load_kernel<false>, dim3(T), dim3(STORE_THREADS), 0, st, cache_args(cache), slots, k, v);
-    else
-        hipLaunchKernelGGL(load_kernel<true>, dim3(T), dim3(STORE_THREADS), 0, st, cache_args(cache), slots, k, v);
+    const int v_wgs = v ? v_workgroups(cache, T) : 0;
+    hipLaunchKernelGGL(cache->type == KQKV_Q8_0 ? load_kernel<true> : load_kernel<false>, dim3((unsigned)(v_wgs + (k ? T : 0))),
+                       dim3(STORE_THREADS), 0, (hipStream_t)stream, cache_args(cache), slots, T, k, v, v_wgs);
     return launched();
 }
 

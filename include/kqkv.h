@@ -147,14 +147,14 @@ typedef struct kqkv_rope {
  * the scale s = fp16(max|x| / 127), at most 65504, and the quants
  * rint(x / s), -127..127 (0 when s is 0); a block with an infinity or a NaN
  * gets a NaN scale.  When two tokens name the same slot, either's values or a
- * mixture stay there.  0 <= T < 2^24, q_heads <= 1024. */
+ * mixture stay there.  0 <= T < 2^23, q_heads <= 1024. */
 int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const int32_t *pos, int64_t pos_stride,
                     const int32_t *slots, int q_heads, const float *q, int64_t ldq, float *q_out, int64_t ldq_out,
                     const float *k, int64_t ldk, const float *v, int64_t ldv, void *stream);
 
 /* Cached tokens as fp32: k[t], v[t] = rows of kv_heads * head_dim values of
  * slot slots[t] (contiguous rows; either may be NULL).  Exact for both formats.
- * Rows whose slot is outside the cache are left as they are.  0 <= T < 2^24. */
+ * Rows whose slot is outside the cache are left as they are.  0 <= T < 2^23. */
 int kqkv_load(const kqkv_cache *cache, int T, const int32_t *slots, float *k, float *v, void *stream);
 
 /* Workspace bytes of kqkv_attn for such a call (0 on invalid sizes; may be 0
