@@ -9,10 +9,16 @@ namespace kv {
 
 // ---------------------------------------------------------------------------
 // Plan
+//
+// Bound: latency.  One work-group holds up to 1024 requests, one a thread:
+// prefix sums of the new tokens and of the pages taken and given back, then a
+// thread per page and per row, which find their request by bisection in LDS.
+// Few rows are filled in by the same work-group, from the free list and the
+// table as they were, beside the writes; many by a second launch.
 
 constexpr int PLAN_THREADS = 1024;
 constexpr int PLAN_WAVES = PLAN_THREADS / 64;
-constexpr int SLOT_THREADS = 256;
+constexpr int ROW_THREADS = 256, ROW_STARTS = 4096;
 
 struct Plan {
     const int32_t *ctx_len, *new_len, *held, *n_free;
@@ -23,72 +29,81 @@ struct Plan {
 
 // What one request does in this step.  `bad`: a value out of range.
 struct Req {
-    int64_t after;      // length with its new tokens
-    int fresh;          // new tokens
-    int need, gone;     // pages taken, pages given back
+    int after;          // length with its new tokens
+    int fresh;          // new tokens, at most T < 2^23
+    int need, gone;     // pages taken, pages given back, at most 2^24
     int held;
     bool bad;
 };
 
 __device__ __forceinline__ Req plan_req(const Plan &p, int b) {
-    Req r = {0, 0, 0, 0, 0, false};
-    if (b >= p.B) return r;
-    const int ctx = p.ctx_len[b], add = p.new_len[b], held = p.held[b];
-    r.held = held;
+    const bool in = b < p.B;
+    const int i = in ? b : 0;
+    const int ctx = p.ctx_len[i], add = p.new_len[i], held = p.held[i];
+    Req r = {0, 0, 0, 0, held, false};
+    if (!in) return r;
     if (ctx < 0 || held < 0 || held > p.stride) {
         r.bad = true;
-        return r;
-    }
-    if (add < 0) {
+    } else if (add < 0) {
         r.gone = held;
-        return r;
+    } else {
+        const int64_t after = (int64_t)ctx + add;
+        const u32 pages = after > INT32_MAX ? ~0u : ((u32)after + (u32)p.P - 1) / (u32)p.P;
+        if (pages > p.stride || add > p.T) {
+            r.bad = true;
+        } else {
+            r.after = (int)after;
+            r.fresh = add;
+            r.need = max((int)pages - held, 0);
+        }
     }
-    r.after = (int64_t)ctx + add;
-    const int64_t pages = (r.after + p.P - 1) / p.P;
-    if (pages > p.stride || r.after > INT32_MAX) {
-        r.bad = true;
-        return r;
-    }
-    r.fresh = add;
-    r.need = pages > held ? (int)(pages - held) : 0;
     return r;
 }
 
-// Three running sums of a block: each thread's exclusive ones and the totals.
-// Sums over all requests stay below 2^16 * 2^31.
-struct Sums { int64_t fresh, need, gone; };
-__device__ __forceinline__ int64_t wave_scan(int64_t v, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int64_t o = __shfl_up(v, d);
-        if (lane >= d) v += o;
-    }
-    return v;
+// Inclusive prefix sums over a wave (or, ROWS_ONLY, over each row of 16 lanes).
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp_or_0(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xF, false);
 }
-__device__ __forceinline__ void block_scan(const Req &r, Sums *wave_sums, Sums *excl, Sums *total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const Sums in = {wave_scan(r.fresh, lane), wave_scan(r.need, lane), wave_scan(r.gone, lane)};
-    __syncthreads();                              // the last use of wave_sums is over
-    if (lane == 63) wave_sums[wave] = in;
-    __syncthreads();
-    Sums e = {in.fresh - r.fresh, in.need - r.need, in.gone - r.gone}, t = {0, 0, 0};
-    for (int w = 0; w < PLAN_WAVES; ++w) {
-        const Sums s = wave_sums[w];
-        if (w < wave) {
-            e.fresh += s.fresh;
-            e.need += s.need;
-            e.gone += s.gone;
-        }
-        t.fresh += s.fresh;
-        t.need += s.need;
-        t.gone += s.gone;
+template <bool ROWS_ONLY> __device__ __forceinline__ int scan(int x) {
+    x += dpp_or_0<0x111, 0xF>(x);
+    x += dpp_or_0<0x112, 0xF>(x);
+    x += dpp_or_0<0x114, 0xF>(x);
+    x += dpp_or_0<0x118, 0xF>(x);
+    if (!ROWS_ONLY) {
+        x += dpp_or_0<0x142, 0xA>(x);
+        x += dpp_or_0<0x143, 0xC>(x);
     }
-    *excl = e;
-    *total = t;
+    return x;
+}
+
+// A running sum over the work-group's threads: each thread's exclusive one and
+// the total.  A wave's sum stays below 2^30, the total is held in 64 bits (where
+// it passes 31, the step fails and the exclusive sums are not used).
+struct Sum { int before; int64_t total; };
+__device__ __forceinline__ Sum block_sum(int x, int scanned, const int *waves, int wave) {
+    const int lane = threadIdx.x & 63, w = waves[lane & 15];
+    const int s = scan<true>(w);
+    const int64_t total = ((int64_t)__builtin_amdgcn_readlane(scan<true>(w >> 16), 15) << 16) +
+                          __builtin_amdgcn_readlane(scan<true>(w & 0xFFFF), 15);
+    return Sum{__builtin_amdgcn_readlane(s - w, wave) + scanned - x, total};
+}
+struct Sums { Sum fresh, need, gone; };
+__device__ __forceinline__ Sums block_sums(const Req &r, int (*waves)[PLAN_WAVES]) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int f = scan<false>(r.fresh), n = scan<false>(r.need), g = scan<false>(r.gone);
+    __syncthreads();                              // the last use of `waves` is over
+    if (lane == 63) {
+        waves[0][wave] = f;
+        waves[1][wave] = n;
+        waves[2][wave] = g;
+    }
+    __syncthreads();
+    return Sums{block_sum(r.fresh, f, waves[0], wave), block_sum(r.need, n, waves[1], wave),
+                block_sum(r.gone, g, waves[2], wave)};
 }
 
 // Last index b in [0, n) with first[b] <= i (first ascending, first[0] <= i).
-template <class T> __device__ __forceinline__ int last_not_after(const T *first, int n, T i) {
+__device__ __forceinline__ int last_not_after(const int *first, int n, int i) {
     int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -97,48 +112,31 @@ template <class T> __device__ __forceinline__ int last_not_after(const T *first,
     return lo;
 }
 
-// Slot and position of row t, from the outputs of the requests' part.
-__device__ __forceinline__ void plan_row(const Plan &p, const int32_t *start, int t) {
-    int pos = 0, slot = -1;
-    if (t < start[p.B]) {
-        const int b = last_not_after(start, p.B, t);
-        pos = p.ctx_out[b] - (start[b + 1] - t);
-        const u32 page = (u32)pos / (u32)p.P;
-        const u32 id = (u32)p.table[(int64_t)b * p.stride + page];
-        if (id < (u32)p.n_pages) slot = (int)(id * p.P + ((u32)pos - page * (u32)p.P));
-    }
-    p.pos[t] = pos;
-    p.slots[t] = slot;
+__device__ __forceinline__ int slot_of(const Plan &p, u32 id, u32 pos, u32 page) {
+    return id < (u32)p.n_pages ? (int)(id * p.P + (pos - page * (u32)p.P)) : -1;
 }
 
-// One work-group for the requests: prefix sums of the new tokens and of the
-// pages taken and given back, then the pages themselves, a thread per page (the
-// request of page i by bisection of the prefix sums in LDS).  `rows`: it fills
-// slots and pos too.
 __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
-    __shared__ Sums wave_sums[PLAN_WAVES];
-    __shared__ int first_need[PLAN_THREADS], first_gone[PLAN_THREADS], base[PLAN_THREADS];
-    __shared__ int any_bad;
+    __shared__ int waves[3][PLAN_WAVES];
+    __shared__ int first[PLAN_THREADS], first_need[PLAN_THREADS], after[PLAN_THREADS], had[PLAN_THREADS];
     const int tid = threadIdx.x;
-    if (tid == 0) any_bad = 0;
-    __syncthreads();
+    const bool one = p.B <= PLAN_THREADS;
+    const int n_free = p.n_free[0];
     // totals, before anything is written
-    Sums total = {0, 0, 0}, excl;
-    Req r;
-    for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
-        Sums t;
-        r = plan_req(p, b0 + tid);
-        if (r.bad) any_bad = 1;
-        block_scan(r, wave_sums, &excl, &t);
-        total.fresh += t.fresh;
-        total.need += t.need;
-        total.gone += t.gone;
+    Req r = plan_req(p, tid);
+    bool bad = r.bad;
+    Sums s = block_sums(r, waves);
+    int64_t fresh = s.fresh.total, need = s.need.total, gone = s.gone.total;
+    for (int b0 = PLAN_THREADS; b0 < p.B; b0 += PLAN_THREADS) {
+        const Req o = plan_req(p, b0 + tid);
+        bad = bad || o.bad;
+        const Sums t = block_sums(o, waves);
+        fresh += t.fresh.total;
+        need += t.need.total;
+        gone += t.gone.total;
     }
-    const int64_t n_free = p.n_free[0];
-    const int64_t top = n_free + total.gone;
-    __syncthreads();
-    const bool ok = !any_bad && n_free >= 0 && top <= p.n_pages && total.need <= top && total.fresh <= p.T;
-    const bool one = p.B <= PLAN_THREADS;          // r and excl are still those of every request
+    const int64_t top = n_free + gone;
+    const bool ok = !__syncthreads_or(bad) && n_free >= 0 && top <= p.n_pages && need <= top && fresh <= p.T;
     if (!ok) {
         for (int b = tid; b < p.B; b += PLAN_THREADS) {
             p.seq_start[b] = 0;
@@ -147,73 +145,100 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
         }
         if (tid == 0) {
             p.seq_start[p.B] = 0;
-            p.n_free_out[0] = (int)n_free;
+            p.n_free_out[0] = n_free;
             if (p.err) p.err[0] = 1;
         }
-    } else {
-        // the ended requests' pages go on the list first: in another order
-        // than the requests' own chunks, so in a pass of their own
-        Sums done = {0, 0, 0};
-        for (int b0 = 0; total.gone > 0 && b0 < p.B; b0 += PLAN_THREADS) {
-            Sums t;
+        for (int t = tid; rows && t < p.T; t += PLAN_THREADS) {
+            p.slots[t] = -1;
+            p.pos[t] = 0;
+        }
+        return;
+    }
+    // the ended requests' pages go on the list before any are taken from it
+    if (gone) {
+        int64_t done = n_free;
+        for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
             if (!one) {
                 r = plan_req(p, b0 + tid);
-                block_scan(r, wave_sums, &excl, &t);
-            } else {
-                t = total;
+                s = block_sums(r, waves);
             }
-            first_gone[tid] = (int)excl.gone;
+            first[tid] = s.gone.before;
             __syncthreads();
-            const int n = p.B - b0 < PLAN_THREADS ? p.B - b0 : PLAN_THREADS;
-            for (int i = tid; i < (int)t.gone; i += PLAN_THREADS) {
-                const int b = last_not_after(first_gone, n, i);
-                p.free_pages[n_free + done.gone + i] = p.table[(int64_t)(b0 + b) * p.stride + (i - first_gone[b])];
+            const int n = min(p.B - b0, PLAN_THREADS);
+            for (int i = tid; i < (int)s.gone.total; i += PLAN_THREADS) {
+                const int b = last_not_after(first, n, i);
+                p.free_pages[done + i] = p.table[(int64_t)(b0 + b) * p.stride + (i - first[b])];
             }
-            done.gone += t.gone;
+            done += s.gone.total;
             __syncthreads();
         }
-        for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
-            Sums t;
-            const int b = b0 + tid;
-            if (!one) {
-                r = plan_req(p, b);
-                block_scan(r, wave_sums, &excl, &t);
-            } else {
-                t = total;
-            }
-            first_need[tid] = (int)excl.need;
-            base[tid] = r.held;
-            __syncthreads();
-            const int n = p.B - b0 < PLAN_THREADS ? p.B - b0 : PLAN_THREADS;
-            for (int i = tid; i < (int)t.need; i += PLAN_THREADS) {
-                const int c = last_not_after(first_need, n, i);
-                p.table[(int64_t)(b0 + c) * p.stride + base[c] + (i - first_need[c])] =
-                    p.free_pages[top - 1 - (done.need + i)];
-            }
-            if (b < p.B) {
-                p.seq_start[b] = (int)(done.fresh + excl.fresh);
-                p.held_out[b] = r.gone ? 0 : r.held + r.need;
-                p.ctx_out[b] = (int)r.after;
-            }
-            done.fresh += t.fresh;
-            done.need += t.need;
-            __syncthreads();
-        }
-        if (tid == 0) {
-            p.seq_start[p.B] = (int)total.fresh;
-            p.n_free_out[0] = (int)(top - total.need);
-        }
-    }
-    if (rows) {
         __threadfence_block();
+    }
+    int tokens = 0, taken = 0;
+    for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+        if (!one) {
+            r = plan_req(p, b0 + tid);
+            s = block_sums(r, waves);
+        }
+        first[tid] = s.fresh.before;
+        first_need[tid] = s.need.before;
+        after[tid] = r.after;
+        had[tid] = r.held;
         __syncthreads();
-        for (int t = tid; t < p.T; t += PLAN_THREADS) plan_row(p, p.seq_start, t);
+        const int n = min(p.B - b0, PLAN_THREADS), b = b0 + tid;
+        auto new_page = [&](int i) { return p.free_pages[top - 1 - (taken + i)]; };
+        // rows (only where one chunk holds every request): their pages from the list and the table as they were
+        for (int t = tid; rows && t < p.T; t += PLAN_THREADS) {
+            int pos = 0, slot = -1;
+            if (t < (int)fresh) {
+                const int c = last_not_after(first, n, t);
+                const int end = c + 1 < n ? first[c + 1] : (int)fresh;
+                pos = after[c] - (end - t);
+                const u32 page = (u32)pos / (u32)p.P;
+                const int at = (int)page - had[c];
+                slot = slot_of(p, (u32)(at < 0 ? p.table[(int64_t)c * p.stride + page] : new_page(first_need[c] + at)), (u32)pos, page);
+            }
+            p.pos[t] = pos;
+            p.slots[t] = slot;
+        }
+        for (int i = tid; i < (int)s.need.total; i += PLAN_THREADS) {
+            const int c = last_not_after(first_need, n, i);
+            p.table[(int64_t)(b0 + c) * p.stride + had[c] + (i - first_need[c])] = new_page(i);
+        }
+        if (b < p.B) {
+            p.seq_start[b] = tokens + s.fresh.before;
+            p.held_out[b] = r.gone ? 0 : r.held + r.need;
+            p.ctx_out[b] = r.after;
+        }
+        tokens += (int)s.fresh.total;
+        taken += (int)s.need.total;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.seq_start[p.B] = tokens;
+        p.n_free_out[0] = (int)top - taken;
     }
 }
 
-__global__ __launch_bounds__(SLOT_THREADS) void plan_rows_kernel(Plan p) {
-    const int t = blockIdx.x * SLOT_THREADS + threadIdx.x;
-    if (t < p.T) plan_row(p, p.seq_start, t);
+// Rows, from the outputs of plan_kernel.
+__global__ __launch_bounds__(ROW_THREADS) void plan_rows_kernel(Plan p) {
+    __shared__ int starts[ROW_STARTS];
+    const int t = blockIdx.x * ROW_THREADS + threadIdx.x;
+    const bool here = p.B <= ROW_STARTS;
+    if (here) {
+        for (int b = threadIdx.x; b < p.B; b += ROW_THREADS) starts[b] = p.seq_start[b];
+        __syncthreads();
+    }
+    if (t >= p.T) return;
+    int pos = 0, slot = -1;
+    if (t < p.seq_start[p.B]) {
+        const int b = here ? last_not_after(starts, p.B, t) : last_not_after(p.seq_start, p.B, t);
+        pos = p.ctx_out[b] - (p.seq_start[b + 1] - t);
+        const u32 page = (u32)pos / (u32)p.P;
+        slot = slot_of(p, (u32)p.table[(int64_t)b * p.stride + page], (u32)pos, page);
+    }
+    p.pos[t] = pos;
+    p.slots[t] = slot;
 }
 
 // ---------------------------------------------------------------------------
@@ -567,7 +592,7 @@ int kqkv_plan(int B, const int32_t *ctx_len, const int32_t *new_len, int page_to
               int64_t table_stride, const int32_t *held, int32_t *held_out, int32_t *free_pages, int64_t n_pages,
               const int32_t *n_free, int32_t *n_free_out, int T, int32_t *slots, int32_t *pos, int32_t *seq_start,
               int32_t *ctx_out, int32_t *err_flag, void *stream) {
-    if (B < 1 || B > 65536 || T < 0 || table_stride < 1 || table_stride > (1 << 24)) return KQ_ERR_SHAPE;
+    if (B < 1 || B > 65536 || T < 0 || T >= (1 << 23) || table_stride < 1 || table_stride > (1 << 24)) return KQ_ERR_SHAPE;
     if (page_tokens < 16 || page_tokens > 256 || page_tokens % 16) return KQ_ERR_SHAPE;
     if (n_pages < 1 || n_pages > INT32_MAX / page_tokens) return KQ_ERR_SHAPE;
     const void *need[] = {ctx_len, new_len, table, held, held_out, free_pages, n_free, n_free_out, seq_start, ctx_out};
@@ -581,11 +606,11 @@ int kqkv_plan(int B, const int32_t *ctx_len, const int32_t *new_len, int page_to
     Plan p = {ctx_len, new_len, held, n_free, table, held_out, free_pages, n_free_out, slots, pos, seq_start, ctx_out,
               err_flag, table_stride, B, page_tokens, T, (int)n_pages};
     hipStream_t st = (hipStream_t)stream;
-    const bool apart = T > 4 * PLAN_THREADS;
+    // a work-group alone fills in 4 rows a thread as fast as a second launch begins
+    const bool apart = T > 4 * PLAN_THREADS || B > PLAN_THREADS;
     hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p, apart ? 0 : 1);
-    if (apart)
-        hipLaunchKernelGGL(plan_rows_kernel, dim3((unsigned)(((int64_t)T + SLOT_THREADS - 1) / SLOT_THREADS)),
-                           dim3(SLOT_THREADS), 0, st, p);
+    if (apart && T)
+        hipLaunchKernelGGL(plan_rows_kernel, dim3((unsigned)((T + ROW_THREADS - 1) / ROW_THREADS)), dim3(ROW_THREADS), 0, st, p);
     return launched();
 }
 

@@ -103,7 +103,7 @@ int64_t kqkv_page_bytes(int type, int kv_heads, int head_dim, int page_tokens);
  * 0, lengths, held and n_free come out unchanged, table and free_pages are left.
  * With in-place arguments (held_out == held, ...) the step is taken once per
  * call; with separate ones the call may be repeated with the same result.
- * 1 <= B <= 65536, 0 <= T < 2^31, 1 <= table_stride <= 2^24, page_tokens and
+ * 1 <= B <= 65536, 0 <= T < 2^23, 1 <= table_stride <= 2^24, page_tokens and
  * n_pages as in a cache.  slots and pos may be NULL when T is 0. */
 int kqkv_plan(int B, const int32_t *ctx_len, const int32_t *new_len, int page_tokens,
               int32_t *table, int64_t table_stride, const int32_t *held, int32_t *held_out,
