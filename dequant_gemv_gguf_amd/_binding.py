@@ -388,19 +388,35 @@ def kq_stream_qgemv(h, qtype, W, N, K, x, M, y):
 # cache: a KVCache, rope: a KVRope (or None).  Tensors or int addresses.  A call
 # goes to the device that its tensors are on, on that device's current stream.
 
+# These calls are made once per layer and token, and take a few microseconds on
+# the GPU: what the host spends on them shows.  So the current stream is asked
+# for by torch._C's raw calls (0.1 us; torch.cuda.current_stream makes a Stream
+# object, 2.8 us), and addresses go to ctypes as ints.
+
+_torch_c = None
+
+
 def _device_call(fn, like, stream, *args):
     """Calls lib().fn(*args, stream) with the tensor `like`'s device current."""
+    global _torch_c
     f = getattr(_lib or lib(), fn)
-    if stream is None and like is not None and not isinstance(like, int) and like.is_cuda:
-        import torch
-        if like.device.index != torch.cuda.current_device():
-            with torch.cuda.device(like.device):
-                _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
-            return
-        stream = torch.cuda.current_stream().cuda_stream
-    elif stream is not None and not isinstance(stream, int):
+    if stream is None:
+        if like is not None and type(like) is not int and like.is_cuda:
+            if _torch_c is None:
+                import torch
+                _torch_c = torch._C
+            device = like.get_device()
+            if device != _torch_c._cuda_getDevice():
+                import torch
+                with torch.cuda.device(device):
+                    _check(fn, f(*args, _torch_c._cuda_getCurrentRawStream(device)))
+                return
+            stream = _torch_c._cuda_getCurrentRawStream(device)
+    elif type(stream) is not int:
         stream = stream.cuda_stream
-    _check(fn, f(*args, stream))
+    r = f(*args, stream)
+    if r:
+        raise KQError(fn, r)
 
 
 def kqkv_page_bytes(qtype, kv_heads, head_dim, page_tokens):
