@@ -39,18 +39,14 @@
 
 #include "kq_kv.h"
 
-#ifndef DEPTH_
-#define DEPTH_ 1
-#endif
-#ifndef OCC_
-#define OCC_ (NB <= 4 ? 3 : NB <= 6 ? 2 : 1)
-#endif
 namespace kq {
 namespace kv {
 
 constexpr int TILE = 32;                       // keys
 constexpr int ATTN_THREADS = 256, ATTN_WAVES = 4;
-constexpr float NONE = -1e30f;                 // m before the first key
+// Waves per SIMD that the registers are cut for (a tile, o and the softmax), so that no kernel spills.
+constexpr int ATTN_OCCUPANCY(int NB) { return NB <= 4 ? 3 : NB <= 6 ? 2 : 1; }
+constexpr float NONE = -3e38f;                 // m before the first key
 constexpr float SLACK = 8.f, LIFT = 6.f;       // weights reach 2^(SLACK + LIFT) < 65504
 
 struct Attn {
@@ -376,12 +372,12 @@ __device__ __forceinline__ float across_groups_sum(float x) {
 // w / row_tiles + i * (4 / row_tiles) of the piece (waves that share a key tile
 // read it through the caches); the waves of a row tile join through LDS.
 template <bool Q8, int NB, bool NT>
-__global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn a) {
+__global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(Cache c, Attn a) {
     constexpr int D = 32 * NB, LD = D + 4;
     // While the tiles go by, a wave's part holds its q limbs (operands as lanes read them), the blocks' sums of
-    // q and two tiles' scales; at the
+    // q and a tile's scales; at the
     // end, [wave][16][LD] outputs, then [wave][16] (m, l).
-    constexpr int QB = NB * 2 * 1024, OB = Q8 ? NB * 256 : 0, SB = Q8 ? NB * 128 : 0, PART = QB + OB + 2 * SB;
+    constexpr int QB = NB * 2 * 1024, OB = Q8 ? NB * 256 : 0, SB = Q8 ? NB * 128 : 0, PART = QB + OB + SB;
     constexpr int JOIN = 16 * (LD + 2) * 4;
     __shared__ __align__(16) uint8_t lds_[ATTN_WAVES * (PART > JOIN ? PART : JOIN)];
     float *lds = (float *)lds_;
@@ -488,26 +484,23 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
     const int sl = lane % (8 * NB);
     const uint8_t *sb = (sl / (4 * NB) ? vb : kb) + (sl % (2 * NB)) * 16;
     const bool second = (sl / (2 * NB)) & 1;
-    auto get_k = [&](Tile<Q8, NB> &to, const Where &w) {
-        load_k<Q8, NB, NT>(to, kb + w.x0, kb + w.x0 + w.dx, lane);
-        if constexpr (Q8) to.s = *(const h8 *)(sb + w.s0 + (second ? w.ds : 0));
+    Tile<Q8, NB> T;
+    auto get_k = [&](const Where &w) {
+        load_k<Q8, NB, NT>(T, kb + w.x0, kb + w.x0 + w.dx, lane);
+        if constexpr (Q8) T.s = *(const h8 *)(sb + w.s0 + (second ? w.ds : 0));
     };
-    auto get_v = [&](Tile<Q8, NB> &to, const Where &w) { load_v<Q8, NB, NT>(to, vb + w.x0 + ((g & 2) ? w.dx : 0), lane); };
+    auto get_v = [&](const Where &w) { load_v<Q8, NB, NT>(T, vb + w.x0 + ((g & 2) ? w.dx : 0), lane); };
     auto wrong_of = [&](int n) { return (u32)(bad >> (2 * (n & 31))) & 3; };
 
-    constexpr int DEPTH = DEPTH_;
-    Tile<Q8, NB> tiles[DEPTH];
-    // The first tiles' loads, also for a wave without tiles (page 0 then): under a condition, every wait for q behind them
+    // The first tile's loads, also for a wave without tiles (page 0 then): under a condition, every wait for q behind them
     // would wait for them too.
     ask_ids(0);
     take_ids(0);
-#pragma unroll
-    for (int u = 0; u < DEPTH; ++u) {
-        const int n = max(min(u, N - 1), 0);
-        const Where w = where(n);
-        get_k(tiles[u], w);
-        get_v(tiles[u], w);
-        tiles[u].wrong = wrong_of(n);
+    {
+        const Where w = where(0);
+        get_k(w);
+        get_v(w);
+        T.wrong = wrong_of(0);
     }
     ask_ids(32);
 
@@ -545,10 +538,10 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
         }
     }
     u32 qat = (u32)lane * 16;
-    auto tile_step = [&](Tile<Q8, NB> &T, int n, int stage) __attribute__((always_inline)) {
+    uint8_t *scales = part + QB + OB;
+    for (int n = 0; n < N; ++n) {
         // (q's address is made anew for each tile, so that the reads stay here)
         asm volatile("" : "+v"(qat));
-        uint8_t *scales = part + QB + OB + stage * SB;
         if constexpr (Q8) *(h8 *)(scales + sl * 16) = T.s;
         // scores of the lane's 8 keys, times 1 / unscale
         order_k<Q8, NB>(T);
@@ -584,14 +577,14 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
             for (int i = 0; i < 4; ++i) s[4 * t + i] = Q8 ? d[t][i] : d[t][i] + d2[t][i];
         const u32 wrong = T.wrong;
         const int tile = first + kws * n;
-        // the keys of the tile after the next (behind the last, the last tile's again)
-        const int nn = min(n + DEPTH, N - 1);
-        if (nn == n + DEPTH && (nn & 31) == 0) {
+        // the next tile's keys (behind the last, the last tile's again)
+        const int nn = min(n + 1, N - 1);
+        if (nn > n && (nn & 31) == 0) {
             take_ids(nn);
             ask_ids(nn + 32);
         }
         const Where next = where(nn);
-        get_k(T, next);
+        get_k(next);
         T.wrong = wrong_of(nn);
         const bool edge = wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min;
         uint32_t gone = 0;                       // keys of the lane that no row may touch
@@ -671,11 +664,7 @@ __global__ __launch_bounds__(ATTN_THREADS, OCC_) void attn_kernel(Cache c, Attn 
 #pragma unroll
             for (int k = 0; k < 2 * NB; ++k) o[k] = mma(vop(k), pl, o[k]);
         }
-        get_v(T, next);
-    };
-    for (int n = 0; n < N; n += DEPTH) {
-        tile_step(tiles[0], n, 0);
-        if (DEPTH > 1 && n + 1 < N) tile_step(tiles[DEPTH - 1], n + 1, 1);
+        get_v(next);
     }
     l = across_groups_sum(l);
     __syncthreads();                            // the q limbs' place is taken by what follows
