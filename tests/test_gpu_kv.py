@@ -484,6 +484,98 @@ def test_attn_on_another_stream_and_two_at_once():
         check_attn(d[4].cpu().numpy(), want, tol)
 
 
+@pytest.mark.parametrize("type", [F16, Q8])
+def test_attn_hint_of_a_huge_context(type):
+    # max_ctx only sets how the work is split and how lines are read: the largest one, on ordinary and empty requests
+    rng = np.random.default_rng(14)
+    ctx, new = [2500, 0, 31, 700], [1, 1, 0, 1]
+    for q_heads, kv_heads, dim in ((8, 2, 128), (6, 3, 96), (4, 4, 32)):
+        ref, table, start, q = attn_case(rng, type, q_heads, kv_heads, dim, 32, ctx, new)
+        got = run_attn(ref, table, ctx, start, q, q_heads, dim ** -0.5, 0, 1, max_ctx=2 ** 31 - 1)
+        want, tol = kv_ref.attn(ref, table, ctx, start, q, q_heads, float(np.float32(dim ** -0.5)), 0, out=np.full_like(q, 3.0))
+        check_attn(got, want, tol)
+
+
+@pytest.mark.parametrize("type", [F16, Q8])
+@pytest.mark.parametrize("q_heads,dim,ctx,new,window", [(16, 64, [3000, 500], [8, 8], 0), (40, 32, [1700], [8], 900),
+                                                         (24, 128, [1200, 40], [2, 1], 0), (5, 256, [1100], [7], 0)])
+def test_attn_many_rows_over_cut_contexts(type, q_heads, dim, ctx, new, window):
+    rng = np.random.default_rng(q_heads)
+    ref, table, start, q = attn_case(rng, type, q_heads, 1, dim, 16, ctx, new)
+    got = run_attn(ref, table, ctx, start, q, q_heads, dim ** -0.5, window, 8)
+    want, tol = kv_ref.attn(ref, table, ctx, start, q, q_heads, float(np.float32(dim ** -0.5)), window, out=np.full_like(q, 3.0))
+    check_attn(got, want, tol)
+
+
+@pytest.mark.parametrize("B,longest", [(65, 1500), (200, 90), (1000, 20)])
+def test_attn_many_requests(B, longest):
+    # more requests than a wave's lanes: lengths and rows are found over several rounds
+    rng = np.random.default_rng(B)
+    ctx = [int(n) for n in rng.integers(0, 40, B)]
+    ctx[B // 2], ctx[-1] = longest, longest // 2
+    new = [int(n) for n in rng.integers(0, 2, B)]
+    new[B // 2] = new[-1] = 1
+    ref, table, start, q = attn_case(rng, F16, 2, 1, 32, 16, ctx, new)
+    want, tol = kv_ref.attn(ref, table, ctx, start, q, 2, float(np.float32(0.18)), 0, out=np.full_like(q, 3.0))
+    for max_ctx in (longest, 2 ** 31 - 1, 1):
+        check_attn(run_attn(ref, table, ctx, start, q, 2, 0.18, 0, 1, max_ctx=max_ctx), want, tol)
+
+
+@pytest.mark.parametrize("type", [F16, Q8])
+def test_pages_past_four_gibibytes(type):
+    # the last pages of a cache of over 4 GiB, K and V each: written, read back and attended to
+    rng = np.random.default_rng(4)
+    H, D, page, n = 8, 256, 64, 70
+    pb = kq.kqkv_page_bytes(type, H, D, page)
+    n_pages = (1 << 32) // pb + 9
+    kb, vb = (torch.empty(n_pages * pb, dtype=torch.uint8, device="cuda") for _ in range(2))
+    cache = kq.KVCache(type, H, D, page, n_pages, kb, vb)
+    k, v = (rng.standard_normal((n, H, D)).astype(np.float32) for _ in range(2))
+    far = np.array([[n_pages - 1, n_pages - 2]], np.int32)
+    slots = far[0][np.arange(n) // page] * page + np.arange(n) % page
+    kq.kqkv_rope_store(cache, None, n, None, 0, i32(slots), 0, None, 0, None, 0, dev(k.reshape(n, -1)), H * D, dev(v.reshape(n, -1)), H * D)
+    small = kv_ref.Cache(type, H, D, page, 2)
+    for t in range(n):
+        small.put(t, k[t], v[t])
+    ko, vo = (torch.zeros(n, H * D, device="cuda") for _ in range(2))
+    kq.kqkv_load(cache, n, i32(slots), ko, vo)
+    want = [small.get(t) for t in range(n)]
+    assert np.array_equal(ko.cpu().numpy().reshape(n, H, D), np.stack([a for a, _ in want]).astype(np.float32))
+    assert np.array_equal(vo.cpu().numpy().reshape(n, H, D), np.stack([a for _, a in want]).astype(np.float32))
+    q = rng.standard_normal((1, H * D)).astype(np.float32)
+    got = run_attn(small, far, [n], [0, 1], q, H, 0.0625, 0, 1, dc=cache)
+    want, tol = kv_ref.attn(small, np.array([[0, 1]]), [n], [0, 1], q, H, 0.0625, 0)
+    check_attn(got, want, tol)
+
+
+def test_attn_two_graphs_share_a_workspace():
+    # captured with different sizes, replayed in turn on one stream with eager work between
+    rng = np.random.default_rng(15)
+    made = []
+    for ctx, new, heads, type in (([1900, 30], [1, 1], 8, F16), ([700, 600, 5], [4, 1, 2], 4, Q8)):
+        ref, table, start, q = attn_case(rng, type, heads, 2, 64, 16, ctx, new)
+        cache = device_cache(ref)
+        nb = kq.kqkv_attn_workspace_bytes(cache[0], len(ctx), 4, 2000, heads)
+        made.append((ref, table, start, q, ctx, heads, cache, nb, (i32(ctx), i32(start), i32(table), dev(q), torch.zeros(q.shape, device="cuda"))))
+    ws = torch.full((max(m[7] for m in made),), 0xFF, dtype=torch.uint8, device="cuda")
+    graphs = []
+    torch.cuda.synchronize()
+    for ref, table, start, q, ctx, heads, cache, nb, d in made:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            kq.kqkv_attn(cache[0], len(ctx), 4, 2000, d[0], d[1], d[2], table.shape[1], heads, q.shape[0], d[3], q.shape[1], 0.125, 0,
+                         d[4], q.shape[1], ws, nb)
+        graphs.append(g)
+    wants = [kv_ref.attn(m[0], m[1], m[4], m[2], m[3], m[5], 0.125, 0) for m in made]
+    for rep in range(4):
+        for i in (0, 1, 1, 0):
+            made[i][8][4].zero_()
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            check_attn(made[i][8][4].cpu().numpy(), *wants[i])
+            torch.empty(1 << 20, device="cuda").normal_()
+
+
 # ---- together --------------------------------------------------------------------------
 
 def test_steps_of_a_layer_between_the_projections():
