@@ -7,7 +7,7 @@
 // for any m_r: the keys are cut into tiles of 32, each wave keeps a running m,
 // sum l and accumulator o of its tiles, and two such states join as
 //   m = max(m', m''), l = l' 2^(m' - m) + l'' 2^(m'' - m), o likewise.
-// m follows the running maximum (Q8_0: see below) only when a score exceeds it by 2^8 (weights
+// m follows the running maximum only when a score exceeds it by 2^8 (weights
 // stay below 2^14 with the offset below): then o and l are rescaled; most tiles
 // need neither the maximum over the lanes of a row nor a rescaling.
 //
@@ -28,13 +28,19 @@
 // load.  A lane belongs to one row throughout: m, l and masks are per lane.
 //
 // Precision.  A row's q is scaled by a power of two that brings its largest
-// element to [2^10, 2^11) and enters as two fp16 limbs (22 bits); cached values
-// enter as they are (int8 quants are whole fp16 numbers, a block's scale is
-// applied to its 32-element partial score in fp32).  Weights, times 2^6, enter
-// as two fp16 limbs too, in a Q8_0 cache multiplied by the value's scale: m then
-// follows the score plus the exponent of the tile's largest scale, so that the
-// products stay below 2^14 whatever the scales are.  The limbs end at 2^-25, 2^-31
-// of the largest product.
+// element to [2^10, 2^11) and enters as two fp16 limbs (22 bits), and so do the
+// weights, times 2^6 (the limbs end at 2^-25, 2^-31 of the largest weight).
+// fp16 keys and values enter as they are.  Int8 quants of keys are whole fp16
+// numbers, a block's scale is applied to its 32-element partial score in fp32;
+// an int8 value, scale times quant (19 bits, a multiple of 2^-24), is exactly the
+// half it rounds to and the half that remains.  Of the products of two two-limb
+// numbers the one of both low limbs is left out (2^-22).
+//
+// Measured (MI355X, 64 query heads, 8 kv heads, head size 128): one request of
+// 131072 fp16 tokens 98 us (5.5 TB/s of K and V), of 524288 369 us (5.8 TB/s); 64
+// requests of up to 32768 Q8_0 tokens 301 us (5.2 TB/s); one of 37 tokens 6.0 us;
+// eight rows of 4 requests of up to 16384 Q8_0 tokens 62 us, for which the matrix
+// and vector units are what is waited for.
 #pragma once
 
 #include "kq_kv.h"
@@ -45,7 +51,9 @@ namespace kv {
 constexpr int TILE = 32;                       // keys
 constexpr int ATTN_THREADS = 256, ATTN_WAVES = 4;
 // Waves per SIMD that the registers are cut for (a tile, o and the softmax), so that no kernel spills.
-constexpr int ATTN_OCCUPANCY(int NB) { return NB <= 4 ? 3 : NB <= 6 ? 2 : 1; }
+constexpr int ATTN_OCCUPANCY(int NB, int RT) { return RT == 1 ? (NB <= 4 ? 3 : NB <= 6 ? 2 : 1) : NB <= 2 ? 3 : 2; }
+// Head sizes that have kernels with two row tiles a wave (past them, the registers do not suffice).
+constexpr int TWO_TILES_NB = 4;
 constexpr float NONE = -3e38f;                 // m before the first key
 constexpr float SLACK = 8.f, LIFT = 6.f;       // weights reach 2^(SLACK + LIFT) < 65504
 
@@ -60,7 +68,7 @@ struct Attn {
     int rows_cap;              // group * max_q
     int items;                 // most pieces that all requests are cut into, >= B
     int min_tiles;             // no piece smaller than this
-    int row_tiles;             // 16-row tiles per work-group: 1, 2 or 4
+    int row_waves;             // waves of a work-group that differ in their rows: 1, 2 or 4
     u32 group_magic, gp_magic; // ceil(2^32 / d) for d = group and page_tokens / 16: x / d is the upper half of x * magic
                                // while x * d < 2^32 (x < rows_cap) or, with d <= 16, x < 2^28 (a 16-token group)
     float scale;               // in units of log2
@@ -368,21 +376,22 @@ __device__ __forceinline__ float across_groups_sum(float x) {
 }
 
 // One work-group: a piece of a request's tiles for one kv head and up to
-// 16 * row_tiles of its rows.  Wave w takes row tile w % row_tiles and the tiles
-// w / row_tiles + i * (4 / row_tiles) of the piece (waves that share a key tile
-// read it through the caches); the waves of a row tile join through LDS.
-template <bool Q8, int NB, bool NT>
-__global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(Cache c, Attn a) {
+// 16 RT * row_waves of its rows.  Wave w takes the RT row tiles of w % row_waves
+// and the tiles w / row_waves + i * (4 / row_waves) of the piece (waves that
+// share a key tile read it through the caches); the waves of a row tile join
+// through LDS.  With RT = 2 a tile's operands are made once for 32 rows.
+template <bool Q8, int NB, bool NT, int RT>
+__global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_kernel(Cache c, Attn a) {
     constexpr int D = 32 * NB, LD = D + 4;
-    // While the tiles go by, a wave's part holds its q limbs (operands as lanes read them), the blocks' sums of
-    // q and a tile's scales; at the
-    // end, [wave][16][LD] outputs, then [wave][16] (m, l).
-    constexpr int QB = NB * 2 * 1024, OB = Q8 ? NB * 256 : 0, SB = Q8 ? NB * 128 : 0, PART = QB + OB + SB;
-    constexpr int JOIN = 16 * (LD + 2) * 4;
+    // While the tiles go by: q's limbs (operands as lanes read them) and the sums of its blocks, of each wave, or (RT = 2)
+    // of each row tile, shared; and each wave's tile's scales.  At the end [wave][16][LD] outputs, then [wave][16] (m, l).
+    constexpr int QB = NB * 2 * 1024, QPART = QB + (Q8 ? NB * 256 : 0), SB = Q8 ? NB * 128 : 0;
+    constexpr int JOIN = 16 * (LD + 2) * 4, PART = QPART + SB;
+    static_assert(RT == 1 || RT == 2, "four row tiles' limbs in LDS");
     __shared__ __align__(16) uint8_t lds_[ATTN_WAVES * (PART > JOIN ? PART : JOIN)];
     float *lds = (float *)lds_;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int groups = (a.rows_cap + 16 * a.row_tiles - 1) / (16 * a.row_tiles);
+    const int wg_rows = 16 * RT * a.row_waves, groups = (a.rows_cap + wg_rows - 1) / wg_rows;
     // row groups of a piece (they read the same keys) lie 8 blocks apart: one L2
     const int head = blockIdx.y;
     int item = blockIdx.x, rgroup = 0;
@@ -399,47 +408,40 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(
     if (a.items > a.B && pc.index == 0 && head == 0 && rgroup == 0 && threadIdx.x == 0)
         a.info[pc.b] = int4{pc.whole, pc.last, pc.of, 0};
     const int rows = min(pc.r.n, a.max_q) * a.group;
-    const int row0 = rgroup * 16 * a.row_tiles;
+    const int row0 = rgroup * wg_rows;
     if (row0 >= rows) return;
 
-    const int rt = wave % a.row_tiles, kw = wave / a.row_tiles, kws = ATTN_WAVES / a.row_tiles;
+    const int rw = wave % a.row_waves, kw = wave / a.row_waves, kws = ATTN_WAVES / a.row_waves;
     const int m = lane & 15, g = lane >> 4;
-    const int r = row0 + 16 * rt + m, j = div_magic(r, a.group_magic), qh = head * a.group + (r - j * a.group);
-    const int64_t trow = (int64_t)pc.r.first + j;
-    const bool live = r < rows && trow >= 0 && trow < a.T;
-    // the row sees keys [lo, hi); hi_all and lo_all: keys that any row sees,
-    // hi_min and lo_max: that every row sees
+    // a row sees keys [lo, hi); hi_all and lo_all: keys that any row sees, hi_min and lo_max: that every row sees
     const int64_t room = attn_room(c, a);
     const int64_t pos0 = (int64_t)pc.r.ctx - pc.r.n;
     const int hi_all = (int)min((int64_t)pc.r.ctx, room);
     const int hi_min = (int)max(min(pos0 + 1, room), (int64_t)0);
     const int lo_all = a.window ? (int)max(pos0 - a.window + 1, (int64_t)0) : 0;
     const int lo_max = a.window ? (int)max((int64_t)pc.r.ctx - a.window, (int64_t)0) : 0;
-    const int hi = (int)max(min(pos0 + j + 1, room), (int64_t)0);
-    const int lo = a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0;
     if ((int64_t)pc.r.ctx > room && a.err && threadIdx.x == 0) a.err[0] = 1;
+    bool live[RT];
+    int hi[RT], lo[RT];
+    // the rows' q (the loads go out first, the limbs are made while the first tile's are on their way)
+    f4 x[RT][2 * NB];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        const int r = row0 + 16 * (rw * RT + i) + m, j = div_magic(r, a.group_magic), qh = head * a.group + (r - j * a.group);
+        const int64_t trow = (int64_t)pc.r.first + j;
+        live[i] = r < rows && trow >= 0 && trow < a.T;
+        hi[i] = (int)max(min(pos0 + j + 1, room), (int64_t)0);
+        lo[i] = a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0;
+        const float *qp = a.q + (live[i] ? trow * a.ldq + (int64_t)qh * D : 0) + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
+#pragma unroll
+        for (int s = 0; s < NB; ++s)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[i][2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
+    }
 
     const int t0 = pc.r.lo + (pc.index ? pc.index * chunk : 0);
     const int t1 = pc.index == pc.of - 1 ? pc.r.lo + pc.r.tiles : t0 + chunk;
     const int first = t0 + kw, N = first < t1 ? (t1 - first + kws - 1) / kws : 0;
-
-    // the row's q (its loads go out first, the limbs are made while the first tile's are on their way)
-    f4 x[2 * NB];
-    {
-        const float *qp = a.q + (live ? trow * a.ldq + (int64_t)qh * D : 0) + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
-#pragma unroll
-        for (int s = 0; s < NB; ++s)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                x[2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
-            }
-    }
-
-    f4 o[2 * NB];
-#pragma unroll
-    for (int n = 0; n < 2 * NB; ++n) o[n] = f4{0.f, 0.f, 0.f, 0.f};
-    float mx = NONE, l = 0.f;
-
     const u32 gp = c.page_tokens >> 4, quants = c.page_tokens * D;
     const uint8_t *kb = c.k + (u64)head * c.head_bytes, *vb = c.v + (u64)head * c.head_bytes;
     // Pages of 32 tiles of the wave: lane i holds group i % 2 of tile i / 2, page << 4 | group in page.  The next 32 tiles'
@@ -479,8 +481,8 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(
         w.ds = p1 + quants + (i1 & 15) * (NB * 32) - w.s0;
         return w;
     };
-    // V keys of lane (m, g) are in group g / 2; of the scales [K, V][group][block][16] a lane takes the
-    // 16 bytes at 16 * (lane % 8 NB)
+    // V keys of lane (m, g) are in group g / 2; of the scales [K, V][group][block][16] a lane takes the 16 bytes at
+    // 16 * (lane % 8 NB)
     const int sl = lane % (8 * NB);
     const uint8_t *sb = (sl / (4 * NB) ? vb : kb) + (sl % (2 * NB)) * 16;
     const bool second = (sl / (2 * NB)) & 1;
@@ -504,77 +506,95 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(
     }
     ask_ids(32);
 
-    // q as two fp16 limbs, in LDS: read again for every tile, they leave their registers to tiles on the way
-    uint8_t *part = lds_ + wave * PART;
-    float unscale;
-    {
+    // q as two fp16 limbs, in LDS: read again for every tile, they leave their registers to the tile on the way
+    auto part = [&](int i) { return lds_ + (RT == 1 ? wave : rw * RT + i) * QPART; };
+    float unscale[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < 2 * NB; ++s) {
-            x[s] *= live ? a.scale : 0.f;
+            x[i][s] *= live[i] ? a.scale : 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[s][i]));
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[i][s][k]));
         }
         top = across_groups_max(top);
         int ex = 0;
         if (top > 0.f && top < INFINITY) ex = min(10 - ilogbf(top), 120);
-        unscale = ldexpf(1.f, (Q8 ? 24 : 0) - ex);
+        unscale[i] = ldexpf(1.f, (Q8 ? 24 : 0) - ex);
 #pragma unroll
         for (int s = 0; s < NB; ++s) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[2 * s + e / 4][e % 4], ex);
-            h8 hi8, lo8;
-            limbs(y, &hi8, &lo8);
+            for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[i][2 * s + e / 4][e % 4], ex);
+            h8 qh, ql;
+            limbs(y, &qh, &ql);
+            float sum = 0.f;                     // Q8_0: -128 2^-24 times the sum of q's block
             if constexpr (Q8) {
-                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum += (float)hi8[e] + (float)lo8[e];
-                // -128 2^-24 times the sum of q's block
-                *(float *)(part + QB + s * 256 + lane * 4) = across_groups_sum(sum) * (-128.f / 16777216.f);
+                for (int e = 0; e < 8; ++e) sum += (float)qh[e] + (float)ql[e];
+                sum = across_groups_sum(sum) * (-128.f / 16777216.f);
             }
-            *(h8 *)(part + (2 * s) * 1024 + lane * 16) = hi8;
-            *(h8 *)(part + (2 * s + 1) * 1024 + lane * 16) = lo8;
+            if (RT == 1 || kw == 0) {
+                *(h8 *)(part(i) + (2 * s) * 1024 + lane * 16) = qh;
+                *(h8 *)(part(i) + (2 * s + 1) * 1024 + lane * 16) = ql;
+                if constexpr (Q8) *(float *)(part(i) + QB + s * 256 + lane * 4) = sum;
+            }
         }
     }
+    if (RT > 1) __syncthreads();
+
+    f4 o[RT][2 * NB];
+    float mx[RT], l[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+        mx[i] = NONE;
+        l[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k) o[i][k] = f4{0.f, 0.f, 0.f, 0.f};
+    }
+    uint8_t *scales = lds_ + ATTN_WAVES * QPART + wave * SB;
     u32 qat = (u32)lane * 16;
-    uint8_t *scales = part + QB + OB;
     for (int n = 0; n < N; ++n) {
         // (q's address is made anew for each tile, so that the reads stay here)
         asm volatile("" : "+v"(qat));
         if constexpr (Q8) *(h8 *)(scales + sl * 16) = T.s;
         // scores of the lane's 8 keys, times 1 / unscale
         order_k<Q8, NB>(T);
-        float s[8];
-        f4 d[2], d2[2];
+        f4 d[RT][2], d2[RT][2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) d[t] = d2[t] = f4{0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) d[i][t] = d2[i][t] = f4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const h8 qh8 = *(const h8 *)(part + (2 * b) * 1024 + qat), ql8 = *(const h8 *)(part + (2 * b + 1) * 1024 + qat);
-            if constexpr (Q8) {
-                const float off = *(const float *)(part + QB + b * 256 + (qat >> 2));
-                const h8 ks = *(const h8 *)(scales + ((g >> 1) * NB + b) * 32 + (g & 1) * 16);
+            h8 k[2], ks;
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8 k = biased_h8(T.k[t][2 * b], T.k[t][2 * b + 1]);
-                    const f4 y = mma(k, qh8, mma(k, ql8, f4{off, off, off, off}));
+            for (int t = 0; t < 2; ++t) {
+                if constexpr (Q8) k[t] = biased_h8(T.k[t][2 * b], T.k[t][2 * b + 1]);
+                else k[t] = __builtin_bit_cast(h8, u4{T.k[t][4 * b], T.k[t][4 * b + 1], T.k[t][4 * b + 2], T.k[t][4 * b + 3]});
+            }
+            if constexpr (Q8) ks = *(const h8 *)(scales + ((g >> 1) * NB + b) * 32 + (g & 1) * 16);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) d[t][i] = fmaf(y[i], (float)ks[4 * t + i], d[t][i]);
-                }
-            } else {
+            for (int i = 0; i < RT; ++i) {
+                const h8 qh = *(const h8 *)(part(i) + (2 * b) * 1024 + qat), ql = *(const h8 *)(part(i) + (2 * b + 1) * 1024 + qat);
+                if constexpr (Q8) {
+                    const float off = *(const float *)(part(i) + QB + b * 256 + (qat >> 2));
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    const h8 k = __builtin_bit_cast(h8, u4{T.k[t][4 * b], T.k[t][4 * b + 1], T.k[t][4 * b + 2], T.k[t][4 * b + 3]});
-                    d[t] = mma(k, qh8, d[t]);
-                    d2[t] = mma(k, ql8, d2[t]);
+                    for (int t = 0; t < 2; ++t) {
+                        const f4 y = mma(k[t], qh, mma(k[t], ql, f4{off, off, off, off}));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[i][t][e] = fmaf(y[e], (float)ks[4 * t + e], d[i][t][e]);
+                    }
+                } else {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        d[i][t] = mma(k[t], qh, d[i][t]);
+                        d2[i][t] = mma(k[t], ql, d2[i][t]);
+                    }
                 }
             }
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[4 * t + i] = Q8 ? d[t][i] : d[t][i] + d2[t][i];
         const u32 wrong = T.wrong;
         const int tile = first + kws * n;
         // the next tile's keys (behind the last, the last tile's again)
@@ -584,68 +604,66 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(
             ask_ids(nn + 32);
         }
         const Where next = where(nn);
+        // (the scales of this tile's values are read below: they are in LDS by now)
         get_k(next);
         T.wrong = wrong_of(nn);
         const bool edge = wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min;
-        uint32_t gone = 0;                       // keys of the lane that no row may touch
+        u32 gone = 0;                            // keys of the lane that no row may touch
         if (edge) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int key = tile * TILE + 8 * g + e;
-                const bool out = key >= hi_all || key < lo_all || ((wrong >> (g >> 1)) & 1);
-                gone |= (u32)out << e;
-                s[e] = out || key >= hi || key < lo ? -INFINITY : s[e];
+                gone |= (u32)(key >= hi_all || key < lo_all || ((wrong >> (g >> 1)) & 1)) << e;
             }
         }
-        [[maybe_unused]] h8 vs[Q8 ? NB : 1];
-        float top = s[0];
+        h8 ph[RT], pl[RT];
 #pragma unroll
-        for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
-        top *= unscale;
-        if constexpr (Q8) {
-            // weights are multiplied by the values' scales before they are rounded: m follows the product
+        for (int i = 0; i < RT; ++i) {
+            float s[8], p[8];
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
-                vs[b] = *(const h8 *)(scales + ((2 + (g >> 1)) * NB + b) * 32 + (g & 1) * 16);
+            for (int e = 0; e < 8; ++e) s[e] = Q8 ? d[i][e / 4][e % 4] : d[i][e / 4][e % 4] + d2[i][e / 4][e % 4];
             if (edge) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) vs[b][e] = (gone >> e) & 1 ? (_Float16)0 : vs[b][e];
+                for (int e = 0; e < 8; ++e) {
+                    const int key = tile * TILE + 8 * g + e;
+                    s[e] = ((gone >> e) & 1) || key >= hi[i] || key < lo[i] ? -INFINITY : s[e];
+                }
             }
-            us8 big = __builtin_bit_cast(us8, vs[0]);    // (scales are not negative: they order like integers)
+            float top = s[0];
 #pragma unroll
-            for (int b = 1; b < NB; ++b) big = __builtin_elementwise_max(big, __builtin_bit_cast(us8, vs[b]));
-            const us4 b4 = __builtin_elementwise_max(__builtin_shufflevector(big, big, 0, 1, 2, 3), __builtin_shufflevector(big, big, 4, 5, 6, 7));
-            const us2 b2 = __builtin_elementwise_max(__builtin_shufflevector(b4, b4, 0, 1), __builtin_shufflevector(b4, b4, 2, 3));
-            top += (float)__builtin_amdgcn_frexp_expf((float)__builtin_bit_cast(_Float16, b2[0] > b2[1] ? b2[0] : b2[1]));
-        }
-        if (__any(top > mx + SLACK)) {
-            const float now = fmaxf(mx, across_groups_max(top));
-            const float keep = __builtin_amdgcn_exp2f(mx - now);
-            mx = now;
-            l *= keep;
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, s[e]);
+            top *= unscale[i];
+            if (__any(top > mx[i] + SLACK)) {
+                const float now = fmaxf(mx[i], across_groups_max(top));
+                const float keep = __builtin_amdgcn_exp2f(mx[i] - now);
+                mx[i] = now;
+                l[i] *= keep;
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) o[k] *= keep;
-        }
-        float p[8];
+                for (int k = 0; k < 2 * NB; ++k) o[i][k] *= keep;
+            }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], unscale, LIFT - mx));
-            l += p[e];
+            for (int e = 0; e < 8; ++e) {
+                p[e] = __builtin_amdgcn_exp2f(fmaf(s[e], unscale[i], LIFT - mx[i]));
+                l[i] += p[e];
+            }
+            limbs(p, &ph[i], &pl[i]);
         }
         order_v<Q8, NB>(T);
         if constexpr (Q8) {
+            // scale times quant (19 bits, a multiple of 2^-24) is exactly a half and a half's remainder
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                float w[8];
+                h8 vs = *(const h8 *)(scales + ((2 + (g >> 1)) * NB + b) * 32 + (g & 1) * 16);
+                if (edge) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = fmaf(p[e], (float)vs[b][e], 0.f);   // (one operation on the half as it is)
-                h8 ph, pl;
-                limbs(w, &ph, &pl);
-                const h8 v0 = quants_h8(T.v[4 * b], T.v[4 * b + 1]), v1 = quants_h8(T.v[4 * b + 2], T.v[4 * b + 3]);
-                o[2 * b] = mma(v0, ph, mma(v0, pl, o[2 * b]));
-                o[2 * b + 1] = mma(v1, ph, mma(v1, pl, o[2 * b + 1]));
+                    for (int e = 0; e < 8; ++e) vs[e] = (gone >> e) & 1 ? (_Float16)0 : vs[e];
+                }
+#pragma unroll
+                for (int k = 2 * b; k < 2 * b + 2; ++k) {
+                    const h8 v = quants_h8(T.v[2 * k], T.v[2 * k + 1]), vh = v * vs, vl = __builtin_elementwise_fma(v, vs, -vh);
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) o[i][k] = mma(vh, ph[i], mma(vh, pl[i], mma(vl, ph[i], o[i][k])));
+                }
             }
         } else {
             if (edge) {
@@ -656,58 +674,62 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB)) void attn_kernel(
 #pragma unroll
                 for (int k = 0; k < 8 * NB; ++k) T.v[k] &= keep[k & 3];
             }
-            h8 ph, pl;
-            limbs(p, &ph, &pl);
             auto vop = [&](int k) { return __builtin_bit_cast(h8, u4{T.v[4 * k], T.v[4 * k + 1], T.v[4 * k + 2], T.v[4 * k + 3]}); };
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(vop(k), ph, o[k]);
+            for (int i = 0; i < RT; ++i) {
 #pragma unroll
-            for (int k = 0; k < 2 * NB; ++k) o[k] = mma(vop(k), pl, o[k]);
+                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(vop(k), ph[i], o[i][k]);
+#pragma unroll
+                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(vop(k), pl[i], o[i][k]);
+            }
         }
         get_v(next);
     }
-    l = across_groups_sum(l);
-    __syncthreads();                            // the q limbs' place is taken by what follows
 
     // join the waves of each row tile
     float *stat = lds + ATTN_WAVES * 16 * LD;
 #pragma unroll
-    for (int k = 0; k < 2 * NB; ++k) *(f4 *)(lds + (wave * 16 + m) * LD + 16 * k + 4 * g) = o[k];
-    if (g == 0) {
-        stat[(wave * 16 + m) * 2] = mx;
-        stat[(wave * 16 + m) * 2 + 1] = l;
-    }
-    __syncthreads();
-    const int todo = min(16 * a.row_tiles, rows - row0) * (D / 4);
-    for (int i = threadIdx.x; i < todo; i += ATTN_THREADS) {
-        const int rr = i / (D / 4), d = (i - rr * (D / 4)) * 4;
-        float M = NONE, L = 0.f, mw[ATTN_WAVES], lw[ATTN_WAVES];
-        f4 x = {0.f, 0.f, 0.f, 0.f}, y[ATTN_WAVES];
+    for (int i = 0; i < RT; ++i) {
+        __syncthreads();                         // the place is free (of q's limbs, or the row tiles before)
+        l[i] = across_groups_sum(l[i]);
 #pragma unroll
-        for (int w = 0; w < ATTN_WAVES; ++w) {           // (behind the last wave of the keys, the first one's with no weight)
-            const int at = ((w < kws ? w * a.row_tiles : 0) + (rr >> 4)) * 16 + (rr & 15);
-            mw[w] = w < kws ? stat[at * 2] : NONE;
-            lw[w] = stat[at * 2 + 1];
-            y[w] = *(const f4 *)(lds + at * LD + d);
-            M = fmaxf(M, mw[w]);
+        for (int k = 0; k < 2 * NB; ++k) *(f4 *)(lds + (wave * 16 + m) * LD + 16 * k + 4 * g) = o[i][k];
+        if (g == 0) {
+            stat[(wave * 16 + m) * 2] = mx[i];
+            stat[(wave * 16 + m) * 2 + 1] = l[i];
         }
+        __syncthreads();
+        for (int k = threadIdx.x; k < 16 * a.row_waves * (D / 4); k += ATTN_THREADS) {
+            const int rr = k / (D / 4), d = (k - rr * (D / 4)) * 4;
+            const int row = row0 + 16 * ((rr >> 4) * RT + i) + (rr & 15);
+            if (row >= rows) continue;
+            float M = NONE, L = 0.f, mw[ATTN_WAVES], lw[ATTN_WAVES];
+            f4 x = {0.f, 0.f, 0.f, 0.f}, y[ATTN_WAVES];
 #pragma unroll
-        for (int w = 0; w < ATTN_WAVES; ++w) {
-            const float f = w < kws ? __builtin_amdgcn_exp2f(mw[w] - M) : 0.f;
-            L = fmaf(f, lw[w], L);
-            x += w < kws ? f * y[w] : f4{0.f, 0.f, 0.f, 0.f};
-        }
-        const int row = row0 + rr;
-        if (pc.of == 1) {
-            const int jj = div_magic(row, a.group_magic);
-            const int64_t to = (int64_t)pc.r.first + jj;
-            if (to >= 0 && to < a.T)
-                *(f4 *)(a.out + to * a.ldo + (int64_t)(head * a.group + row - jj * a.group) * D + d) =
-                    L == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : x * (1.f / L);
-        } else {
-            const int64_t at = ((int64_t)item * c.kv_heads + head) * a.rows_cap + row;
-            *(f4 *)(a.part + at * LD + d) = x;
-            if (d == 0) *(f4 *)(a.part + at * LD + D) = f4{M, L, 0.f, 0.f};
+            for (int w = 0; w < ATTN_WAVES; ++w) {       // (behind the last wave of the keys, the first one's with no weight)
+                const int at = ((w < kws ? w * a.row_waves : 0) + (rr >> 4)) * 16 + (rr & 15);
+                mw[w] = w < kws ? stat[at * 2] : NONE;
+                lw[w] = stat[at * 2 + 1];
+                y[w] = *(const f4 *)(lds + at * LD + d);
+                M = fmaxf(M, mw[w]);
+            }
+#pragma unroll
+            for (int w = 0; w < ATTN_WAVES; ++w) {
+                const float f = w < kws ? __builtin_amdgcn_exp2f(mw[w] - M) : 0.f;
+                L = fmaf(f, lw[w], L);
+                x += w < kws ? f * y[w] : f4{0.f, 0.f, 0.f, 0.f};
+            }
+            if (pc.of == 1) {
+                const int j = div_magic(row, a.group_magic);
+                const int64_t to = (int64_t)pc.r.first + j;
+                if (to >= 0 && to < a.T)
+                    *(f4 *)(a.out + to * a.ldo + (int64_t)(head * a.group + row - j * a.group) * D + d) =
+                        L == 0.f ? f4{0.f, 0.f, 0.f, 0.f} : x * (1.f / L);
+            } else {
+                const int64_t at = ((int64_t)item * c.kv_heads + head) * a.rows_cap + row;
+                *(f4 *)(a.part + at * LD + d) = x;
+                if (d == 0) *(f4 *)(a.part + at * LD + D) = f4{M, L, 0.f, 0.f};
+            }
         }
     }
 }
@@ -774,7 +796,7 @@ __global__ __launch_bounds__(THREADS) void attn_join_kernel(Cache c, Attn a) {
     }
 }
 
-template <int NB> int launch_attn(bool q8, bool nt, const Cache &c, const Attn &a, hipStream_t st);
+template <int NB> int launch_attn(bool q8, bool nt, int rt, const Cache &c, const Attn &a, hipStream_t st);
 
 } // namespace kv
 } // namespace kq

@@ -15,30 +15,37 @@ using namespace kq::kv;
 // requests of up to 32768 Q8_0 tokens 354 -> 321; one of 512, kept, 12.5 -> 14.2).
 constexpr double KEPT_BYTES = 256e6;
 
-// The split of a call.
-//  * row_tiles: 16-row tiles per work-group, 1, 2 or 4: its four waves share the rows first, then the keys.
+// The split of a call.  Returns the row tiles a wave.
+//  * Rows: up to 16 are one row tile; more, two tiles a wave (heads of up to 128) and up to 64 rows a work-group, whose
+//    four waves share the rows first, then the keys (8 rows of 8 requests of 4096 fp16 tokens: one tile a wave 61 us, two
+//    48).
 //  * A piece has at least min_tiles tiles.  A work-group costs about 6 us beside its tiles (a chain of dependent loads,
 //    the join of its waves) and a cut one its share of a second launch, so where requests and heads alone make a
 //    work-group per compute unit, only long contexts are cut (32 requests of 1024 tokens: not cut 28 us, cut in two 37),
 //    and where they do not, contexts past 8 tiles are cut finely (one request of 1024 tokens: not cut 15.4 us, pieces
 //    of 8 tiles 11.5, of 4 10.2).
-//  * As many pieces as work-groups run at once (3 on each of 256 compute units; more of them cost one long request 5 to
-//    25 %), and up to four times that for large batches, 64 tiles a piece, where they even out the requests' lengths (64
-//    requests of up to 32768: 760 pieces 354 us, 3040 315).
-static void attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, int window, Attn *a) {
+//  * Where it leaves each request two pieces or more on average, as many pieces as work-groups run at once and no more
+//    (3 on each of 256 compute units, by their registers; 32 requests of up to 8192 tokens: 69 us, with 30 % more 73).
+//    Larger batches take up to four times that, 64 tiles a piece, so that the requests' lengths even out (64 requests
+//    of up to 32768: 760 pieces 354 us, 3040 315).
+static int attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, int window, Attn *a) {
     a->group = q_heads / c->kv_heads;
     a->rows_cap = a->group * max_q;
-    a->row_tiles = a->rows_cap <= 16 ? 1 : a->rows_cap <= 32 ? 2 : 4;
+    const int rt = a->rows_cap <= 16 || c->head_dim > 32 * TWO_TILES_NB ? 1 : 2;
+    a->row_waves = a->rows_cap <= 16 * rt ? 1 : rt == 2 || a->rows_cap <= 32 ? 2 : 4;
     auto magic = [](int d) { return d == 1 ? 0u : (u32)(((1ull << 32) + d - 1) / d); };
     a->group_magic = magic(a->group);
     a->gp_magic = magic(c->page_tokens / 16);
-    const int groups = (a->rows_cap + 16 * a->row_tiles - 1) / (16 * a->row_tiles);
+    const int wg_rows = 16 * rt * a->row_waves, groups = (a->rows_cap + wg_rows - 1) / wg_rows;
     if (window) max_ctx = std::min<int64_t>(max_ctx, (int64_t)window + max_q + 2 * TILE);
     const int64_t tiles = (max_ctx + TILE - 1) / TILE, base = (int64_t)B * c->kv_heads * groups;
     a->min_tiles = base < 32 ? 4 : base < 256 ? 8 : 32;
-    const int64_t pieces = std::max<int64_t>(760, std::min<int64_t>(base * tiles / 64, 3040));
+    const int64_t each = (int64_t)c->kv_heads * groups, at_once = 256 * ATTN_OCCUPANCY(c->head_dim / 32, rt);
     const int64_t most = tiles <= std::max(8, a->min_tiles * 9 / 8) ? B : B * ((tiles + a->min_tiles - 1) / a->min_tiles);
-    a->items = (int)std::min<int64_t>(most, B + std::max<int64_t>(1, pieces / (c->kv_heads * groups)));
+    const int64_t items = at_once / each >= 2 * B ? at_once / each
+                                                  : B + std::max<int64_t>(1, std::max(at_once, std::min(base * tiles / 64, 4 * at_once)) / each);
+    a->items = (int)std::min(most, items);
+    return rt;
 }
 
 // The pieces' unnormalised outputs with their m and l, then the requests'
@@ -85,7 +92,7 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     if (workspace_bytes < ws) return KQ_ERR_SHAPE;
     if (device_check()) return KQ_ERR_DEVICE;
     Attn a;
-    attn_split(cache, B, max_q, max_ctx, q_heads, window, &a);
+    const int rt = attn_split(cache, B, max_q, max_ctx, q_heads, window, &a);
     a.ctx_len = ctx_len;
     a.seq_start = seq_start;
     a.table = table;
@@ -104,17 +111,17 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     a.scale = (float)(scale * 1.4426950408889634);
     const bool q8 = cache->type == KQKV_Q8_0;
     const Cache c = cache_args(cache);
-    const bool nt = a.row_tiles == 1 && (double)B * max_ctx * 2 * c.page_bytes / c.page_tokens > KEPT_BYTES;
+    const bool nt = rt == 1 && a.row_waves == 1 && (double)B * max_ctx * 2 * c.page_bytes / c.page_tokens > KEPT_BYTES;
     hipStream_t st = (hipStream_t)stream;
     switch (cache->head_dim / 32) {
-    case 1: return launch_attn<1>(q8, nt, c, a, st);
-    case 2: return launch_attn<2>(q8, nt, c, a, st);
-    case 3: return launch_attn<3>(q8, nt, c, a, st);
-    case 4: return launch_attn<4>(q8, nt, c, a, st);
-    case 5: return launch_attn<5>(q8, nt, c, a, st);
-    case 6: return launch_attn<6>(q8, nt, c, a, st);
-    case 7: return launch_attn<7>(q8, nt, c, a, st);
-    default: return launch_attn<8>(q8, nt, c, a, st);
+    case 1: return launch_attn<1>(q8, nt, rt, c, a, st);
+    case 2: return launch_attn<2>(q8, nt, rt, c, a, st);
+    case 3: return launch_attn<3>(q8, nt, rt, c, a, st);
+    case 4: return launch_attn<4>(q8, nt, rt, c, a, st);
+    case 5: return launch_attn<5>(q8, nt, rt, c, a, st);
+    case 6: return launch_attn<6>(q8, nt, rt, c, a, st);
+    case 7: return launch_attn<7>(q8, nt, rt, c, a, st);
+    default: return launch_attn<8>(q8, nt, rt, c, a, st);
     }
 }
 

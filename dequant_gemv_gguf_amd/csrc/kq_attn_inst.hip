@@ -4,10 +4,13 @@
 namespace kq {
 namespace kv {
 
-template <int NB> int launch_attn(bool q8, bool nt, const Cache &c, const Attn &a, hipStream_t st) {
-    const int groups = (a.rows_cap + 16 * a.row_tiles - 1) / (16 * a.row_tiles);
-    void (*kern)(Cache, Attn) = q8 ? (nt ? attn_kernel<true, NB, true> : attn_kernel<true, NB, false>)
-                                   : (nt ? attn_kernel<false, NB, true> : attn_kernel<false, NB, false>);
+template <int NB> int launch_attn(bool q8, bool nt, int rt, const Cache &c, const Attn &a, hipStream_t st) {
+    const int wg_rows = 16 * rt * a.row_waves, groups = (a.rows_cap + wg_rows - 1) / wg_rows;
+    void (*kern)(Cache, Attn) = q8 ? (nt ? attn_kernel<true, NB, true, 1> : attn_kernel<true, NB, false, 1>)
+                                   : (nt ? attn_kernel<false, NB, true, 1> : attn_kernel<false, NB, false, 1>);
+    if constexpr (NB <= TWO_TILES_NB) {
+        if (rt == 2) kern = q8 ? attn_kernel<true, NB, false, 2> : attn_kernel<false, NB, false, 2>;
+    }
     const unsigned pieces = groups == 1 ? (unsigned)a.items : (unsigned)((a.items + 7) / 8 * 8 * groups);
     hipLaunchKernelGGL(kern, dim3(pieces, (unsigned)c.kv_heads), dim3(ATTN_THREADS), 0, st, c, a);
     if (a.items > a.B) {
@@ -21,7 +24,7 @@ template <int NB> int launch_attn(bool q8, bool nt, const Cache &c, const Attn &
     return launched();
 }
 
-template int launch_attn<KQ_ATTN_NB>(bool, bool, const Cache &, const Attn &, hipStream_t);
+template int launch_attn<KQ_ATTN_NB>(bool, bool, int, const Cache &, const Attn &, hipStream_t);
 
 } // namespace kv
 } // namespace kq
