@@ -28,14 +28,22 @@ class GGUFTensor(ctypes.Structure):
 
 
 class KVCache(ctypes.Structure):
-    """struct kqkv_cache (include/kqkv.h).  k and v: tensors (kept alive by
-    this object) or int addresses."""
+    """struct kqkv_cache (include/kqkv.h).  k and v: contiguous device tensors of
+    at least n_pages * kqkv_page_bytes bytes (kept alive by this object), or int
+    addresses."""
     _fields_ = [("type", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("page_tokens", ctypes.c_int), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p)]
 
     def __init__(self, type, kv_heads, head_dim, page_tokens, n_pages, k, v):
         super().__init__(int(type), int(kv_heads), int(head_dim), int(page_tokens), int(n_pages), _addr(k), _addr(v))
+        page = lib().kqkv_page_bytes(int(type), int(kv_heads), int(head_dim), int(page_tokens))
+        for t in (k, v):
+            if t is None or isinstance(t, int) or page < 0:
+                continue
+            if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < page * int(n_pages):
+                raise ValueError("KVCache: k and v must be contiguous device tensors of at least %d bytes" %
+                                 (page * int(n_pages)))
         self.tensors = (k, v)
         self.ref = ctypes.byref(self)
 
@@ -51,6 +59,10 @@ class KVRope(ctypes.Structure):
         sections = [int(rot_dims) // 2] if sections is None else [int(n) for n in sections]
         padded = (ctypes.c_int * 4)(*sections[:4])
         super().__init__(int(style), int(rot_dims), float(base), len(sections), padded, _addr(freq_factors))
+        if freq_factors is not None and not isinstance(freq_factors, int):
+            f = freq_factors
+            if not f.is_cuda or not f.is_contiguous() or f.element_size() != 4 or f.numel() < int(rot_dims) // 2:
+                raise ValueError("KVRope: freq_factors must be rot_dims / 2 contiguous fp32 values on the device")
         self.tensors = (freq_factors,)
         self.ref = ctypes.byref(self)
 
@@ -401,7 +413,9 @@ def _device_call(fn, like, stream, *args):
     global _torch_c
     f = getattr(_lib or lib(), fn)
     if stream is None:
-        if like is not None and type(like) is not int and like.is_cuda:
+        if like is not None and type(like) is not int:
+            if not like.is_cuda:
+                raise ValueError("%s: tensors must be on the device" % fn)
             if _torch_c is None:
                 import torch
                 _torch_c = torch._C

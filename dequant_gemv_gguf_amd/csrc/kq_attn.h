@@ -441,7 +441,9 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
 
     const int t0 = pc.r.lo + (pc.index ? pc.index * chunk : 0);
     const int t1 = pc.index == pc.of - 1 ? pc.r.lo + pc.r.tiles : t0 + chunk;
-    const int first = t0 + kw, N = first < t1 ? (t1 - first + kws - 1) / kws : 0;
+    const int first = t0 + kw;
+    // (a wave whose rows the request does not have takes no tiles)
+    const int N = first < t1 && row0 + 16 * RT * rw < rows ? (t1 - first + kws - 1) / kws : 0;
     const u32 gp = c.page_tokens >> 4, quants = c.page_tokens * D;
     const uint8_t *kb = c.k + (u64)head * c.head_bytes, *vb = c.v + (u64)head * c.head_bytes;
     // Pages of 32 tiles of the wave: lane i holds group i % 2 of tile i / 2, page << 4 | group in page.  The next 32 tiles'

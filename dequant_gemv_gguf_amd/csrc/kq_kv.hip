@@ -10,14 +10,15 @@ namespace kv {
 // ---------------------------------------------------------------------------
 // Plan
 //
-// Bound: latency.  One work-group holds up to 1024 requests, one a thread:
+// Bound: latency.  One work-group holds up to 1024 requests (256 where that
+// suffices, and few rows: its barriers are shorter, 16 requests and rows 5.2 ->
+// 4.4 us, but 3600 pages for 256 requests 6.9 -> 14.9), one a thread:
 // prefix sums of the new tokens and of the pages taken and given back, then a
 // thread per page and per row, which find their request by bisection in LDS.
 // Few rows are filled in by the same work-group, from the free list and the
 // table as they were, beside the writes; many by a second launch.
 
-constexpr int PLAN_THREADS = 1024;
-constexpr int PLAN_WAVES = PLAN_THREADS / 64;
+constexpr int PLAN_THREADS = 1024, PLAN_FEW = 256;
 constexpr int ROW_THREADS = 256, ROW_STARTS = 4096;
 
 struct Plan {
@@ -80,15 +81,15 @@ template <bool ROWS_ONLY> __device__ __forceinline__ int scan(int x) {
 // the total.  A wave's sum stays below 2^30, the total is held in 64 bits (where
 // it passes 31, the step fails and the exclusive sums are not used).
 struct Sum { int before; int64_t total; };
-__device__ __forceinline__ Sum block_sum(int x, int scanned, const int *waves, int wave) {
-    const int lane = threadIdx.x & 63, w = waves[lane & 15];
+template <int WAVES> __device__ __forceinline__ Sum block_sum(int x, int scanned, const int *waves, int wave) {
+    const int lane = threadIdx.x & 63, w = (lane & 15) < WAVES ? waves[lane & (WAVES - 1)] : 0;
     const int s = scan<true>(w);
     const int64_t total = ((int64_t)__builtin_amdgcn_readlane(scan<true>(w >> 16), 15) << 16) +
                           __builtin_amdgcn_readlane(scan<true>(w & 0xFFFF), 15);
     return Sum{__builtin_amdgcn_readlane(s - w, wave) + scanned - x, total};
 }
 struct Sums { Sum fresh, need, gone; };
-__device__ __forceinline__ Sums block_sums(const Req &r, int (*waves)[PLAN_WAVES]) {
+template <int WAVES> __device__ __forceinline__ Sums block_sums(const Req &r, int (*waves)[WAVES]) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int f = scan<false>(r.fresh), n = scan<false>(r.need), g = scan<false>(r.gone);
     __syncthreads();                              // the last use of `waves` is over
@@ -98,8 +99,8 @@ __device__ __forceinline__ Sums block_sums(const Req &r, int (*waves)[PLAN_WAVES
         waves[2][wave] = g;
     }
     __syncthreads();
-    return Sums{block_sum(r.fresh, f, waves[0], wave), block_sum(r.need, n, waves[1], wave),
-                block_sum(r.gone, g, waves[2], wave)};
+    return Sums{block_sum<WAVES>(r.fresh, f, waves[0], wave), block_sum<WAVES>(r.need, n, waves[1], wave),
+                block_sum<WAVES>(r.gone, g, waves[2], wave)};
 }
 
 // Last index b in [0, n) with first[b] <= i (first ascending, first[0] <= i).
@@ -116,18 +117,19 @@ __device__ __forceinline__ int slot_of(const Plan &p, u32 id, u32 pos, u32 page)
     return id < (u32)p.n_pages ? (int)(id * p.P + (pos - page * (u32)p.P)) : -1;
 }
 
-__global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
-    __shared__ int waves[3][PLAN_WAVES];
-    __shared__ int first[PLAN_THREADS], first_need[PLAN_THREADS], after[PLAN_THREADS], had[PLAN_THREADS];
+template <int THREADS>
+__global__ __launch_bounds__(THREADS) void plan_kernel(Plan p, int rows) {
+    __shared__ int waves[3][THREADS / 64];
+    __shared__ int first[THREADS], first_need[THREADS], after[THREADS], had[THREADS];
     const int tid = threadIdx.x;
-    const bool one = p.B <= PLAN_THREADS;
+    const bool one = p.B <= THREADS;
     const int n_free = p.n_free[0];
     // totals, before anything is written
     Req r = plan_req(p, tid);
     bool bad = r.bad;
     Sums s = block_sums(r, waves);
     int64_t fresh = s.fresh.total, need = s.need.total, gone = s.gone.total;
-    for (int b0 = PLAN_THREADS; b0 < p.B; b0 += PLAN_THREADS) {
+    for (int b0 = THREADS; b0 < p.B; b0 += THREADS) {
         const Req o = plan_req(p, b0 + tid);
         bad = bad || o.bad;
         const Sums t = block_sums(o, waves);
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
     const int64_t top = n_free + gone;
     const bool ok = !__syncthreads_or(bad) && n_free >= 0 && top <= p.n_pages && need <= top && fresh <= p.T;
     if (!ok) {
-        for (int b = tid; b < p.B; b += PLAN_THREADS) {
+        for (int b = tid; b < p.B; b += THREADS) {
             p.seq_start[b] = 0;
             p.held_out[b] = p.held[b];
             p.ctx_out[b] = p.ctx_len[b];
@@ -148,7 +150,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
             p.n_free_out[0] = n_free;
             if (p.err) p.err[0] = 1;
         }
-        for (int t = tid; rows && t < p.T; t += PLAN_THREADS) {
+        for (int t = tid; rows && t < p.T; t += THREADS) {
             p.slots[t] = -1;
             p.pos[t] = 0;
         }
@@ -157,15 +159,15 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
     // the ended requests' pages go on the list before any are taken from it
     if (gone) {
         int64_t done = n_free;
-        for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+        for (int b0 = 0; b0 < p.B; b0 += THREADS) {
             if (!one) {
                 r = plan_req(p, b0 + tid);
                 s = block_sums(r, waves);
             }
             first[tid] = s.gone.before;
             __syncthreads();
-            const int n = min(p.B - b0, PLAN_THREADS);
-            for (int i = tid; i < (int)s.gone.total; i += PLAN_THREADS) {
+            const int n = min(p.B - b0, THREADS);
+            for (int i = tid; i < (int)s.gone.total; i += THREADS) {
                 const int b = last_not_after(first, n, i);
                 p.free_pages[done + i] = p.table[(int64_t)(b0 + b) * p.stride + (i - first[b])];
             }
@@ -175,7 +177,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
         __threadfence_block();
     }
     int tokens = 0, taken = 0;
-    for (int b0 = 0; b0 < p.B; b0 += PLAN_THREADS) {
+    for (int b0 = 0; b0 < p.B; b0 += THREADS) {
         if (!one) {
             r = plan_req(p, b0 + tid);
             s = block_sums(r, waves);
@@ -185,10 +187,10 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
         after[tid] = r.after;
         had[tid] = r.held;
         __syncthreads();
-        const int n = min(p.B - b0, PLAN_THREADS), b = b0 + tid;
+        const int n = min(p.B - b0, THREADS), b = b0 + tid;
         auto new_page = [&](int i) { return p.free_pages[top - 1 - (taken + i)]; };
         // rows (only where one chunk holds every request): their pages from the list and the table as they were
-        for (int t = tid; rows && t < p.T; t += PLAN_THREADS) {
+        for (int t = tid; rows && t < p.T; t += THREADS) {
             int pos = 0, slot = -1;
             if (t < (int)fresh) {
                 const int c = last_not_after(first, n, t);
@@ -201,7 +203,7 @@ __global__ __launch_bounds__(PLAN_THREADS) void plan_kernel(Plan p, int rows) {
             p.pos[t] = pos;
             p.slots[t] = slot;
         }
-        for (int i = tid; i < (int)s.need.total; i += PLAN_THREADS) {
+        for (int i = tid; i < (int)s.need.total; i += THREADS) {
             const int c = last_not_after(first_need, n, i);
             p.table[(int64_t)(b0 + c) * p.stride + had[c] + (i - first_need[c])] = new_page(i);
         }
@@ -608,7 +610,10 @@ int kqkv_plan(int B, const int32_t *ctx_len, const int32_t *new_len, int page_to
     hipStream_t st = (hipStream_t)stream;
     // a work-group alone fills in 4 rows a thread as fast as a second launch begins
     const bool apart = T > 4 * PLAN_THREADS || B > PLAN_THREADS;
-    hipLaunchKernelGGL(plan_kernel, dim3(1), dim3(PLAN_THREADS), 0, st, p, apart ? 0 : 1);
+    if (B <= PLAN_FEW && T <= 4 * PLAN_FEW)
+        hipLaunchKernelGGL(plan_kernel<PLAN_FEW>, dim3(1), dim3(PLAN_FEW), 0, st, p, apart ? 0 : 1);
+    else
+        hipLaunchKernelGGL(plan_kernel<PLAN_THREADS>, dim3(1), dim3(PLAN_THREADS), 0, st, p, apart ? 0 : 1);
     if (apart && T)
         hipLaunchKernelGGL(plan_rows_kernel, dim3((unsigned)((T + ROW_THREADS - 1) / ROW_THREADS)), dim3(ROW_THREADS), 0, st, p);
     return launched();

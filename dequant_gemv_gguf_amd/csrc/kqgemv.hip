@@ -6,7 +6,7 @@
 
 #include <cstring>
 
-#define KQ_VERSION 10000
+#define KQ_VERSION 10100
 
 namespace kq {
 

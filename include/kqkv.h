@@ -37,8 +37,8 @@
  * call can be captured into a graph; what a replay computes follows the
  * contents of the device arrays at that time.  Calls on different streams run
  * side by side when they write different memory (each needs its own
- * workspace).  Results do not depend on timing (no atomics), except where two
- * rows of one call name the same slot.  All int32 arrays 4-byte aligned;
+ * workspace).  Results do not depend on timing, except where two rows of one call
+ * name the same slot.  All int32 arrays 4-byte aligned;
  * fp32 rows 16-byte aligned with strides that are multiples of 4 floats.
  *
  * Device-side checks.  Lengths, pages and slots are read on the device only.

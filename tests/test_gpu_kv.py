@@ -82,7 +82,7 @@ def same_plan(got, want):
 @pytest.mark.parametrize("in_place", [False, True])
 @pytest.mark.parametrize("B,page,max_ctx,most", [(1, 16, 0, 1), (1, 16, 100, 1), (3, 48, 50, 8), (17, 16, 300, 1),
                                                  (64, 32, 1000, 200), (1000, 64, 200, 3), (1024, 16, 40, 5),
-                                                 (1025, 16, 40, 1), (2500, 32, 100, 9)])
+                                                 (1025, 16, 40, 1), (2500, 32, 100, 9), (5000, 16, 20, 2)])
 def test_plan(B, page, max_ctx, most, in_place):
     rng = np.random.default_rng(B + most)
     stride = -(-(max_ctx + most) // page) + 2
@@ -259,6 +259,16 @@ def test_rope_store(type, T, q_heads, kv_heads, dim, page, style, rot, sections,
                 ref.put(slots[t], kr[t], vn[t])
         assert np.array_equal(kb.cpu().numpy(), ref.k)
         assert np.array_equal(vb.cpu().numpy(), ref.v)
+
+
+@pytest.mark.parametrize("type", [F16, Q8])
+def test_binding_refuses_short_buffers(type):
+    n = kq.kqkv_page_bytes(type, 2, 64, 16)
+    t = torch.zeros(3 * n, dtype=torch.uint8, device="cuda")
+    kq.KVCache(type, 2, 64, 16, 3, t, t)
+    for k, v in ((t[:-1], t), (t, t[:-1]), (torch.zeros(3 * n, 2, dtype=torch.uint8, device="cuda")[:, 0], t)):
+        with pytest.raises(ValueError):
+            kq.KVCache(type, 2, 64, 16, 3, k, v)
 
 
 @pytest.mark.parametrize("type", [F16, Q8])

@@ -142,6 +142,20 @@ def test_workspace_bytes_of_invalid_sizes():
     assert f(cache(), 4, 1, 0, 32) == f(cache(), 4, 1, 4096, 30) == 0
 
 
+def test_binding_refuses_host_tensors():
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(1 << 20, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        kq.KVCache(1, 1, 32, 16, 2, t, t)
+    with pytest.raises(ValueError):
+        kq.KVRope(0, 32, 1e4, None, torch.ones(16))
+    i = torch.zeros(8, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        kq.kqkv_plan(1, i, i, 16, i, 1, i, i, i, 1, i, i, 1, i, i, i, i)
+    with pytest.raises(ValueError):
+        kq.kqkv_attn(cache(), 1, 1, 16, FAKE, FAKE, FAKE, 1, 8, 1, torch.zeros(1, 1024), 1024, 1.0, 0, FAKE, 1024, FAKE, 1 << 30)
+
+
 def test_reference_quantises_to_the_nearest_multiple():
     # every quant within half a step, and the layout's indexes a bijection
     rng = np.random.default_rng(3)
