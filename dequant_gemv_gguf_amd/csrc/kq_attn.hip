@@ -8,8 +8,6 @@
 using namespace kq;
 using namespace kq::kv;
 
-// Work-groups that the requests' tokens are cut into (beside one per request
-// and kv head), and the fewest tiles of such a piece.
 // Contexts past this may not be kept by the last-level cache: where no two work-groups or waves share a line (up to 16
 // rows a kv head), lines are then read with the non-temporal hint (one request of 131072 fp16 tokens 110 -> 102 us, 64
 // requests of up to 32768 Q8_0 tokens 354 -> 321; one of 512, kept, 12.5 -> 14.2).
@@ -111,7 +109,8 @@ int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const 
     a.scale = (float)(scale * 1.4426950408889634);
     const bool q8 = cache->type == KQKV_Q8_0;
     const Cache c = cache_args(cache);
-    const bool nt = rt == 1 && a.row_waves == 1 && (double)B * max_ctx * 2 * c.page_bytes / c.page_tokens > KEPT_BYTES;
+    const int64_t seen = window ? std::min<int64_t>(max_ctx, (int64_t)window + max_q) : max_ctx;
+    const bool nt = rt == 1 && a.row_waves == 1 && (double)B * seen * 2 * c.page_bytes / c.page_tokens > KEPT_BYTES;
     hipStream_t st = (hipStream_t)stream;
     switch (cache->head_dim / 32) {
     case 1: return launch_attn<1>(q8, nt, rt, c, a, st);
