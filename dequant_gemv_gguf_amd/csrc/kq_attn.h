@@ -554,7 +554,11 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     }
     uint8_t *scales = lds_ + ATTN_WAVES * QPART + wave * SB;
     u32 qat = (u32)lane * 16;
-    for (int n = 0; n < N; ++n) {
+    // One tile, while the next one's keys and values are asked for.  The last tile is a copy of its own, without these
+    // loads: asked for and not used, the barrier behind the loop would wait for them (under a condition, the waits for
+    // this tile's values would wait for the next one's keys).
+    auto step = [&](int n, auto more) __attribute__((always_inline)) {
+        constexpr bool MORE = decltype(more)::value;
         // (q's address is made anew for each tile, so that the reads stay here)
         asm volatile("" : "+v"(qat));
         if constexpr (Q8) *(h8 *)(scales + sl * 16) = T.s;
@@ -596,16 +600,16 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
         }
         const u32 wrong = T.wrong;
         const int tile = first + kws * n;
-        // the next tile's keys (behind the last, the last tile's again)
-        const int nn = min(n + 1, N - 1);
-        if (nn > n && (nn & 31) == 0) {
-            take_ids(nn);
-            ask_ids(nn + 32);
+        Where next;
+        if constexpr (MORE) {
+            if (((n + 1) & 31) == 0) {
+                take_ids(n + 1);
+                ask_ids(n + 33);
+            }
+            next = where(n + 1);
+            get_k(next);
+            T.wrong = wrong_of(n + 1);
         }
-        const Where next = where(nn);
-        // (the scales of this tile's values are read below: they are in LDS by now)
-        get_k(next);
-        T.wrong = wrong_of(nn);
         const bool edge = wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min;
         u32 gone = 0;                            // keys of the lane that no row may touch
         if (edge) {
@@ -682,8 +686,10 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
                 for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(vop(k), pl[i], o[i][k]);
             }
         }
-        get_v(next);
-    }
+        if constexpr (MORE) get_v(next);
+    };
+    for (int n = 0; n + 1 < N; ++n) step(n, std::true_type());
+    if (N > 0) step(N - 1, std::false_type());
 
     // join the waves of each row tile
     float *stat = lds + ATTN_WAVES * 16 * LD;
