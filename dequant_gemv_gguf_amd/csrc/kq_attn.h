@@ -667,6 +667,7 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
 #pragma unroll
                     for (int i = 0; i < RT; ++i) o[i][k] = mma(vh, ph[i], mma(vh, pl[i], mma(vl, ph[i], o[i][k])));
                 }
+                __builtin_amdgcn_sched_barrier(0);      // (blocks taken further ahead of each other cost registers to scratch)
             }
         } else {
             if (edge) {
