@@ -10,7 +10,7 @@ using namespace kq::kv;
 
 // Contexts past this may not be kept by the last-level cache: where no two work-groups or waves share a line (up to 16
 // rows a kv head), lines are then read with the non-temporal hint (one request of 131072 fp16 tokens 110 -> 102 us, 64
-// requests of up to 32768 Q8_0 tokens 354 -> 321; one of 512, kept, 12.5 -> 14.2).
+// requests of up to 32768 Q8_0 tokens 354 -> 321; one of 512, kept, 12.5 -> 14.2; all before the last steps).
 constexpr double KEPT_BYTES = 256e6;
 
 // The split of a call.  Returns the row tiles a wave.
@@ -18,10 +18,11 @@ constexpr double KEPT_BYTES = 256e6;
 //    four waves share the rows first, then the keys (8 rows of 8 requests of 4096 fp16 tokens: one tile a wave 61 us, two
 //    48).
 //  * A piece has at least min_tiles tiles.  A work-group costs about 6 us beside its tiles (a chain of dependent loads,
-//    the join of its waves) and a cut one its share of a second launch, so where requests and heads alone make a
-//    work-group per compute unit, only long contexts are cut (32 requests of 1024 tokens: not cut 28 us, cut in two 37),
-//    and where they do not, contexts past 8 tiles are cut finely (one request of 1024 tokens: not cut 15.4 us, pieces
-//    of 8 tiles 11.5, of 4 10.2).
+//    the join of its waves) and a cut one its share of a second launch, so contexts are cut past 16 tiles where there
+//    are few work-groups (8 where a tile is heavy), past 48 where requests and heads alone make one per compute unit.
+//    Uncut against cut, fp16, 64 query and 8 kv heads of 128: one request of 512 tokens 8.8 us against 10.1, of 1024
+//    13.2 against 10.1 (in pieces of 4; of 8 11.5); 8 of 512 10.5 against 12.5; 20 of 1024 17.5 against 23.4; 56 of 1536
+//    57 against 72, 56 of 64 to 1536 35 against 41, 40 of them 34 against 30; 8 rows of one request of 512 20 against 17.
 //  * Where it leaves each request two pieces or more on average, as many pieces as work-groups run at once and no more
 //    (3 on each of 256 compute units, by their registers; 32 requests of up to 8192 tokens: 69 us, with 30 % more 73).
 //    Larger batches take up to four times that, 64 tiles a piece, so that the requests' lengths even out (64 requests
@@ -39,7 +40,8 @@ static int attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, in
     const int64_t tiles = (max_ctx + TILE - 1) / TILE, base = (int64_t)B * c->kv_heads * groups;
     a->min_tiles = base < 32 ? 4 : base < 256 ? 8 : 32;
     const int64_t each = (int64_t)c->kv_heads * groups, at_once = 256 * ATTN_OCCUPANCY(c->head_dim / 32, rt);
-    const int64_t most = tiles <= std::max(8, a->min_tiles * 9 / 8) ? B : B * ((tiles + a->min_tiles - 1) / a->min_tiles);
+    const int64_t whole = base < 32 && rt * c->head_dim > 128 ? 8 : base < 160 ? 16 : base < 256 ? 32 : 48;
+    const int64_t most = tiles <= whole ? B : B * ((tiles + a->min_tiles - 1) / a->min_tiles);
     const int64_t items = at_once / each >= 2 * B ? at_once / each
                                                   : B + std::max<int64_t>(1, std::max(at_once, std::min(base * tiles / 64, 4 * at_once)) / each);
     a->items = (int)std::min(most, items);
