@@ -129,17 +129,33 @@ __device__ __forceinline__ float wave_sum(float x) {
 
 // How the requests are cut: whole pieces of `chunk` tiles, and a last one of
 // more than chunk / 8 and up to 9 / 8 chunk (a request's only one may be
-// shorter), so that there are at most a.items pieces (sum of whole ones <= total
-// / chunk <= items - B, and a last one each).  The sum of up to 4096 counts is
-// taken in fp32 and raised by 2^-16, more than its rounding.  All whole pieces
-// come before all last ones: the work-groups that start last are the short ones.
-// (r0: the lane's request of the first 64.)
+// shorter), so that there are at most a.items pieces.  total / (items - B) is
+// always enough: sum of whole ones <= total / chunk <= items - B, and a last one
+// each.  (The sum of up to 4096 counts is taken in fp32 and raised by 2^-16,
+// more than its rounding.)  With up to 64 requests, one a lane, smaller chunks
+// from total / items on are tried, which make as many pieces as there may be
+// (16 requests of 4096 Q8_0 tokens and 8 rows 87 -> 74 us, 32 of 8192 fp16
+// tokens and heads of 160 295 -> 221).
+// All whole pieces come before all last ones: the work-groups that start last
+// are the short ones.  (r0: the lane's request of the first 64.)
+__device__ __forceinline__ int whole_pieces(const Req1 &r, int chunk) {
+    return r.tiles > chunk / 8 ? (int)((u32)(r.tiles - chunk / 8) / (u32)chunk) : 0;
+}
 __device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, const Req1 &r0, int lane) {
     if (a.items <= a.B) return INT32_MAX;
     float total = wave_sum((float)r0.tiles);
     for (int b0 = 64; b0 < a.B; b0 += 64) total += wave_sum((float)attn_req(c, a, b0 + lane).tiles);
     const float each = total * (1.f + 1.f / 65536.f) / (float)(a.items - a.B);
-    return max((int)fminf(each, 1e9f) + 1, a.min_tiles);
+    int hi = max(__builtin_amdgcn_readfirstlane((int)fminf(each, 1e9f)) + 1, a.min_tiles);
+    if (a.B > 64 || a.B == 1) return hi;
+    int lo = max(__builtin_amdgcn_readfirstlane((int)fminf(total / (float)a.items, 1e9f)), a.min_tiles);
+    for (int i = 0; i < 4 && lo < hi; ++i) {
+        const int at = i ? (lo + hi) / 2 : lo;
+        const int pieces = __builtin_amdgcn_readlane(wave_scan(r0.n ? whole_pieces(r0, at) + 1 : 0), 63);
+        if (pieces <= a.items) hi = at;
+        else lo = at + 1;
+    }
+    return hi;
 }
 
 // Piece `item` (b -1 when there are fewer).  All results are uniform.
@@ -148,9 +164,6 @@ struct Piece {
     int whole, last;           // the items of its first whole piece and of its last one
     Req1 r;
 };
-__device__ __forceinline__ int whole_pieces(const Req1 &r, int chunk) {
-    return r.tiles > chunk / 8 ? (int)((u32)(r.tiles - chunk / 8) / (u32)chunk) : 0;
-}
 __device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, const Req1 &r0, int chunk, int item,
                                             int lane) {
     if (a.items <= a.B) {                            // one piece a request

@@ -26,7 +26,9 @@ constexpr double KEPT_BYTES = 256e6;
 //  * Where it leaves each request two pieces or more on average, as many pieces as work-groups run at once and no more
 //    (3 on each of 256 compute units, by their registers; 32 requests of up to 8192 tokens: 69 us, with 30 % more 73).
 //    Larger batches take up to four times that, 64 tiles a piece, so that the requests' lengths even out (64 requests
-//    of up to 32768: 760 pieces 354 us, 3040 315).
+//    of up to 32768: 760 pieces 354 us, 3040 315).  Contexts of up to 256 tiles do so past 1.5 pieces only (64 requests
+//    of 8192 fp16 tokens: 96 pieces a head 337 us, 160 362; of up to 8192 91 and 93; of up to 32768 Q8_0 tokens 164 and
+//    145), but not rows of two tiles a wave (40 requests of 4096 Q8_0 tokens and 8 rows: 64 pieces 211 us, 104 166).
 static int attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, int window, Attn *a) {
     a->group = q_heads / c->kv_heads;
     a->rows_cap = a->group * max_q;
@@ -42,7 +44,7 @@ static int attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, in
     const int64_t each = (int64_t)c->kv_heads * groups, at_once = 256 * ATTN_OCCUPANCY(c->head_dim / 32, rt);
     const int64_t whole = base < 32 && rt * c->head_dim > 128 ? 8 : base < 160 ? 16 : base < 256 ? 32 : 48;
     const int64_t most = tiles <= whole ? B : B * ((tiles + a->min_tiles - 1) / a->min_tiles);
-    const int64_t items = at_once / each >= 2 * B ? at_once / each
+    const int64_t items = 2 * (at_once / each) >= (rt == 1 && tiles <= 256 ? 3 : 4) * B ? at_once / each
                                                   : B + std::max<int64_t>(1, std::max(at_once, std::min(base * tiles / 64, 4 * at_once)) / each);
     a->items = (int)std::min(most, items);
     return rt;

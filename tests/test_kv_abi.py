@@ -142,6 +142,16 @@ def test_workspace_bytes_of_invalid_sizes():
     assert f(cache(), 4, 1, 0, 32) == f(cache(), 4, 1, 4096, 30) == 0
 
 
+def test_workspace_grows_with_max_ctx():
+    # a buffer for the longest context serves every shorter one, and (checked by the call) every window
+    for heads, dim, q_heads, max_q in ((8, 128, 64, 1), (8, 128, 64, 8), (1, 32, 1, 1), (8, 256, 8, 3), (2, 160, 16, 8)):
+        c = cache(heads=heads, dim=dim)
+        for B in (1, 2, 5, 16, 20, 32, 40, 48, 49, 64, 72, 130, 400, 4096):
+            need = [kq.kqkv_attn_workspace_bytes(c, B, max_q, n, q_heads)
+                    for n in [*range(1, 4000, 31), *range(4000, 20000, 32), 10 ** 5, 10 ** 6, 2 ** 31 - 1]]
+            assert need == sorted(need) and need[-1] > 0
+
+
 def test_binding_refuses_host_tensors():
     torch = pytest.importorskip("torch")
     t = torch.zeros(1 << 20, dtype=torch.uint8)
