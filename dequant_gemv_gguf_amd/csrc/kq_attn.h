@@ -395,7 +395,7 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     constexpr int D = 32 * NB, LD = D + 4;
     // While the tiles go by: q's limbs (operands as lanes read them) and the sums of its blocks, of each wave, or (RT = 2)
     // of each row tile, shared; and each wave's tile's scales.  At the end [wave][16][LD] outputs, then [wave][16] (m, l).
-    constexpr int QB = NB * 2 * 1024, QPART = QB + (Q8 ? NB * 256 : 0), SB = Q8 ? NB * 128 : 0;
+    constexpr int QB = NB * 2 * 1024, QU = QB + (Q8 ? NB * 256 : 0), QPART = QU + (RT > 1 ? 256 : 0), SB = Q8 ? NB * 128 : 0;
     constexpr int JOIN = 16 * (LD + 2) * 4, PART = QPART + SB;
     static_assert(RT == 1 || RT == 2, "four row tiles' limbs in LDS");
     __shared__ __align__(16) uint8_t lds_[ATTN_WAVES * (PART > JOIN ? PART : JOIN)];
@@ -431,22 +431,27 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     const int lo_all = a.window ? (int)max(pos0 - a.window + 1, (int64_t)0) : 0;
     const int lo_max = a.window ? (int)max((int64_t)pc.r.ctx - a.window, (int64_t)0) : 0;
     if ((int64_t)pc.r.ctx > room && a.err && threadIdx.x == 0) a.err[0] = 1;
-    bool live[RT];
     int hi[RT], lo[RT];
-    // the rows' q (the loads go out first, the limbs are made while the first tile's are on their way)
-    f4 x[RT][2 * NB];
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const int r = row0 + 16 * (rw * RT + i) + m, j = div_magic(r, a.group_magic), qh = head * a.group + (r - j * a.group);
-        const int64_t trow = (int64_t)pc.r.first + j;
-        live[i] = r < rows && trow >= 0 && trow < a.T;
+        const int r = row0 + 16 * (rw * RT + i) + m, j = div_magic(r, a.group_magic);
         hi[i] = (int)max(min(pos0 + j + 1, room), (int64_t)0);
         lo[i] = a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0;
-        const float *qp = a.q + (live[i] ? trow * a.ldq + (int64_t)qh * D : 0) + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
+    }
+    // The q of one row tile (the loads go out first, the limbs are made while the first tile's are on their way): where a
+    // wave has two, the waves of the same rows make one each.
+    const int qt = RT == 1 ? 0 : kw % RT;
+    f4 x[2 * NB];
+    bool live;
+    {
+        const int r = row0 + 16 * (rw * RT + qt) + m, j = div_magic(r, a.group_magic), qh = head * a.group + (r - j * a.group);
+        const int64_t trow = (int64_t)pc.r.first + j;
+        live = r < rows && trow >= 0 && trow < a.T;
+        const float *qp = a.q + (live ? trow * a.ldq + (int64_t)qh * D : 0) + (Q8 ? 16 * (g & 1) + 8 * (g >> 1) : 8 * g);
 #pragma unroll
         for (int s = 0; s < NB; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) x[i][2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
+            for (int e = 0; e < 2; ++e) x[2 * s + e] = *(const f4 *)(qp + 32 * s + 4 * e);
     }
 
     const int t0 = pc.r.lo + (pc.index ? pc.index * chunk : 0);
@@ -521,24 +526,24 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     // q as two fp16 limbs, in LDS: read again for every tile, they leave their registers to the tile on the way
     auto part = [&](int i) { return lds_ + (RT == 1 ? wave : rw * RT + i) * QPART; };
     float unscale[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
+    {
         float top = 0.f;
 #pragma unroll
         for (int s = 0; s < 2 * NB; ++s) {
-            x[i][s] *= live[i] ? a.scale : 0.f;
+            x[s] *= live ? a.scale : 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[i][s][k]));
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fabsf(x[s][k]));
         }
         top = across_groups_max(top);
         int ex = 0;
         if (top > 0.f && top < INFINITY) ex = min(10 - ilogbf(top), 120);
-        unscale[i] = ldexpf(1.f, (Q8 ? 24 : 0) - ex);
+        unscale[0] = ldexpf(1.f, (Q8 ? 24 : 0) - ex);
+        if (RT > 1 && kw < RT) *(float *)(part(qt) + QU + lane * 4) = unscale[0];
 #pragma unroll
         for (int s = 0; s < NB; ++s) {
             float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[i][2 * s + e / 4][e % 4], ex);
+            for (int e = 0; e < 8; ++e) y[e] = ldexpf(x[2 * s + e / 4][e % 4], ex);
             h8 qh, ql;
             limbs(y, &qh, &ql);
             float sum = 0.f;                     // Q8_0: -128 2^-24 times the sum of q's block
@@ -547,14 +552,18 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
                 for (int e = 0; e < 8; ++e) sum += (float)qh[e] + (float)ql[e];
                 sum = across_groups_sum(sum) * (-128.f / 16777216.f);
             }
-            if (RT == 1 || kw == 0) {
-                *(h8 *)(part(i) + (2 * s) * 1024 + lane * 16) = qh;
-                *(h8 *)(part(i) + (2 * s + 1) * 1024 + lane * 16) = ql;
-                if constexpr (Q8) *(float *)(part(i) + QB + s * 256 + lane * 4) = sum;
+            if (RT == 1 || kw < RT) {
+                *(h8 *)(part(qt) + (2 * s) * 1024 + lane * 16) = qh;
+                *(h8 *)(part(qt) + (2 * s + 1) * 1024 + lane * 16) = ql;
+                if constexpr (Q8) *(float *)(part(qt) + QB + s * 256 + lane * 4) = sum;
             }
         }
     }
-    if (RT > 1) __syncthreads();
+    if constexpr (RT > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) unscale[i] = *(const float *)(part(i) + QU + lane * 4);
+    }
 
     f4 o[RT][2 * NB];
     float mx[RT], l[RT];
