@@ -400,6 +400,11 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     static_assert(RT == 1 || RT == 2, "four row tiles' limbs in LDS");
     __shared__ __align__(16) uint8_t lds_[ATTN_WAVES * (PART > JOIN ? PART : JOIN)];
     float *lds = (float *)lds_;
+    // Priority falls with the tiles done: of a SIMD's waves the oldest issues first, and where loads or vector work queue,
+    // the last to come began its tiles only as the first ended (of 32 requests of 8192 tokens, 70 us into 160), and then
+    // ran on alone (one request of 65536 Q8_0 tokens and heads of 64 26.9 -> 25.5 us, 8 rows of 4 requests of up to
+    // 16384 51 -> 49, one request of 524288 fp16 tokens 334 -> 327).
+    __builtin_amdgcn_s_setprio(3);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wg_rows = 16 * RT * a.row_waves, groups = (a.rows_cap + wg_rows - 1) / wg_rows;
     // row groups of a piece (they read the same keys) lie 8 blocks apart: one L2
@@ -711,7 +716,12 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
         }
         if constexpr (MORE) get_v(next);
     };
-    for (int n = 0; n + 1 < N; ++n) step(n, std::true_type());
+    for (int n = 0; n + 1 < N; ++n) {
+        if (n == N / 4) __builtin_amdgcn_s_setprio(2);
+        if (n == N / 2) __builtin_amdgcn_s_setprio(1);
+        if (n == N * 3 / 4) __builtin_amdgcn_s_setprio(0);
+        step(n, std::true_type());
+    }
     if (N > 0) step(N - 1, std::false_type());
 
     // join the waves of each row tile
