@@ -37,10 +37,10 @@
 // numbers the one of both low limbs is left out (2^-22).
 //
 // Measured (MI355X, 64 query heads, 8 kv heads, head size 128): one request of
-// 131072 fp16 tokens 98 us (5.5 TB/s of K and V), of 524288 369 us (5.8 TB/s); 64
-// requests of up to 32768 Q8_0 tokens 301 us (5.2 TB/s); one of 37 tokens 6.0 us;
-// eight rows of 4 requests of up to 16384 Q8_0 tokens 62 us, of the kernel's 56
-// the vector units work 40 % and the matrix units 16 %.
+// 131072 fp16 tokens 90 us (6.0 TB/s of K and V), of 524288 327 us (6.6 TB/s); 64
+// requests of up to 32768 Q8_0 tokens 287 us (5.5 TB/s); one of 37 tokens 5.8 us;
+// eight rows of 4 requests of up to 16384 Q8_0 tokens 59 us, of the kernel's 50
+// the vector units work 42 % and the matrix units 18 %.
 #pragma once
 
 #include "kq_kv.h"
