@@ -531,6 +531,21 @@ def test_attn_many_requests(B, longest):
         check_attn(run_attn(ref, table, ctx, start, q, 2, 0.18, 0, 1, max_ctx=max_ctx), want, tol)
 
 
+@pytest.mark.parametrize("lengths", ["equal", "ragged", "one", "two_long"])
+@pytest.mark.parametrize("type,B,heads", [(F16, 20, 8), (Q8, 40, 8), (F16, 64, 4), (Q8, 2, 8)])
+def test_attn_cut_to_fill_the_device(type, B, heads, lengths):
+    # fewer pieces than the lengths would take: their size is searched for
+    rng = np.random.default_rng(B + heads)
+    most = 1700
+    ctx = {"equal": [most] * B, "ragged": [int(n) for n in rng.integers(0, most, B)], "one": [0] * (B - 1) + [most],
+           "two_long": [most, most - 33] + [int(n) for n in rng.integers(0, 40, B - 2)]}[lengths]
+    new = [1 if n else 0 for n in ctx]
+    ref, table, start, q = attn_case(rng, type, heads, heads, 32, 64, ctx, new)
+    want, tol = kv_ref.attn(ref, table, ctx, start, q, heads, float(np.float32(0.18)), 0, out=np.full_like(q, 3.0))
+    for max_ctx in (most, 10 ** 6):
+        check_attn(run_attn(ref, table, ctx, start, q, heads, 0.18, 0, 1, max_ctx=max_ctx), want, tol)
+
+
 @pytest.mark.parametrize("type", [F16, Q8])
 def test_pages_past_four_gibibytes(type):
     # the last pages of a cache of over 4 GiB, K and V each: written, read back and attended to
