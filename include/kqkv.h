@@ -144,9 +144,9 @@ typedef struct kqkv_rope {
  *          they are.  Both NULL: nothing is stored
  * rope NULL: nothing turns (q_heads must be 0).  fp16 values are rounded to
  * nearest (beyond the fp16 range: infinities).  A Q8_0 block of 32 values x has
- * the scale s = fp16(max|x| / 127), at most 65504, and the quants
- * rint(x / s), -127..127 (0 when s is 0); a block with an infinity or a NaN
- * gets a NaN scale.  When two tokens name the same slot, either's values or a
+ * the scale s = fp16(max|x| * (1 / 127)), reciprocal and product rounded to
+ * fp32, at most 65504, and the quants rint(x / s), -127..127 (0 when s is 0); a
+ * block with an infinity or a NaN gets a NaN scale.  When two tokens name the same slot, either's values or a
  * mixture stay there.  0 <= T < 2^23, q_heads <= 1024. */
 int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const int32_t *pos, int64_t pos_stride,
                     const int32_t *slots, int q_heads, const float *q, int64_t ldq, float *q_out, int64_t ldq_out,

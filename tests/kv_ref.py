@@ -12,7 +12,7 @@ def quantise(x):
     m = np.abs(x).max(-1)
     bad = ~np.isfinite(x).all(-1)
     with np.errstate(all="ignore"):
-        s = np.minimum(m / np.float32(127), np.float32(65504)).astype(np.float16)
+        s = np.minimum(m * (np.float32(1) / np.float32(127)), np.float32(65504)).astype(np.float16)
         f = s.astype(np.float32)[..., None]
         n = np.where(f > 0, np.rint(x / f), 0)
     n = np.where(bad[..., None], 0, np.clip(n, -127, 127)).astype(np.int8)

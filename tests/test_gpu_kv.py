@@ -271,6 +271,25 @@ def test_binding_refuses_short_buffers(type):
             kq.KVCache(type, 2, 64, 16, 3, k, v)
 
 
+def test_scales_between_two_halves():
+    # largest magnitudes whose 127th rounds to one half as a product with the reciprocal and to the next as a quotient
+    rng = np.random.default_rng(31)
+    top = np.array([0x3FFF9CC1, 0x3FFE1FC1], dtype=np.uint32).view(np.float32)
+    assert ((top * (np.float32(1) / np.float32(127))).astype(np.float16) != (top / np.float32(127)).astype(np.float16)).all()
+    T, H, D, page = 32, 4, 32, 16
+    m = rng.choice(np.concatenate([top, -top]), (2, T, H))
+    x = (rng.uniform(-0.9, 0.9, (2, T, H, D)) * m[..., None]).astype(np.float32)
+    x[0, :, :, 7], x[1, :, :, 19] = m
+    ref = kv_ref.Cache(Q8, H, D, page, 2)
+    cache, kb, vb = device_cache(ref)
+    kq.kqkv_rope_store(cache, None, T, None, 0, i32(np.arange(T)), 0, None, 0, None, 0, dev(x[0].reshape(T, -1)), H * D,
+                       dev(x[1].reshape(T, -1)), H * D)
+    for t in range(T):
+        ref.put(t, x[0, t], x[1, t])
+    assert np.array_equal(kb.cpu().numpy().reshape(-1), ref.k.reshape(-1))
+    assert np.array_equal(vb.cpu().numpy().reshape(-1), ref.v.reshape(-1))
+
+
 @pytest.mark.parametrize("type", [F16, Q8])
 def test_store_without_rotation_in_place_and_load(type):
     rng = np.random.default_rng(9)
