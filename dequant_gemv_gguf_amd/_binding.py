@@ -45,7 +45,6 @@ class KVCache(ctypes.Structure):
                 raise ValueError("KVCache: k and v must be contiguous device tensors of at least %d bytes" %
                                  (page * int(n_pages)))
         self.tensors = (k, v)
-        self.ref = ctypes.byref(self)
 
 
 class KVRope(ctypes.Structure):
@@ -64,7 +63,6 @@ class KVRope(ctypes.Structure):
             if not f.is_cuda or not f.is_contiguous() or f.element_size() != 4 or f.numel() < int(rot_dims) // 2:
                 raise ValueError("KVRope: freq_factors must be rot_dims / 2 contiguous fp32 values on the device")
         self.tensors = (freq_factors,)
-        self.ref = ctypes.byref(self)
 
 
 class KQError(RuntimeError):
@@ -408,6 +406,13 @@ def kq_stream_qgemv(h, qtype, W, N, K, x, M, y):
 _torch_c = None
 
 
+def _struct(s):
+    """A KVCache or KVRope as an argument.  (Made for each call: a byref that the
+    object itself held would be a cycle that is never collected, and keep the
+    buffers.)"""
+    return None if s is None else ctypes.byref(s)
+
+
 def _device_call(fn, like, stream, *args):
     """Calls lib().fn(*args, stream) with the tensor `like`'s device current."""
     global _torch_c
@@ -449,23 +454,21 @@ def kqkv_plan(B, ctx_len, new_len, page_tokens, table, table_stride, held, held_
 
 def kqkv_rope_store(cache, rope, T, pos, pos_stride, slots, q_heads, q, ldq, q_out, ldq_out, k, ldk, v, ldv,
                     stream=None):
-    _device_call("kqkv_rope_store", q if q is not None else k, stream, cache.ref if cache is not None else None,
-                 rope.ref if rope is not None else None, T, _addr(pos), pos_stride, _addr(slots), q_heads, _addr(q),
-                 ldq, _addr(q_out), ldq_out, _addr(k), ldk, _addr(v), ldv)
+    _device_call("kqkv_rope_store", q if q is not None else k, stream, _struct(cache), _struct(rope), T,
+                 _addr(pos), pos_stride, _addr(slots), q_heads, _addr(q), ldq, _addr(q_out), ldq_out, _addr(k), ldk,
+                 _addr(v), ldv)
 
 
 def kqkv_load(cache, T, slots, k=None, v=None, stream=None):
-    _device_call("kqkv_load", slots, stream, cache.ref if cache is not None else None, T, _addr(slots), _addr(k),
-                 _addr(v))
+    _device_call("kqkv_load", slots, stream, _struct(cache), T, _addr(slots), _addr(k), _addr(v))
 
 
 def kqkv_attn_workspace_bytes(cache, B, max_q, max_ctx, q_heads):
-    return int(lib().kqkv_attn_workspace_bytes(cache.ref if cache is not None else None, int(B), int(max_q),
-                                               int(max_ctx), int(q_heads)))
+    return int(lib().kqkv_attn_workspace_bytes(_struct(cache), int(B), int(max_q), int(max_ctx), int(q_heads)))
 
 
 def kqkv_attn(cache, B, max_q, max_ctx, ctx_len, seq_start, table, table_stride, q_heads, T, q, ldq, scale, window,
               out, ldo, workspace=None, workspace_bytes=0, err_flag=None, stream=None):
-    _device_call("kqkv_attn", q, stream, cache.ref if cache is not None else None, B, max_q, max_ctx, _addr(ctx_len),
-                 _addr(seq_start), _addr(table), table_stride, q_heads, T, _addr(q), ldq, scale, window, _addr(out),
-                 ldo, _addr(workspace), workspace_bytes, _addr(err_flag))
+    _device_call("kqkv_attn", q, stream, _struct(cache), B, max_q, max_ctx, _addr(ctx_len), _addr(seq_start),
+                 _addr(table), table_stride, q_heads, T, _addr(q), ldq, scale, window, _addr(out), ldo,
+                 _addr(workspace), workspace_bytes, _addr(err_flag))
