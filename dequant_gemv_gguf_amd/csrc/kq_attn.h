@@ -202,6 +202,7 @@ __device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, const
 }
 
 typedef u32 u2 __attribute__((ext_vector_type(2)));
+typedef unsigned short us8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
@@ -385,6 +386,13 @@ __device__ __forceinline__ float across_groups_sum(float x) {
     return x + __shfl_xor(x, 32);
 }
 
+// The lane, made anew: for what is seldom done, so that no register keeps anything of it over the tiles.
+__device__ __forceinline__ int fresh_lane() {
+    int lane = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+    asm volatile("" : "+v"(lane));
+    return lane;
+}
+
 // One work-group: a piece of a request's tiles for one kv head and up to
 // 16 RT * row_waves of its rows.  Wave w takes the RT row tiles of w % row_waves
 // and the tiles w / row_waves + i * (4 / row_waves) of the piece (waves that
@@ -436,13 +444,12 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     const int lo_all = a.window ? (int)max(pos0 - a.window + 1, (int64_t)0) : 0;
     const int lo_max = a.window ? (int)max((int64_t)pc.r.ctx - a.window, (int64_t)0) : 0;
     if ((int64_t)pc.r.ctx > room && a.err && threadIdx.x == 0) a.err[0] = 1;
-    int hi[RT], lo[RT];
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-        const int r = row0 + 16 * (rw * RT + i) + m, j = div_magic(r, a.group_magic);
-        hi[i] = (int)max(min(pos0 + j + 1, room), (int64_t)0);
-        lo[i] = a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0;
-    }
+    // (of the lane's row of tile i; made where a tile is cut, not kept)
+    struct Sight { int lo, hi; };
+    auto sight = [&](int i) {
+        const int j = div_magic(row0 + 16 * (rw * RT + i) + (fresh_lane() & 15), a.group_magic);
+        return Sight{a.window ? (int)max(pos0 + j - a.window + 1, (int64_t)0) : 0, (int)max(min(pos0 + j + 1, room), (int64_t)0)};
+    };
     // The q of one row tile (the loads go out first, the limbs are made while the first tile's are on their way): where a
     // wave has two, the waves of the same rows make one each.
     const int qt = RT == 1 ? 0 : kw % RT;
@@ -471,6 +478,7 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     u32 ids = 0, raw = 0;
     uint64_t bad = 0;
     auto group_of = [&](int n, bool *in) {
+        const int lane = fresh_lane();
         const int grp = 2 * (first + kws * (n + (lane >> 1))) + (lane & 1);
         *in = n + (lane >> 1) < N && grp * 16 < hi_all && grp * 16 + 16 > lo_all;
         return grp;
@@ -581,6 +589,15 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     }
     uint8_t *scales = lds_ + ATTN_WAVES * QPART + wave * SB;
     u32 qat = (u32)lane * 16;
+    auto is_edge = [&](int tile, u32 wrong) { return wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min; };
+    auto v_half = [&](int k) { return __builtin_bit_cast(h8, u4{T.v[4 * k], T.v[4 * k + 1], T.v[4 * k + 2], T.v[4 * k + 3]}); };
+    auto v_scales = [&](int b) { return *(const h8 *)(scales + ((2 + (g >> 1)) * NB + b) * 32 + (g & 1) * 16); };
+    // Keys that some rows of the request see and others do not (the newest of several tokens, the oldest of a window): a
+    // weight of 0 takes no infinity and no NaN out of the product.  Values that are no numbers (Q8_0: whose product with the
+    // scale is none as a half) are taken as 0 in tiles with such keys, and looked up again behind the loop for the rows that
+    // see them.  (Looking for them costs 0.1 us a call, 0.2 to 0.4 for Q8_0; the lanes made anew gave back the registers.)
+    bool cleared = false;
+    auto no_number = [](h8 x, int e) { return (__builtin_bit_cast(us8, x)[e] & 0x7C00) == 0x7C00; };
     // One tile, while the next one's keys and values are asked for.  The last tile is a copy of its own, without these
     // loads: asked for and not used, the barrier behind the loop would wait for them (under a condition, the waits for
     // this tile's values would wait for the next one's keys).
@@ -637,7 +654,7 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
             get_k(next);
             T.wrong = wrong_of(n + 1);
         }
-        const bool edge = wrong || tile * TILE < lo_max || tile * TILE + TILE > hi_min;
+        const bool edge = is_edge(tile, wrong);
         u32 gone = 0;                            // keys of the lane that no row may touch
         if (edge) {
 #pragma unroll
@@ -653,10 +670,11 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] = Q8 ? d[i][e / 4][e % 4] : d[i][e / 4][e % 4] + d2[i][e / 4][e % 4];
             if (edge) {
+                const Sight see = sight(i);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int key = tile * TILE + 8 * g + e;
-                    s[e] = ((gone >> e) & 1) || key >= hi[i] || key < lo[i] ? -INFINITY : s[e];
+                    s[e] = ((gone >> e) & 1) || key >= see.hi || key < see.lo ? -INFINITY : s[e];
                 }
             }
             float top = s[0];
@@ -680,10 +698,45 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
         }
         order_v<Q8, NB>(T);
         if constexpr (Q8) {
+            // (values of their own from here on: as they are changed below, they would else be copied where they are loaded, at
+            // the loop's end, with a wait for them)
+            if constexpr (RT > 1) {
+#pragma unroll
+                for (int k = 0; k < 4 * NB; ++k) asm volatile("" : "+v"(T.v[k]));
+            }
+            bool far = false;                    // a scale is no number, or 512 or more (below, times 128 is a half)
+            if (edge && pc.r.n > 1) {
+                us8 top = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+                for (int b = 0; b < NB; ++b) top = __builtin_elementwise_max(top, __builtin_bit_cast(us8, v_scales(b)));
+                const u4 w = __builtin_bit_cast(u4, top);
+                u32 any = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const u32 keep = ((gone >> (2 * i)) & 1 ? 0u : 0x7FFFu) | ((gone >> (2 * i + 1)) & 1 ? 0u : 0x7FFF0000u);
+                    any |= (w[i] & keep) + 0x20002000u;
+                }
+                far = __any((any & 0x80008000u) != 0) != 0;
+            }
+            if (far) {
+                cleared = true;
+#pragma unroll
+                for (int k = 0; k < 2 * NB; ++k) {
+                    h8 vs = v_scales(k / 2);
+                    const h8 v = quants_h8(T.v[2 * k], T.v[2 * k + 1]) * vs;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) T.v[2 * k + e / 4] &= no_number(v, e) ? ~(0xFFu << (8 * (e & 3))) : ~0u;
+                    if (k & 1) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) vs[e] = no_number(vs, e) ? (_Float16)0 : vs[e];
+                        *(h8 *)(scales + ((2 + (g >> 1)) * NB + k / 2) * 32 + (g & 1) * 16) = vs;
+                    }
+                }
+            }
             // scale times quant (19 bits, a multiple of 2^-24) is exactly a half and a half's remainder
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                h8 vs = *(const h8 *)(scales + ((2 + (g >> 1)) * NB + b) * 32 + (g & 1) * 16);
+                h8 vs = v_scales(b);
                 if (edge) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) vs[e] = (gone >> e) & 1 ? (_Float16)0 : vs[e];
@@ -704,14 +757,27 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
                     keep[i] = ((gone >> (2 * i)) & 1 ? 0u : 0xFFFFu) | ((gone >> (2 * i + 1)) & 1 ? 0u : 0xFFFF0000u);
 #pragma unroll
                 for (int k = 0; k < 8 * NB; ++k) T.v[k] &= keep[k & 3];
+                if (pc.r.n > 1) {
+                    const h8 zero = {0, 0, 0, 0, 0, 0, 0, 0};
+                    h8 z = zero;                 // stays 0 but for infinities and NaN
+#pragma unroll
+                    for (int k = 0; k < 2 * NB; ++k) z = __builtin_elementwise_fma(v_half(k), zero, z);
+                    const u4 w = __builtin_bit_cast(u4, z);
+                    if (__any((w[0] | w[1] | w[2] | w[3]) != 0)) {
+                        cleared = true;
+#pragma unroll
+                        for (int k = 0; k < 2 * NB; ++k)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) T.v[4 * k + e / 2] &= no_number(v_half(k), e) ? ~(0xFFFFu << (16 * (e & 1))) : ~0u;
+                    }
+                }
             }
-            auto vop = [&](int k) { return __builtin_bit_cast(h8, u4{T.v[4 * k], T.v[4 * k + 1], T.v[4 * k + 2], T.v[4 * k + 3]}); };
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
 #pragma unroll
-                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(vop(k), ph[i], o[i][k]);
+                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(v_half(k), ph[i], o[i][k]);
 #pragma unroll
-                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(vop(k), pl[i], o[i][k]);
+                for (int k = 0; k < 2 * NB; ++k) o[i][k] = mma(v_half(k), pl[i], o[i][k]);
             }
         }
         if constexpr (MORE) get_v(next);
@@ -723,6 +789,48 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
         step(n, std::true_type());
     }
     if (N > 0) step(N - 1, std::false_type());
+    // outputs of rows that see an infinity or a NaN among the values of such tiles: NaN
+    if (cleared) {
+        const int g = fresh_lane() >> 4;
+        for (int n = 0; n < N; ++n) {
+            if ((n & 31) == 0) {
+                ask_ids(n);
+                take_ids(n);
+            }
+            const int tile = first + kws * n;
+            const u32 wrong = wrong_of(n);
+            if (!is_edge(tile, wrong)) continue;
+            const Where w = where(n);
+            if constexpr (Q8) *(h8 *)(scales + sl * 16) = *(const h8 *)(sb + w.s0 + (second ? w.ds : 0));
+            Tile<Q8, NB> P;
+            load_v<Q8, NB, NT>(P, vb + w.x0 + ((g & 2) ? w.dx : 0), lane);
+            order_v<Q8, NB>(P);
+            h8 seen[RT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const Sight see = sight(i);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int key = tile * TILE + 8 * g + e;
+                    seen[i][e] = ((wrong >> (g >> 1)) & 1) || key >= see.hi || key < see.lo ? (_Float16)0 : (_Float16)1;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 2 * NB; ++k) {
+                h8 v, none;
+                if constexpr (Q8) v = quants_h8(P.v[2 * k], P.v[2 * k + 1]) * v_scales(k / 2);
+                else v = __builtin_bit_cast(h8, u4{P.v[4 * k], P.v[4 * k + 1], P.v[4 * k + 2], P.v[4 * k + 3]});
+#pragma unroll
+                for (int e = 0; e < 8; ++e) none[e] = no_number(v, e) ? (_Float16)1 : (_Float16)0;
+#pragma unroll
+                for (int i = 0; i < RT; ++i) {
+                    const f4 count = mma(none, seen[i], f4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[i][k][e] = count[e] > 0.f ? __builtin_nanf("") : o[i][k][e];
+                }
+            }
+        }
+    }
 
     // join the waves of each row tile
     float *stat = lds + ATTN_WAVES * 16 * LD;
