@@ -29,7 +29,8 @@
 //
 // Precision.  A row's q is scaled by a power of two that brings its largest
 // element to [2^10, 2^11) and enters as two fp16 limbs (22 bits), and so do the
-// weights, times 2^6 (the limbs end at 2^-25, 2^-31 of the largest weight).
+// weights, times 2^6: rounded at 2^-25, 2^-31 of the largest weight, which takes
+// bits from those below 2^-9 of it.
 // fp16 keys and values enter as they are.  Int8 quants of keys are whole fp16
 // numbers, a block's scale is applied to its 32-element partial score in fp32;
 // an int8 value, scale times quant (19 bits, a multiple of 2^-24), is exactly the
@@ -203,6 +204,7 @@ __device__ __forceinline__ Piece attn_piece(const Cache &c, const Attn &a, const
 
 typedef u32 u2 __attribute__((ext_vector_type(2)));
 typedef unsigned short us8 __attribute__((ext_vector_type(8)));
+typedef float f2 __attribute__((ext_vector_type(2)));
 
 __device__ __forceinline__ f4 mma(h8 a, h8 b, f4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
@@ -242,13 +244,15 @@ __device__ __forceinline__ float minus_hi(u32 h, float x) {
     asm("v_fma_mix_f32 %0, %1, -1.0, %2 op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(r) : "v"(h), "v"(x));
     return r;
 }
-// x = hi + lo to 22 bits: hi rounded to zero, lo the rest.
+// x = hi + lo to 22 bits: hi rounded to zero, lo the rest, rounded to nearest (where it is subnormal, at 2^-25, a rounding
+// to zero would take from every small weight of a row, and nothing from their sum).
 __device__ __forceinline__ void limbs(const float *x, h8 *hi, h8 *lo) {
     u4 a, b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         a[i] = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(x[2 * i], x[2 * i + 1]));
-        b[i] = __builtin_bit_cast(u32, __builtin_amdgcn_cvt_pkrtz(minus_lo(a[i], x[2 * i]), minus_hi(a[i], x[2 * i + 1])));
+        const f2 rest = {minus_lo(a[i], x[2 * i]), minus_hi(a[i], x[2 * i + 1])};
+        b[i] = __builtin_bit_cast(u32, __builtin_convertvector(rest, hf2));
     }
     *hi = __builtin_bit_cast(h8, a);
     *lo = __builtin_bit_cast(h8, b);

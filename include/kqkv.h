@@ -187,13 +187,13 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
  * A page outside [0, n_pages), or a length past table_stride * P (or 2^31 - 64), takes its
  * tokens out of the sum and sets *err_flag; a negative length counts as 0.
  * Accumulation is fp32; q and the weights enter the matrix instructions as two
- * fp16 limbs (about 22 bits), the cached values as they are.  |scale * q| is to
- * stay below 2^100.  What a row does not see never reaches it, whatever it holds;
- * infinities and NaN in a key or value that it sees, and values that a Q8_0 cache
- * holds past the fp16 range (65504), give infinities or NaN (an infinite key also
- * where its weight would be 0).  Reruns are
- * bit-identical; a request's bits may depend on the other requests' lengths
- * (they set where its tokens are split).  1 <= B <= 4096, q_heads a multiple
+ * fp16 limbs (22 bits, weights no finer than 2^-31 of their row's largest), the
+ * cached values as they are.  |scale * q| is to stay below 2^100.  What a row does
+ * not see never reaches it, whatever it holds; infinities and NaN in a key or
+ * value that it sees, and values that a Q8_0 cache holds past the fp16 range
+ * (65504), give infinities or NaN (an infinite key also where its weight would be
+ * 0).  Reruns are bit-identical; a request's bits may depend on the other
+ * requests' lengths (they set where its tokens are split).  1 <= B <= 4096, q_heads a multiple
  * of kv_heads, at most 1024, B * q_heads * max_q < 2^24, 0 <= T < 2^24,
  * window >= 0, scale finite. */
 int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const int32_t *ctx_len,

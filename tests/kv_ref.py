@@ -147,7 +147,10 @@ def attn(cache, table, ctx, start, q, q_heads, scale, window, max_q=8, out=None)
     most e = A (2^-21 + dim u), A = scale * max|q| sum |k| (largest over
     the keys), a weight by e + 2^-21 (exp2 and its limbs) of itself, numerator and
     denominator alike; their sums run over at most n / 32 + 64 additions.  So
-    |error| <= 2 (e + 2^-21 + (n / 32 + 64) u) * sum w |v| / sum w."""
+    |error| <= 2 (e + 2^-21 + (n / 32 + 64) u) * sum w |v| / sum w.
+    (A weight below 2^-9 of the largest is off by up to 2^-31 of the largest, n
+    2^-31 max|v| over a row: within the n 2^-28 of the additions' term as long as
+    max|v| is at most 8 times the weighted mean of |v|.)"""
     T = q.shape[0]
     kv, d, page = cache.heads, cache.dim, cache.page
     g = q_heads // kv
