@@ -128,9 +128,9 @@ __device__ __forceinline__ float wave_sum(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(bits(x), 63));
 }
 
-// How the requests are cut: whole pieces of `chunk` tiles, and a last one of
-// more than chunk / 8 and up to 9 / 8 chunk (a request's only one may be
-// shorter), so that there are at most a.items pieces.  total / (items - B) is
+// How the requests are cut: whole pieces of `chunk` tiles, and a last one of at
+// least chunk / 8 (and 1) and less than chunk more than that (a request's only
+// one may be shorter), so that there are at most a.items pieces.  total / (items - B) is
 // always enough: sum of whole ones <= total / chunk <= items - B, and a last one
 // each.  (The sum of up to 4096 counts is taken in fp32 and raised by 2^-16,
 // more than its rounding.)  With up to 64 requests, one a lane, smaller chunks
@@ -140,7 +140,8 @@ __device__ __forceinline__ float wave_sum(float x) {
 // All whole pieces come before all last ones: the work-groups that start last
 // are the short ones.  (r0: the lane's request of the first 64.)
 __device__ __forceinline__ int whole_pieces(const Req1 &r, int chunk) {
-    return r.tiles > chunk / 8 ? (int)((u32)(r.tiles - chunk / 8) / (u32)chunk) : 0;
+    const int least = max(chunk / 8, 1);
+    return r.tiles > least ? (int)((u32)(r.tiles - least) / (u32)chunk) : 0;
 }
 __device__ __forceinline__ int attn_chunk(const Cache &c, const Attn &a, const Req1 &r0, int lane) {
     if (a.items <= a.B) return INT32_MAX;
