@@ -44,6 +44,7 @@ class KVCache(ctypes.Structure):
             if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < page * int(n_pages):
                 raise ValueError("KVCache: k and v must be contiguous device tensors of at least %d bytes" %
                                  (page * int(n_pages)))
+        self.device = _device_of("KVCache", (k, v))
         self.tensors = (k, v)
 
 
@@ -60,8 +61,9 @@ class KVRope(ctypes.Structure):
         super().__init__(int(style), int(rot_dims), float(base), len(sections), padded, _addr(freq_factors))
         if freq_factors is not None and not isinstance(freq_factors, int):
             f = freq_factors
-            if not f.is_cuda or not f.is_contiguous() or f.element_size() != 4 or f.numel() < int(rot_dims) // 2:
+            if not f.is_cuda or not f.is_contiguous() or str(f.dtype) != "torch.float32" or f.numel() < int(rot_dims) // 2:
                 raise ValueError("KVRope: freq_factors must be rot_dims / 2 contiguous fp32 values on the device")
+        self.device = _device_of("KVRope", (freq_factors,))
         self.tensors = (freq_factors,)
 
 
@@ -396,14 +398,18 @@ def kq_stream_qgemv(h, qtype, W, N, K, x, M, y):
 
 # ---- paged key-value cache (include/kqkv.h) -------------------------------------
 # cache: a KVCache, rope: a KVRope (or None).  Tensors or int addresses.  A call
-# goes to the device that its tensors are on, on that device's current stream.
+# goes to the device that its tensors are on, on that device's current stream
+# where none is given.  Tensors are checked for what they are, not for their
+# sizes: all on one device, int32 or fp32 as the header says, contiguous, or with
+# rows that are, as far apart as the call's stride says.
 
 # These calls are made once per layer and token, and take a few microseconds on
 # the GPU: what the host spends on them shows.  So the current stream is asked
 # for by torch._C's raw calls (0.1 us; torch.cuda.current_stream makes a Stream
-# object, 2.8 us), and addresses go to ctypes as ints.
+# object, 2.8 us), addresses go to ctypes as ints, and a call's tensors are
+# looked over together, one property after the other (1.1 to 1.7 us a call).
 
-_torch_c = None
+_torch_c = _int32 = _float32 = _dtype = _get_device = _is_contiguous = _data_ptr = None      # until a tensor comes
 
 
 def _struct(s):
@@ -413,27 +419,97 @@ def _struct(s):
     return None if s is None else ctypes.byref(s)
 
 
-def _device_call(fn, like, stream, *args):
-    """Calls lib().fn(*args, stream) with the tensor `like`'s device current."""
-    global _torch_c
-    f = getattr(_lib or lib(), fn)
-    if stream is None:
-        if like is not None and type(like) is not int:
-            if not like.is_cuda:
-                raise ValueError("%s: tensors must be on the device" % fn)
-            if _torch_c is None:
-                import torch
-                _torch_c = torch._C
-            device = like.get_device()
-            if device != _torch_c._cuda_getDevice():
-                import torch
-                with torch.cuda.device(device):
-                    _check(fn, f(*args, _torch_c._cuda_getCurrentRawStream(device)))
-                return
+def _load_torch():
+    global _torch_c, _int32, _float32, _dtype, _get_device, _is_contiguous, _data_ptr
+    import torch
+    T = torch.Tensor
+    _int32, _float32 = torch.int32, torch.float32
+    _dtype, _get_device, _is_contiguous, _data_ptr = T.dtype.__get__, T.get_device, T.is_contiguous, T.data_ptr
+    _torch_c = torch._C
+
+
+def _device_of(fn, tensors):
+    """The device index of the tensors among `tensors` (None where there are none)."""
+    device = None
+    for t in tensors:
+        if t is None or isinstance(t, int):
+            continue
+        if not t.is_cuda:
+            raise ValueError("%s: tensors must be on the device" % fn)
+        if device is None:
+            device = t.get_device()
+        elif t.get_device() != device:
+            raise ValueError("%s: tensors on devices %d and %d" % (fn, device, t.get_device()))
+    return device
+
+
+def _rows_apart(t, ld):
+    """Whether t[i] are contiguous and ld elements apart."""
+    shape, strides, n = t.shape, t.stride(), 1
+    for size, stride in zip(reversed(shape[1:]), reversed(strides[1:])):
+        if size != 1 and stride != n:
+            return False
+        n *= size
+    return len(shape) > 1 and (shape[0] == 1 or strides[0] == ld)
+
+
+def _addresses(fn, device, dtypes, tensors, strides):
+    """The tensors' addresses (int addresses and None as they are), all on this
+    device and of these dtypes (those behind the last one's: of any).  strides:
+    the rows' of those that have any, else None."""
+    n = len(tensors)
+    try:
+        if (list(map(_get_device, tensors)).count(device) == n and list(map(_is_contiguous, tensors)).count(True) == n and
+                list(map(_dtype, tensors))[:len(dtypes)] == dtypes):
+            return list(map(_data_ptr, tensors))
+    except TypeError:                                  # not all are tensors
+        pass
+    out = []
+    for i, t in enumerate(tensors):
+        if t is not None and not isinstance(t, int):
+            if _device_of(fn, (t,)) != device:
+                raise ValueError("%s: tensors on devices %d and %d" % (fn, device, t.get_device()))
+            if i < len(dtypes) and t.dtype != dtypes[i]:
+                raise ValueError("%s: a %s tensor where %s is asked for" % (fn, t.dtype, dtypes[i]))
+            if not t.is_contiguous() and (strides[i] is None or not _rows_apart(t, strides[i])):
+                raise ValueError("%s: a tensor of shape %s and strides %s is neither contiguous nor rows at the call's stride"
+                                 % (fn, tuple(t.shape), t.stride()))
+        out.append(_addr(t))
+    return out
+
+
+def _target(fn, stream, first, others, *structs):
+    """Where a call goes: the device of its tensors (`first` mostly is one) or of
+    its cache, which has to be the same (None: the current one), and the stream."""
+    if first is not None and type(first) is not int:
+        device = first.get_device()
+        if device < 0:
+            raise ValueError("%s: tensors must be on the device" % fn)
+    else:
+        device = _device_of(fn, others)
+    for s in structs:
+        if s is not None and s.device != device and s.device is not None:
+            if device is not None:
+                raise ValueError("%s: tensors on devices %d and %d" % (fn, device, s.device))
+            device = s.device
+    if device is not None:
+        if _torch_c is None:
+            _load_torch()
+        if stream is None:
             stream = _torch_c._cuda_getCurrentRawStream(device)
-    elif type(stream) is not int:
+    if stream is not None and type(stream) is not int:
         stream = stream.cuda_stream
-    r = f(*args, stream)
+    return device, stream
+
+
+def _call(fn, f, device, args):
+    """f(*args) with `device` current."""
+    if device is None or device == _torch_c._cuda_getDevice():
+        r = f(*args)
+    else:
+        import torch
+        with torch.cuda.device(device):
+            r = f(*args)
     if r:
         raise KQError(fn, r)
 
@@ -447,20 +523,42 @@ def kqkv_page_bytes(qtype, kv_heads, head_dim, page_tokens):
 
 def kqkv_plan(B, ctx_len, new_len, page_tokens, table, table_stride, held, held_out, free_pages, n_pages, n_free,
               n_free_out, T, slots, pos, seq_start, ctx_out, err_flag=None, stream=None):
-    _device_call("kqkv_plan", ctx_len, stream, B, _addr(ctx_len), _addr(new_len), page_tokens, _addr(table),
-                 table_stride, _addr(held), _addr(held_out), _addr(free_pages), n_pages, _addr(n_free),
-                 _addr(n_free_out), T, _addr(slots), _addr(pos), _addr(seq_start), _addr(ctx_out), _addr(err_flag))
+    if slots is None and pos is None and err_flag is None:
+        tensors = (ctx_len, new_len, held, held_out, free_pages, n_free, n_free_out, seq_start, ctx_out, table)
+    elif err_flag is None:
+        tensors = (ctx_len, new_len, held, held_out, free_pages, n_free, n_free_out, seq_start, ctx_out, table, slots, pos)
+    else:
+        tensors = (ctx_len, new_len, held, held_out, free_pages, n_free, n_free_out, seq_start, ctx_out, table, slots, pos,
+                   err_flag)
+    device, stream = _target("kqkv_plan", stream, ctx_len, tensors)
+    a = _addresses("kqkv_plan", device, [_int32] * len(tensors), tensors,
+                   (None, None, None, None, None, None, None, None, None, table_stride, None, None, None))
+    a += [None] * (13 - len(a))
+    _call("kqkv_plan", (_lib or lib()).kqkv_plan, device,
+          (B, a[0], a[1], page_tokens, a[9], table_stride, a[2], a[3], a[4], n_pages, a[5], a[6], T, a[10], a[11], a[7],
+           a[8], a[12], stream))
 
 
 def kqkv_rope_store(cache, rope, T, pos, pos_stride, slots, q_heads, q, ldq, q_out, ldq_out, k, ldk, v, ldv,
                     stream=None):
-    _device_call("kqkv_rope_store", q if q is not None else k, stream, _struct(cache), _struct(rope), T,
-                 _addr(pos), pos_stride, _addr(slots), q_heads, _addr(q), ldq, _addr(q_out), ldq_out, _addr(k), ldk,
-                 _addr(v), ldv)
+    fn = "kqkv_rope_store"
+    if q is None and q_out is None:
+        tensors, strides = (pos, slots, k, v), (pos_stride, None, ldk, ldv)
+    else:
+        tensors, strides = (pos, slots, k, v, q, q_out), (pos_stride, None, ldk, ldv, ldq, ldq_out)
+    device, stream = _target(fn, stream, slots, tensors, cache, rope)
+    a = _addresses(fn, device, [_int32, _int32, _float32, _float32, _float32, _float32][:len(tensors)], tensors, strides)
+    if len(a) == 4:
+        a += (None, None)
+    _call(fn, (_lib or lib()).kqkv_rope_store, device,
+          (_struct(cache), _struct(rope), T, a[0], pos_stride, a[1], q_heads, a[4], ldq, a[5], ldq_out, a[2], ldk, a[3],
+           ldv, stream))
 
 
 def kqkv_load(cache, T, slots, k=None, v=None, stream=None):
-    _device_call("kqkv_load", slots, stream, _struct(cache), T, _addr(slots), _addr(k), _addr(v))
+    device, stream = _target("kqkv_load", stream, slots, (k, v), cache)
+    a = _addresses("kqkv_load", device, [_int32, _float32, _float32], (slots, k, v), (None, None, None))
+    _call("kqkv_load", (_lib or lib()).kqkv_load, device, (_struct(cache), T, a[0], a[1], a[2], stream))
 
 
 def kqkv_attn_workspace_bytes(cache, B, max_q, max_ctx, q_heads):
@@ -469,6 +567,15 @@ def kqkv_attn_workspace_bytes(cache, B, max_q, max_ctx, q_heads):
 
 def kqkv_attn(cache, B, max_q, max_ctx, ctx_len, seq_start, table, table_stride, q_heads, T, q, ldq, scale, window,
               out, ldo, workspace=None, workspace_bytes=0, err_flag=None, stream=None):
-    _device_call("kqkv_attn", q, stream, _struct(cache), B, max_q, max_ctx, _addr(ctx_len), _addr(seq_start),
-                 _addr(table), table_stride, q_heads, T, _addr(q), ldq, scale, window, _addr(out), ldo,
-                 _addr(workspace), workspace_bytes, _addr(err_flag))
+    fn = "kqkv_attn"
+    if err_flag is None:
+        tensors, types = (ctx_len, seq_start, table, q, out), [_int32, _int32, _int32, _float32, _float32]
+    else:
+        tensors, types = (ctx_len, seq_start, table, q, out, err_flag), [_int32, _int32, _int32, _float32, _float32, _int32]
+    if workspace is not None:
+        tensors += (workspace,)
+    device, stream = _target(fn, stream, q, tensors, cache)
+    a = _addresses(fn, device, types, tensors, (None, None, table_stride, ldq, ldo, None, None))
+    _call(fn, (_lib or lib()).kqkv_attn, device,
+          (_struct(cache), B, max_q, max_ctx, a[0], a[1], a[2], table_stride, q_heads, T, a[3], ldq, scale, window, a[4],
+           ldo, a[-1] if workspace is not None else None, workspace_bytes, a[5] if err_flag is not None else None, stream))
