@@ -448,7 +448,7 @@ __global__ __launch_bounds__(ATTN_THREADS, ATTN_OCCUPANCY(NB, RT)) void attn_ker
     const int hi_min = (int)max(min(pos0 + 1, room), (int64_t)0);
     const int lo_all = a.window ? (int)max(pos0 - a.window + 1, (int64_t)0) : 0;
     const int lo_max = a.window ? (int)max((int64_t)pc.r.ctx - a.window, (int64_t)0) : 0;
-    if ((int64_t)pc.r.ctx > room && a.err && threadIdx.x == 0) a.err[0] = 1;
+    if (((int64_t)pc.r.ctx > room || pc.r.n > a.max_q) && a.err && threadIdx.x == 0) a.err[0] = 1;
     // (of the lane's row of tile i; made where a tile is cut, not kept)
     struct Sight { int lo, hi; };
     auto sight = [&](int i) {

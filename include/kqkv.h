@@ -175,7 +175,7 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
  *              table[b][i / P]
  *   max_q      rows of the longest request, 1..8 (one new token, or the
  *              positions of a verify pass); rows of a request past max_q are
- *              left
+ *              left, and *err_flag is set
  *   max_ctx    the longest context expected, 1 .. 2^31 - 1: it sets how the
  *              work is split (a longer one is computed all the same, slowly
  *              when max_ctx was short)
