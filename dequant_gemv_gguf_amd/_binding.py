@@ -568,13 +568,12 @@ def kqkv_attn_workspace_bytes(cache, B, max_q, max_ctx, q_heads):
 def kqkv_attn(cache, B, max_q, max_ctx, ctx_len, seq_start, table, table_stride, q_heads, T, q, ldq, scale, window,
               out, ldo, workspace=None, workspace_bytes=0, err_flag=None, stream=None):
     fn = "kqkv_attn"
-    if err_flag is None:
-        tensors, types = (ctx_len, seq_start, table, q, out), [_int32, _int32, _int32, _float32, _float32]
-    else:
-        tensors, types = (ctx_len, seq_start, table, q, out, err_flag), [_int32, _int32, _int32, _float32, _float32, _int32]
+    tensors = (ctx_len, seq_start, table, q, out) if err_flag is None else (ctx_len, seq_start, table, q, out, err_flag)
+    typed = len(tensors)
     if workspace is not None:
         tensors += (workspace,)
     device, stream = _target(fn, stream, q, tensors, cache)
+    types = [_int32, _int32, _int32, _float32, _float32, _int32][:typed]
     a = _addresses(fn, device, types, tensors, (None, None, table_stride, ldq, ldo, None, None))
     _call(fn, (_lib or lib()).kqkv_attn, device,
           (_struct(cache), B, max_q, max_ctx, a[0], a[1], a[2], table_stride, q_heads, T, a[3], ldq, scale, window, a[4],

@@ -244,3 +244,19 @@ def test_optional_tensors(library):
     kq.kqkv_load(**dict(c["kqkv_load"], v=None))
     kq.kqkv_attn(**dict(c["kqkv_attn"], workspace=None, workspace_bytes=0, err_flag=None))
     assert len(library) == 7
+
+
+@pytest.mark.parametrize("fn", ["kqkv_plan", "kqkv_rope_store", "kqkv_load", "kqkv_attn"])
+def test_the_first_call_of_a_process(library, devices, monkeypatch, fn):
+    load = binding._load_torch
+    for name in ("_torch_c", "_int32", "_float32", "_dtype", "_get_device", "_is_contiguous", "_data_ptr"):
+        monkeypatch.setattr(binding, name, None)
+
+    def loads():
+        load()
+        binding._torch_c = devices
+
+    monkeypatch.setattr(binding, "_load_torch", loads)
+    kw = calls()[fn]
+    getattr(kq, fn)(**kw)
+    assert len(library) == 1
