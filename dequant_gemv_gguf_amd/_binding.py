@@ -29,8 +29,9 @@ class GGUFTensor(ctypes.Structure):
 
 class KVCache(ctypes.Structure):
     """struct kqkv_cache (include/kqkv.h).  k and v: contiguous device tensors of
-    at least n_pages * kqkv_page_bytes bytes (kept alive by this object), or int
-    addresses."""
+    at least n_pages * kqkv_page_bytes bytes, on one device, or int addresses.  This
+    object keeps the tensors alive; when it goes, theirs is any dropped tensor's
+    memory, also for calls on other streams that still run."""
     _fields_ = [("type", ctypes.c_int), ("kv_heads", ctypes.c_int), ("head_dim", ctypes.c_int),
                 ("page_tokens", ctypes.c_int), ("n_pages", ctypes.c_int64), ("k", ctypes.c_void_p),
                 ("v", ctypes.c_void_p)]

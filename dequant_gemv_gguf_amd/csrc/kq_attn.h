@@ -38,10 +38,11 @@
 // numbers the one of both low limbs is left out (2^-22).
 //
 // Measured (MI355X, 64 query heads, 8 kv heads, head size 128): one request of
-// 131072 fp16 tokens 90 us (6.0 TB/s of K and V), of 524288 327 us (6.6 TB/s); 64
-// requests of up to 32768 Q8_0 tokens 287 us (5.5 TB/s); one of 37 tokens 5.8 us;
-// eight rows of 4 requests of up to 16384 Q8_0 tokens 59 us, of the kernel's 50
-// the vector units work 42 % and the matrix units 18 %.
+// 131072 fp16 tokens 90 to 94 us (5.7 to 6.0 TB/s of K and V); 64 requests of up to
+// 32768 Q8_0 tokens 289 us (5.4 TB/s); one of 37 tokens 5.8 us; eight rows of 4
+// requests of up to 16384 Q8_0 tokens 57 us, of the kernel's 49 the vector units
+// work 43 % and the matrix units 18 %; of 8 of 4096 tokens 45 us (fp16) and 44;
+// eight rows of 4 of 4096, 8 query heads and one kv head of 256, 30 and 33.
 #pragma once
 
 #include "kq_kv.h"

@@ -15,7 +15,8 @@ using namespace kq::kv;
 // heads of 64 15.1 -> 16.5).
 constexpr double KEPT_BYTES = 128e6;
 
-// The split of a call.  Returns the row tiles a wave.
+// The split of a call.  Returns the row tiles a wave.  (Measured with 64 query and 8 kv heads of 128 where nothing else is
+// said; heads of other sizes and numbers follow the same rules.)
 //  * Rows: up to 16 are one row tile; more, two tiles a wave (heads of up to 128) and up to 64 rows a work-group, whose
 //    four waves share the rows first, then the keys (8 rows of 8 requests of 4096 fp16 tokens: one tile a wave 55 us, two
 //    45).
@@ -26,12 +27,12 @@ constexpr double KEPT_BYTES = 128e6;
 //    13.2 against 10.2 (in pieces of 4; of 8 11.2); 8 of 512 10.5 against 12.5; 20 of 1024 17.5 against 23.4; 56 of 1536
 //    57 against 72, 56 of 64 to 1536 35 against 41, 40 of them 34 against 30; 8 rows of one request of 512 20 against 17.
 //  * Where it leaves each request two pieces or more on average, as many pieces as work-groups run at once and no more
-//    (3 on each of 256 compute units, by their registers; with 30 % more, one request of 131072 tokens 111 us instead of
-//    91, 8 rows of 8 requests of 4096 55 instead of 45, 32 requests of up to 8192 60 instead of 61).  Larger batches take
-//    up to four times that, 64 tiles a piece, so that the requests' lengths even out (64 requests of up to 32768 Q8_0
-//    tokens 145 us, in one round 164).  Contexts of up to 256 tiles do so past 1.5 pieces only (64 requests of 8192 fp16
-//    tokens: 96 pieces a head 325 us, 160 362; of up to 8192 89 and 91), but not rows of two tiles a wave (40 requests of
-//    4096 Q8_0 tokens and 8 rows: 64 pieces 211 us, 104 166).
+//    (3 on each of 256 compute units, by their registers; with 30 % more, one request of 131072 tokens 113 us instead of
+//    94, 8 rows of 8 requests of 4096 55 instead of 45).  Larger batches take up to four times that, 64 tiles a piece, so
+//    that the requests' lengths even out (64 requests of up to 16384 fp16 tokens 318 us, in one round 322).  Contexts of up
+//    to 256 tiles do so past 1.5 pieces only (64 requests of 8192 fp16 tokens: 96 pieces a head 325 us, 160 362; of up to
+//    8192 89 and 91), but not rows of two tiles a wave (40 requests of 4096 Q8_0 tokens and 8 rows: 64 pieces 211 us, 104
+//    166).
 static int attn_split(const kqkv_cache *c, int B, int max_q, int64_t max_ctx, int q_heads, int window, Attn *a) {
     a->group = q_heads / c->kv_heads;
     a->rows_cap = a->group * max_q;

@@ -146,8 +146,11 @@ typedef struct kqkv_rope {
  * nearest (beyond the fp16 range: infinities).  A Q8_0 block of 32 values x has
  * the scale s = fp16(max|x| * (1 / 127)), reciprocal and product rounded to
  * fp32, at most 65504, and the quants rint(x / s), -127..127 (0 when s is 0); a
- * block with an infinity or a NaN gets a NaN scale.  When two tokens name the same slot, either's values or a
- * mixture stay there.  0 <= T < 2^23, q_heads <= 1024. */
+ * block with an infinity or a NaN gets a NaN scale.  (GGUF's quantiser divides by
+ * 127 and makes the quants from that quotient unrounded: about one scale in 10^6
+ * is its neighbour, and quants near a half step differ.)  When two tokens name
+ * the same slot, either's values or a mixture stay there.  0 <= T < 2^23,
+ * q_heads <= 1024. */
 int kqkv_rope_store(const kqkv_cache *cache, const kqkv_rope *rope, int T, const int32_t *pos, int64_t pos_stride,
                     const int32_t *slots, int q_heads, const float *q, int64_t ldq, float *q_out, int64_t ldq_out,
                     const float *k, int64_t ldk, const float *v, int64_t ldv, void *stream);
@@ -184,8 +187,9 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
  *              rows past T are never touched
  *   workspace  kqkv_attn_workspace_bytes, 16-B aligned; scratch that needs no
  *              preparation and keeps nothing between calls
- * A page outside [0, n_pages), or a length past table_stride * P (or 2^31 - 64), takes its
- * tokens out of the sum and sets *err_flag; a negative length counts as 0.
+ * A page outside [0, n_pages), or a length past table_stride * P (or 2^31 - 64),
+ * takes its tokens out of the sum and sets *err_flag; a negative length counts as
+ * 0.
  * Accumulation is fp32; q and the weights enter the matrix instructions as two
  * fp16 limbs (22 bits, weights no finer than 2^-31 of their row's largest), the
  * cached values as they are.  |scale * q| is to stay below 2^100.  What a row does
@@ -193,9 +197,9 @@ size_t kqkv_attn_workspace_bytes(const kqkv_cache *cache, int B, int max_q, int6
  * value that it sees, and values that a Q8_0 cache holds past the fp16 range
  * (65504), give infinities or NaN (an infinite key also where its weight would be
  * 0).  Reruns are bit-identical; a request's bits may depend on the other
- * requests' lengths (they set where its tokens are split).  1 <= B <= 4096, q_heads a multiple
- * of kv_heads, at most 1024, B * q_heads * max_q < 2^24, 0 <= T < 2^24,
- * window >= 0, scale finite. */
+ * requests' lengths (they set where its tokens are split).  1 <= B <= 4096,
+ * q_heads a multiple of kv_heads, at most 1024, B * q_heads * max_q < 2^24,
+ * 0 <= T < 2^24, window >= 0, scale finite. */
 int kqkv_attn(const kqkv_cache *cache, int B, int max_q, int64_t max_ctx, const int32_t *ctx_len,
               const int32_t *seq_start, const int32_t *table, int64_t table_stride, int q_heads, int T,
               const float *q, int64_t ldq, float scale, int window, float *out, int64_t ldo,
