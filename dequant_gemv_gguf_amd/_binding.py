@@ -1,5 +1,5 @@
-"""ctypes marshalling for libkqgemv.so (see include/kqgemv.h and include/kqkv.h
-for semantics)."""
+"""ctypes marshalling for libkqgemv.so (see include/kqgemv.h, include/kqkv.h and
+include/kqstep.h for semantics)."""
 import ctypes
 import os
 
@@ -7,6 +7,8 @@ KQ_TYPE_Q4_0, KQ_TYPE_Q8_0, KQ_TYPE_Q2_K, KQ_TYPE_Q3_K = 2, 8, 10, 11
 KQ_TYPE_Q4_K, KQ_TYPE_Q5_K, KQ_TYPE_Q6_K = 12, 13, 14
 KQKV_F16, KQKV_Q8_0 = 1, 8
 KQKV_ROPE_HALVES, KQKV_ROPE_PAIRS = 0, 1
+KQSTEP_SOFTMAX, KQSTEP_SIGMOID = 0, 1
+KQSTEP_SILU, KQSTEP_GELU = 0, 1
 
 STATUS = {
     0: "KQ_OK", -1: "KQ_ERR_TYPE", -2: "KQ_ERR_SHAPE", -3: "KQ_ERR_M", -4: "KQ_ERR_NULL",
@@ -66,6 +68,34 @@ class KVRope(ctypes.Structure):
                 raise ValueError("KVRope: freq_factors must be rot_dims / 2 contiguous fp32 values on the device")
         self.device = _device_of("KVRope", (freq_factors,))
         self.tensors = (freq_factors,)
+
+
+class MoELayer(ctypes.Structure):
+    """struct kqstep_moe_layer (include/kqstep.h).  gate, up, down: contiguous device
+    tensors of the experts' packed matrices, router and bias fp32 ones, all on one
+    device, or int addresses.  This object keeps the tensors alive; when it goes,
+    theirs is any dropped tensor's memory, also for calls on other streams that
+    still run."""
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("hidden", ctypes.c_int64), ("inner", ctypes.c_int64),
+                ("gate_type", ctypes.c_int), ("down_type", ctypes.c_int), ("gate", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("down", ctypes.c_void_p), ("router", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("score", ctypes.c_int),
+                ("renorm", ctypes.c_int), ("scale", ctypes.c_float), ("act", ctypes.c_int)]
+
+    def __init__(self, E, k, hidden, inner, gate_type, gate, up, down_type, down, router, bias=None, score=KQSTEP_SOFTMAX,
+                 renorm=True, scale=1.0, act=KQSTEP_SILU):
+        E, hidden, inner = int(E), int(hidden), int(inner)
+        super().__init__(E, int(k), hidden, inner, int(gate_type), int(down_type), _addr(gate), _addr(up), _addr(down),
+                         _addr(router), _addr(bias), int(score), int(bool(renorm)), float(scale), int(act))
+        gate_row, down_row = (int(lib().kq_row_bytes(int(t), n)) for t, n in ((gate_type, hidden), (down_type, inner)))
+        for t, need, fp32 in ((gate, E * inner * gate_row, False), (up, E * inner * gate_row, False), (down, E * hidden * down_row, False),
+                              (router, 4 * E * hidden, True), (bias, 4 * E, True)):
+            if t is None or isinstance(t, int) or need < 0:
+                continue
+            if not t.is_cuda or not t.is_contiguous() or t.numel() * t.element_size() < need or (fp32 and str(t.dtype) != "torch.float32"):
+                raise ValueError("MoELayer: weights must be contiguous device tensors of at least %d bytes%s" %
+                                 (need, ", fp32" if fp32 else ""))
+        self.device = _device_of("MoELayer", (gate, up, down, router, bias))
+        self.tensors = (gate, up, down, router, bias)
 
 
 class KQError(RuntimeError):
@@ -135,6 +165,13 @@ def lib():
         L.kqkv_attn_workspace_bytes.restype = ctypes.c_size_t
         L.kqkv_attn.argtypes = [P, I, I, I64, P, P, P, I64, I, I, P, I64, ctypes.c_float, I, P, I64, P,
                                 ctypes.c_size_t, P, P]
+        L.kqstep_norm.argtypes = [I, I, I, P, I64, P, I64, P, I64, P, ctypes.c_float, P, I64, P, P]
+        L.kqstep_moe_workspace_bytes.argtypes = [P, I]
+        L.kqstep_moe_workspace_bytes.restype = ctypes.c_size_t
+        L.kqstep_moe.argtypes = [P, I, P, I64, P, I64, P, I64, P, P, P, ctypes.c_size_t, P]
+        L.kqstep_sample_workspace_bytes.argtypes = [I, I64]
+        L.kqstep_sample_workspace_bytes.restype = ctypes.c_size_t
+        L.kqstep_sample.argtypes = [I, I64, P, I64, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         _lib = L
     return _lib
 
@@ -579,3 +616,64 @@ def kqkv_attn(cache, B, max_q, max_ctx, ctx_len, seq_start, table, table_stride,
     _call(fn, (_lib or lib()).kqkv_attn, device,
           (_struct(cache), B, max_q, max_ctx, a[0], a[1], a[2], table_stride, q_heads, T, a[3], ldq, scale, window, a[4],
            ldo, a[-1] if workspace is not None else None, workspace_bytes, a[5] if err_flag is not None else None, stream))
+
+
+# ---- a step's other operators (include/kqstep.h) ----------------------------------
+# layer: a MoELayer.  Tensors or int addresses, checked as for the paged cache.
+
+def _some(tensors, dtypes, strides):
+    """The tensors that are given, with their types and strides (of those behind
+    the last type: any)."""
+    at = [i for i, t in enumerate(tensors) if t is not None]
+    return at, [tensors[i] for i in at], [dtypes[i] for i in at if i < len(dtypes)], [strides[i] for i in at]
+
+
+def _step_call(fn, f, stream, tensors, dtypes, strides, struct, args):
+    """f(*args(addresses)) on the tensors' device."""
+    given = [t for t in tensors if t is not None]
+    device, stream = _target(fn, stream, given[0] if given else None, given, struct)
+    if len(given) == len(tensors):
+        a = _addresses(fn, device, dtypes, tensors, strides)
+    else:
+        at, given, dtypes, strides = _some(tensors, dtypes, strides)
+        a = [None] * len(tensors)
+        for i, p in zip(at, _addresses(fn, device, dtypes, given, strides)):
+            a[i] = p
+    _call(fn, f, device, args(a, stream))
+
+
+def kqstep_norm(T, heads, n, x, ldx, add, ldadd, sum, ldsum, weight, eps, y, ldy, y8=None, stream=None):
+    if _torch_c is None:
+        _load_torch()
+    f = _float32
+    _step_call("kqstep_norm", (_lib or lib()).kqstep_norm, stream, (x, add, sum, weight, y, y8), [f, f, f, f, f],
+               (ldx, ldadd, ldsum, None, ldy, None), None,
+               lambda a, s: (T, heads, n, a[0], ldx, a[1], ldadd, a[2], ldsum, a[3], eps, a[4], ldy, a[5], s))
+
+
+def kqstep_moe_workspace_bytes(layer, T):
+    return int(lib().kqstep_moe_workspace_bytes(_struct(layer), int(T)))
+
+
+def kqstep_moe(layer, T, x, ldx, add, ldadd, y, ldy, ids=None, weights=None, workspace=None, workspace_bytes=0, stream=None):
+    if _torch_c is None:
+        _load_torch()
+    f = _float32
+    _step_call("kqstep_moe", (_lib or lib()).kqstep_moe, stream, (x, y, add, ids, weights, workspace), [f, f, f, _int32, f],
+               (ldx, ldy, ldadd, None, None, None), layer,
+               lambda a, s: (_struct(layer), T, a[0], ldx, a[2], ldadd, a[1], ldy, a[3], a[4], a[5], workspace_bytes, s))
+
+
+def kqstep_sample_workspace_bytes(M, V):
+    return int(lib().kqstep_sample_workspace_bytes(int(M), int(V)))
+
+
+def kqstep_sample(M, V, logits, ld, temperature, top_k, top_p, min_p, u, tokens, probs=None, workspace=None, workspace_bytes=0,
+                  stream=None):
+    if _torch_c is None:
+        _load_torch()
+    f, i = _float32, _int32
+    _step_call("kqstep_sample", (_lib or lib()).kqstep_sample, stream,
+               (logits, u, tokens, temperature, top_k, top_p, min_p, probs, workspace), [f, f, i, f, i, f, f, f],
+               (ld, None, None, None, None, None, None, None, None), None,
+               lambda a, s: (M, V, a[0], ld, a[3], a[4], a[5], a[6], a[1], a[2], a[7], a[8], workspace_bytes, s))

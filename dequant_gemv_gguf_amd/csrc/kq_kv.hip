@@ -300,28 +300,6 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The scale and the quants' divisor of a block whose largest magnitude has the
-// bits m (magnitudes order like integers, NaN on top).  The 127th is a product
-// with the reciprocal: beside the rounding to fp16 the difference to a quotient
-// is nothing (2^-23 of it), but it decides about one block in 10^6 that lies
-// between two fp16 scales, so it is part of the format.
-struct Scale {
-    float s;               // fp16, as stored
-    bool none;             // every quant is 0
-};
-__device__ __forceinline__ Scale block_scale(u32 m) {
-    const bool bad = m >= 0x7F800000u;
-    const float s = (float)(_Float16)fminf(__builtin_bit_cast(float, m) * (1.f / 127.f), 65504.f);
-    return Scale{bad ? __builtin_nanf("") : s, bad || s == 0.f};
-}
-__device__ __forceinline__ int quant(float x, const Scale &s) {
-    return s.none ? 0 : (int)fmaxf(-127.f, fminf(127.f, rintf(x / s.s)));
-}
-__device__ __forceinline__ u32 magnitude(float x) { return __builtin_bit_cast(u32, x) & 0x7FFFFFFFu; }
-__device__ __forceinline__ u32 magnitude(f4 x) {
-    return max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
-}
-
 // 4 elements at d of one head's row of one token into K.
 template <bool Q8>
 __device__ __forceinline__ void store_k4(const Cache &c, uint8_t *head, u32 t, int d, f4 x, u32 block_max) {
