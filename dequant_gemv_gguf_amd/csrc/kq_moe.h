@@ -15,7 +15,7 @@ struct Moe {
     const uint8_t *gate, *up, *down;
     float *y;
     int32_t *ids;               // [T][k], the caller's or scratch
-    float *weights;             // [T][k]
+    float *weights;             // [T][k], or NULL
     double *logits;             // [T][E] scratch
     float *inner;               // [T][k][inner] scratch
     int64_t ldx, ldadd, ldy;

@@ -20,28 +20,32 @@ KQ_MOE_LAUNCHERS(extern template, T_Q6_K)
 // bits, the sums' order does not depend on T.
 constexpr int ROUTER_THREADS = 256;
 
+// NT >= T tokens: their rows are asked for together (past T: the last one's again).
+template <int NT>
 __global__ __launch_bounds__(ROUTER_THREADS) void router_kernel(const Moe a) {
-    __shared__ double waves[MOE_TOKENS][ROUTER_THREADS / 64];
+    __shared__ double waves[NT][ROUTER_THREADS / 64];
     const int e = blockIdx.x, tid = threadIdx.x;
-    const float *w = a.router + (int64_t)e * a.hidden;
-    double acc[MOE_TOKENS] = {};
+    const float *w = a.router + (int64_t)e * a.hidden, *x[NT];
+    double acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        x[t] = a.x + min(t, a.T - 1) * a.ldx;
+        acc[t] = 0.0;
+    }
     for (int i = 4 * tid; i < a.hidden; i += 4 * ROUTER_THREADS) {
         const f4 v = *(const f4 *)(w + i);
+        f4 xs[NT];
 #pragma unroll
-        for (int t = 0; t < MOE_TOKENS; ++t) {
-            if (t < a.T) {
-                const f4 x = *(const f4 *)(a.x + t * a.ldx + i);
+        for (int t = 0; t < NT; ++t) xs[t] = *(const f4 *)(x[t] + i);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[t] = fma((double)v[j], (double)x[j], acc[t]);
-            }
-        }
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[t] = fma((double)v[j], (double)xs[t][j], acc[t]);
     }
 #pragma unroll
-    for (int t = 0; t < MOE_TOKENS; ++t) {
-        if (t < a.T) {
-            const double s = sum_d<64>(acc[t]);
-            if ((tid & 63) == 0) waves[t][tid >> 6] = s;
-        }
+    for (int t = 0; t < NT; ++t) {
+        const double s = sum_d<64>(acc[t]);
+        if ((tid & 63) == 0) waves[t][tid >> 6] = s;
     }
     __syncthreads();
     if (tid < a.T) {
@@ -67,14 +71,13 @@ static int layer_check(const kqstep_moe_layer *l, int64_t *gate_bytes, int64_t *
 
 static size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// The parts of a workspace: logits, inner rows, ids, weights.
-struct MoeSpace { size_t inner, ids, weights, end; };
+// The parts of a workspace: logits, inner rows, ids.
+struct MoeSpace { size_t inner, ids, end; };
 static MoeSpace moe_space(const kqstep_moe_layer *l, int T) {
     MoeSpace s;
     s.inner = round16((size_t)T * l->E * sizeof(double));
     s.ids = s.inner + round16((size_t)T * l->k * l->inner * sizeof(float));
-    s.weights = s.ids + round16((size_t)T * l->k * sizeof(int32_t));
-    s.end = s.weights + round16((size_t)T * l->k * sizeof(float));
+    s.end = s.ids + round16((size_t)T * l->k * sizeof(int32_t));
     return s;
 }
 
@@ -123,7 +126,7 @@ int kqstep_moe(const kqstep_moe_layer *layer, int T, const float *x, int64_t ldx
     a.down = (const uint8_t *)layer->down;
     a.y = y;
     a.ids = ids ? ids : (int32_t *)(ws + s.ids);
-    a.weights = weights ? weights : (float *)(ws + s.weights);
+    a.weights = weights;
     a.logits = (double *)ws;
     a.inner = (float *)(ws + s.inner);
     a.ldx = ldx;
@@ -141,7 +144,8 @@ int kqstep_moe(const kqstep_moe_layer *layer, int T, const float *x, int64_t ldx
     a.renorm = layer->renorm;
     a.act = layer->act;
     hipStream_t st = (hipStream_t)stream;
-    hipLaunchKernelGGL(router_kernel, dim3((unsigned)a.E), dim3(ROUTER_THREADS), 0, st, a);
+    hipLaunchKernelGGL(T == 1 ? router_kernel<1> : T == 2 ? router_kernel<2> : T <= 4 ? router_kernel<4> : router_kernel<8>, dim3((unsigned)a.E),
+                       dim3(ROUTER_THREADS), 0, st, a);
     if ((r = kv::launched())) return r;
     if ((r = with_type(layer->gate_type, [&](auto tag) { return launch_gate_up<decltype(tag)::value>(a, st); }))) return r;
     return with_type(layer->down_type, [&](auto tag) { return launch_down<decltype(tag)::value>(a, st); });
