@@ -1,12 +1,25 @@
 // kq_sample.hip -- a token for each row of logits (include/kqstep.h).
 //
 // Everything that the filters leave is a leading part of the tokens in the order
-// of (logit descending, index ascending), so a filter is a place in that order:
-// a logit's key (its bits, made to order like integers) and how many of the
-// tokens with that very key stay.  A place is found digit by digit of the key,
-// from the counts (top_k) or the summed weights (top_p) of the tokens that share
-// its digits so far.  Weights are 64-bit integers, multiples of 2^-42: sums of
-// them are exact, so that it does not matter in which order LDS atomics add them.
+// of (logit descending, index ascending), so a filter is a place in that order.
+//
+// Bound: for few rows the chain of two launches, for many the arithmetic of the
+// first (a 64-bit power of two a logit) and HBM.  Two launches:
+//  * chunk_kernel, a work-group a chunk of 8192 tokens of a row: the chunk's first
+//    token of the order, and a histogram over bins of an eighth of an octave of
+//    weight (counts and weights of 512 bins below the chunk's largest).  The bins
+//    lie at fixed places of l / t, so chunks need not know of each other.  A bin's
+//    count and the sum of its weights, integers, share one 64-bit LDS atomic: the
+//    sums do not depend on the order.
+//  * row_kernel, a work-group a row: the chunks' histograms added up give the bin
+//    in which each filter ends.  One scan of the row gathers that bin's tokens (with
+//    top_k: those of all bins down to it) in LDS, where the place is found digit by
+//    digit of the logits' keys.  The chunks' kept weights say which chunk holds the
+//    token; its logits are gone over once more.  Where the gathered tokens do not
+//    fit in LDS (thousands of equal logits, a very high temperature), the digits are
+//    found over the row itself.
+// Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
+// the row's largest.
 #include "kq_step.h"
 
 #include <cmath>
@@ -14,21 +27,29 @@
 namespace kq {
 namespace step {
 
+constexpr int CHUNK_THREADS = 512, CHUNK = 8192;
 constexpr int ROW_THREADS = 1024, ROW_WAVES = ROW_THREADS / 64;
-constexpr int CHUNK = 4096;                       // tokens whose kept weight is summed apart
 constexpr int MAX_V = 1 << 20, MAX_CHUNKS = MAX_V / CHUNK;
-constexpr double ONE = 4398046511104.0;           // 2^42, the weight of the largest logit
+constexpr int BINS = 512, OCTAVE = 8;             // bins, and those of an octave
+constexpr int COUNT_SHIFT = 50;                   // a bin: count, and below it the sum of weights
+constexpr int LIST = 5888;                      // (all of row_kernel's LDS below 64 KB)
+constexpr int SLICE = 32768;                      // rows of a launch
+static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
 
 struct Sample {
     const float *logits, *temperature, *top_p, *min_p, *u;
     const int32_t *top_k;
     int32_t *tokens;
     float *probs;
+    u64 *tops, *hist;       // [row][chunk], [row][chunk][BINS]
     int64_t ld;
-    int V;
+    int V, chunks, row0;
 };
 
-// The key of a logit: 0 for what is never taken.  (+ 0: the zeros are equal.)
+typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// The key of a logit, in the logits' order: 0 for what is never taken.  (+ 0: the
+// zeros are equal.)  A token: its key, and the lower index first.
 __device__ __forceinline__ u32 key_of(float l) {
     const u32 b = __builtin_bit_cast(u32, l + 0.f);
     return l > -__builtin_inff() ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
@@ -36,17 +57,42 @@ __device__ __forceinline__ u32 key_of(float l) {
 __device__ __forceinline__ float logit_of(u32 key) {
     return __builtin_bit_cast(float, key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
 }
+__device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 | (u32)~i; }
 
-// Weight of a key in a row whose largest key is `top`.
-struct Weigh {
-    u32 top;
-    double max, t;
-    __device__ __forceinline__ u64 operator()(u32 key) const {
-        if (key == top) return (u64)ONE;
-        const double d = (double)logit_of(key) - max;
-        return key && d > -__builtin_inf() ? (u64)rint(exp(d / t) * ONE) : 0;
+// Where a logit's weight lies: the bin (counted upwards), its octave, and the
+// mantissa, 2^35 .. 2^36.  An infinite logit lies above all others.
+struct Scale {
+    double eighths;         // of an octave, per logit: 8 log2(e) / t
+    __device__ __forceinline__ double at(float l) const {
+        return l == __builtin_inff() ? __builtin_inf() : (double)l * eighths;
+    }
+    __device__ __forceinline__ double bin(float l) const { return floor(at(l)); }
+    __device__ __forceinline__ u64 mantissa(float l) const {
+        double y = at(l) * 0.125;
+        y -= floor(y);
+        const double x = l == __builtin_inff() ? 0.0 : y * 0.6931471805599453;
+        // e^x for 0 <= x < log 2: its series to x^13 / 13! (2^-40 is left)
+        double p = 1.0 / 6227020800.0;
+        p = fma(p, x, 1.0 / 479001600.0);
+        p = fma(p, x, 1.0 / 39916800.0);
+        p = fma(p, x, 1.0 / 3628800.0);
+        p = fma(p, x, 1.0 / 362880.0);
+        p = fma(p, x, 1.0 / 40320.0);
+        p = fma(p, x, 1.0 / 5040.0);
+        p = fma(p, x, 1.0 / 720.0);
+        p = fma(p, x, 1.0 / 120.0);
+        p = fma(p, x, 1.0 / 24.0);
+        p = fma(p, x, 1.0 / 6.0);
+        p = fma(p, x, 0.5);
+        p = fma(p, x, 1.0);
+        p = fma(p, x, 1.0);
+        // to an integer: 2^52 in front leaves it in the low bits, rounded
+        return __builtin_bit_cast(u64, fma(p, 34359738368.0, 4503599627370496.0)) - 0x4330000000000000ull;
     }
 };
+__device__ __forceinline__ Scale scale_of(float t) { return Scale{t < __builtin_inff() ? 8.0 * 1.4426950408889634 / (double)t : 0.0}; }
+
+__device__ __forceinline__ float temperature_of(const Sample &a, int row) { return a.temperature ? a.temperature[row] : 1.f; }
 
 __device__ __forceinline__ u64 wave_max(u64 x) {
 #pragma unroll
@@ -56,218 +102,482 @@ __device__ __forceinline__ u64 wave_max(u64 x) {
     }
     return x;
 }
-__device__ __forceinline__ u64 wave_scan(u64 x, int lane) {      // inclusive
+template <class N> __device__ __forceinline__ N wave_scan(N x, int lane) {      // inclusive
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) {
-        const u64 o = (u64)__shfl_up((long long)x, i);
+        const N o = __shfl_up(x, i);
         if (lane >= i) x += o;
     }
     return x;
 }
 
-// A place in the order: tokens with a greater key, and the first `ties` of those
-// with this one.
-struct Place { u32 key, ties; };
-
-// One row, a work-group: each step goes over the whole row.
-__global__ __launch_bounds__(ROW_THREADS) void sample_kernel(const Sample a) {
-    __shared__ u64 hist[256], chunk_weight[MAX_CHUNKS], waves[ROW_WAVES];
-    __shared__ u32 chunk_ties[MAX_CHUNKS];
-    __shared__ u64 found[3];
-    const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+__global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
+    // two histograms, of the even and the odd lanes: half the lanes of a wave meet in a bin
+    __shared__ __align__(16) u64 hist[BINS][2];
+    __shared__ u64 waves[CHUNK_THREADS / 64];
+    constexpr int PER = CHUNK / CHUNK_THREADS / 4;
+    const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
-    const float t = a.temperature ? a.temperature[row] : 1.f;
-    // the first token of the order
-    u64 best = 0;
-    for (int i = tid; i < a.V; i += ROW_THREADS) {
-        const u64 x = (u64)key_of(l[i]) << 32 | (u32)~i;
-        best = x > best ? x : best;
+    const float t = temperature_of(a, row);
+    const int first = chunk * CHUNK + 4 * tid;
+    f4 v[PER];
+#pragma unroll
+    for (int p = 0; p < PER; ++p) {
+        const int i = first + p * 4 * CHUNK_THREADS;
+        if (i + 4 <= a.V) {
+            v[p] = *(const f4u *)(l + i);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[p][j] = i + j < a.V ? l[min(i + j, a.V - 1)] : -__builtin_inff();
+        }
     }
+    for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
+    u64 best = 0;
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const u64 x = token_of(key_of(v[p][j]), first + p * 4 * CHUNK_THREADS + j);
+            best = x > best ? x : best;
+        }
     best = wave_max(best);
-    if (lane == 0) waves[wave] = best;
+    if (lane == 0) waves[tid >> 6] = best;
     __syncthreads();
-    best = wave_max(waves[lane & (ROW_WAVES - 1)]);
+    best = wave_max(waves[lane & (CHUNK_THREADS / 64 - 1)]);
     const u32 top = (u32)(best >> 32);
-    const int first = (int)~(u32)best;
-    if (!top || !(t > 0.f)) {
+    const int64_t at = (int64_t)row * a.chunks + chunk;
+    if (tid == 0) a.tops[at] = best;
+    if (!top || !(t > 0.f)) return;
+    const Scale s = scale_of(t);
+    const float most = logit_of(top);
+    const double from = s.bin(most);
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = v[p][j];
+            if (x > -__builtin_inff()) {
+                const double d = from - s.bin(x);
+                const int b = x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
+                // (the last bin, 64 octaves below: its weights count as nothing)
+                const u64 w = b < BINS - 1 ? s.mantissa(x) : 0;
+                atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
+            }
+        }
+    __syncthreads();
+    for (int i = tid; i < BINS; i += CHUNK_THREADS) a.hist[at * BINS + i] = hist[i][0] + hist[i][1];
+}
+
+// What row_kernel shares between its threads.
+struct RowSpace {
+    u64 list[LIST];                 // gathered tokens
+    u64 weight[BINS];               // of the row's bins
+    double upto[BINS];              // summed weights up to and with a bin, in units of the top octave's mantissas
+    u32 count[BINS], counts[BINS];  // tokens of a bin, and up to and with it
+    u64 digit_weight[256];
+    u32 digit_count[256];
+    u64 chunk_list[MAX_CHUNKS];     // kept weight of a chunk's gathered tokens
+    double chunk_sum[MAX_CHUNKS];
+    u64 waves[ROW_WAVES];
+    double waves_d[ROW_WAVES];
+    u64 found[4];
+    double picked[2];
+    int n, low, high;
+};
+
+// One row of logits as every thread of row_kernel sees it.
+struct Row {
+    const float *l;
+    Scale s;
+    u64 best;               // the first token of the order
+    double from;            // its bin
+    int V, phase;           // phase: from mod OCTAVE
+    double least;           // min_p: the least weight kept
+    // bin b (downwards from the top's) is this many octaves below the top's octave
+    __device__ __forceinline__ int octaves(int b) const { return (b + OCTAVE - 1 - phase) >> 3; }
+    __device__ __forceinline__ int bin(float x) const {
+        if (x == logit_of((u32)(best >> 32))) return 0;
+        const double d = from - s.bin(x);
+        return d < BINS ? (int)d : BINS;
+    }
+    // in units of the top octave's mantissas
+    __device__ __forceinline__ double weight(float x) const {
+        const int b = bin(x);
+        return b < BINS - 1 ? ldexp((double)s.mantissa(x), -octaves(b)) : 0.0;
+    }
+    __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
+};
+
+// The shortest leading part of the tokens that `each` goes over (descending) of
+// which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the whole
+// sum): the tokens from *least on.  Returns the part's sum.
+template <bool WEIGHTS, class Each> __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 want, u64 *least) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    u64 prefix = 0, before = 0, sum = 0;
+    for (int shift = 56; shift >= 0; shift -= 8) {
+        __syncthreads();
+        if (tid < 256) {
+            m.digit_weight[tid] = 0;
+            m.digit_count[tid] = 0;
+        }
+        __syncthreads();
+        each([&](u64 token, u64 w) {
+            if (shift < 56 && token >> (shift + 8) != prefix) return;
+            const int d = (int)(token >> shift) & 255;
+            atomicAdd(&m.digit_count[d], 1u);
+            if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], w);
+        });
+        __syncthreads();
+        if (tid < 64) {
+            // 4 digits a lane, descending
+            u64 d[4], s = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int digit = 255 - (4 * lane + i);
+                d[i] = WEIGHTS ? m.digit_weight[digit] : m.digit_count[digit];
+                s += d[i];
+            }
+            const u64 upto = (u64)wave_scan((long long)s, lane);
+            const u64 reach = __ballot(before + upto >= want);
+            if (lane == (reach ? __builtin_ctzll(reach) : 63)) {
+                u64 b = before + upto - s;
+                int i = 0;
+                for (; i < 3 && b + d[i] < want; ++i) b += d[i];
+                m.found[0] = (u64)(255 - (4 * lane + i));
+                m.found[1] = b;
+                m.found[2] = b + d[i];
+                m.found[3] = m.digit_count[255 - (4 * lane + i)];
+            }
+        }
+        __syncthreads();
+        prefix = prefix << 8 | m.found[0];
+        before = m.found[1];
+        sum = m.found[2];
+        if (m.found[3] == 1 && shift) {     // one token has these digits: that one
+            each([&](u64 token, u64) {
+                if (token >> shift == prefix) m.found[3] = token;
+            });
+            __syncthreads();
+            prefix = m.found[3];
+            break;
+        }
+    }
+    *least = prefix;
+    return sum;
+}
+
+__device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
+    const int tid = threadIdx.x, lane = tid & 63;
+    x = (u64)wave_scan((long long)x, lane);
+    __syncthreads();
+    if (lane == 63) m.waves[tid >> 6] = x;
+    __syncthreads();
+    x = 0;
+    for (int w = 0; w < ROW_WAVES; ++w) x += m.waves[w];
+    return x;
+}
+
+__global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
+    __shared__ RowSpace m;
+    const int row = a.row0 + blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const float t = temperature_of(a, row);
+    const u64 *tops = a.tops + (int64_t)row * a.chunks;
+    u64 best = 0;
+    for (int c = lane; c < a.chunks; c += 64) best = tops[c] > best ? tops[c] : best;
+    best = wave_max(best);
+    if (!(best >> 32) || !(t > 0.f)) {
         if (tid == 0) {
-            a.tokens[row] = top ? first : -1;
-            if (a.probs) a.probs[row] = top ? 1.f : 0.f;
+            a.tokens[row] = best >> 32 ? (int)~(u32)best : -1;
+            if (a.probs) a.probs[row] = best >> 32 ? 1.f : 0.f;
         }
         return;
     }
-    const Weigh weigh = {top, (double)logit_of(top), (double)t};
-
-    // The shortest leading part of `in` of which `by` (1: tokens, 2: weights)
-    // sums to at least `want`, and its sum of weights.
-    auto cut = [&](Place in, bool weights, u64 want, Place *out, u64 *weight) {
-        u32 prefix = 0;
-        u64 before = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            __syncthreads();
-            if (tid < 256) hist[tid] = 0;
-            __syncthreads();
-            for (int i = tid; i < a.V; i += ROW_THREADS) {
-                const u32 key = key_of(l[i]);
-                if (key <= in.key || (shift < 24 && key >> (shift + 8) != prefix)) continue;
-                atomicAdd((unsigned long long *)&hist[(key >> shift) & 255], weights ? weigh(key) : 1ull);
-            }
-            __syncthreads();
-            if (tid < 64) {
-                // 4 digits a lane, descending
-                u64 d[4], s = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u32 digit = 255 - (4 * lane + i);
-                    d[i] = hist[digit];
-                    if (in.ties && (shift == 24 || in.key >> (shift + 8) == prefix) && ((in.key >> shift) & 255) == digit)
-                        d[i] += in.ties * (weights ? weigh(in.key) : 1ull);
-                    s += d[i];
-                }
-                const u64 upto = wave_scan(s, lane);
-                const u64 reach = __ballot(before + upto >= want);
-                // (the sum over all digits reaches `want`, unless it is 0)
-                const int at = reach ? __builtin_ctzll(reach) : 63;
-                if (lane == at) {
-                    u64 sum = before + upto - s;
-                    int i = 0;
-                    for (; i < 3 && sum + d[i] < want; ++i) sum += d[i];
-                    found[0] = (u64)(255 - (4 * lane + i));
-                    found[1] = sum;
-                }
-            }
-            __syncthreads();
-            prefix = prefix << 8 | (u32)found[0];
-            before = found[1];
-        }
-        // tokens of this key: one tokens's worth after the other
-        const u64 each = weights ? weigh(prefix) : 1;
-        const u64 need = want > before ? want - before : 0;
-        u64 n = each ? (need + each - 1) / each : 0;
-        n = n ? n : 1;
-        if (prefix == in.key && n > in.ties) n = in.ties;
-        out->key = prefix;
-        out->ties = (u32)n;
-        *weight = before + n * each;
-        __syncthreads();
-    };
-
-    Place kept = {0, 0};                          // all tokens
-    u64 unused;
+    Row r;
+    r.l = a.logits + row * a.ld;
+    r.s = scale_of(t);
+    r.best = best;
+    r.V = a.V;
+    const float most = logit_of((u32)(best >> 32));
+    r.from = r.s.bin(most);
+    r.phase = most == __builtin_inff() ? OCTAVE - 1 : (int)(r.from - OCTAVE * floor(r.from / OCTAVE));
+    const float min_p = a.min_p ? a.min_p[row] : 0.f;
+    r.least = min_p > 0.f ? (double)min_p * (double)r.s.mantissa(most) : 0.0;
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const float top_p = a.top_p ? a.top_p[row] : 1.f;
-    if (top_k > 0 && top_k < a.V) {
-        // (tokens at -infinity are not counted: fewer may remain than top_k)
-        u64 n = 0;
-        for (int i = tid; i < a.V; i += ROW_THREADS) n += key_of(l[i]) != 0;
-        n = wave_scan(n, lane);
-        __syncthreads();
-        if (lane == 63) waves[wave] = n;
-        __syncthreads();
-        n = 0;
-        for (int w = 0; w < ROW_WAVES; ++w) n += waves[w];
-        if ((u64)top_k < n) cut(Place{0, 0}, false, (u64)top_k, &kept, &unused);
-    }
 
-    // Sums over the chunks of what a place keeps; returns the whole sum.
-    double min_weight = a.min_p ? (double)a.min_p[row] * ONE : 0.0;
-    min_weight = min_weight > 0.0 ? min_weight : 0.0;
-    auto keep = [&](u32 key, u64 w) { return key == top || (double)w >= min_weight; };
-    const int chunks = (a.V + CHUNK - 1) / CHUNK;
-    auto sums = [&](const Place &p, bool filter) {
-        __syncthreads();
-        for (int c = tid; c < chunks; c += ROW_THREADS) {
-            chunk_weight[c] = 0;
-            chunk_ties[c] = 0;
+    // the row's histogram
+    for (int b = tid; b < BINS; b += ROW_THREADS) {
+        m.weight[b] = 0;
+        m.count[b] = 0;
+    }
+    if (tid == 0) {
+        m.n = 0;
+        m.low = BINS;
+        m.high = -1;
+    }
+    for (int c = tid; c < MAX_CHUNKS; c += ROW_THREADS) m.chunk_list[c] = 0;
+    __syncthreads();
+    // bins that chunk c's are below the row's (BINS: it has none)
+    auto below = [&](int c) {
+        const u32 key = (u32)(tops[c] >> 32);
+        if (!key) return BINS;
+        const float x = logit_of(key);
+        const double d = x == most ? 0.0 : r.from - r.s.bin(x);
+        return d < BINS ? (int)d : BINS;
+    };
+    for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+        const int off = below(c);
+        if (!(tops[c] >> 32)) continue;
+        const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
+        u64 x[BINS / 64];
+#pragma unroll
+        for (int i = 0; i < BINS / 64; ++i) x[i] = h[lane + 64 * i];
+#pragma unroll
+        for (int i = 0; i < BINS / 64; ++i) {
+            const int d = lane + 64 * i, b = min(d + off, BINS - 1);
+            if (!x[i]) continue;
+            atomicAdd(&m.count[b], (u32)(x[i] >> COUNT_SHIFT));
+            if (b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], x[i] & ((1ull << COUNT_SHIFT) - 1));
         }
-        __syncthreads();
-        for (int i = tid; i < a.V; i += ROW_THREADS) {
-            const u32 key = key_of(l[i]);
-            if (key > p.key) {
-                const u64 w = weigh(key);
-                if (w && (!filter || keep(key, w))) atomicAdd((unsigned long long *)&chunk_weight[i / CHUNK], w);
-            } else if (key == p.key) {
-                atomicAdd(&chunk_ties[i / CHUNK], 1u);
+    }
+    __syncthreads();
+    {
+        // sums over the bins from the top
+        u32 n = 0;
+        double w = 0.0;
+        if (tid < BINS) {
+            n = (u32)wave_scan((int)m.count[tid], lane);
+            w = wave_scan(ldexp((double)m.weight[tid], -r.octaves(tid)), lane);
+            if (lane == 63) {
+                m.waves[wave] = n;
+                m.waves_d[wave] = w;
             }
         }
         __syncthreads();
+        if (tid < BINS) {
+            for (int v = 0; v < wave; ++v) {
+                n += (u32)m.waves[v];
+                w += m.waves_d[v];
+            }
+            m.counts[tid] = n;
+            m.upto[tid] = w;
+        }
+        __syncthreads();
+    }
+    const int total = (int)m.counts[BINS - 1];
+    const bool by_k = top_k > 0 && top_k < total, by_p = top_p < 1.f;
+    const double all = m.upto[BINS - 1], want_p = (double)(top_p > 0.f ? top_p : 0.f) * all;
+    // the bins in which top_k, top_p and min_p end
+    if (tid < BINS) {
+        const u32 n0 = tid ? m.counts[tid - 1] : 0, n1 = m.counts[tid];
+        const double w0 = tid ? m.upto[tid - 1] : 0.0, w1 = m.upto[tid];
+        if (by_k) {
+            if ((int)n0 < top_k && (int)n1 >= top_k) m.low = tid;
+        } else if (by_p && (tid == 0 || w0 < want_p) && (w1 >= want_p || tid == BINS - 1)) {
+            atomicMin(&m.low, tid);
+        }
+    }
+    __syncthreads();
+    int low = m.low;
+    bool one = !by_k && low < BINS;               // the tokens of bin `low` alone decide
+    if (!by_k && r.least > 0.0) {
+        // the bin of the least weight; those above it are kept whole
+        const double octave = floor(log2(r.least)) - 35.0, part = floor(OCTAVE * (log2(r.least) - 35.0 - octave));
+        const double b = r.phase - (OCTAVE * octave + part);
+        const int edge = b < 0.0 ? 0 : b < BINS ? (int)b : BINS - 1;
+        if (edge <= low) {
+            low = edge;
+            one = true;
+        }
+    }
+    const int high = by_k ? 0 : low;              // bins high .. low are gathered
+    const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
+    const bool scan = low < BINS, listed = scan && low < BINS - 1 && gathered <= LIST;
+    if (listed) {
+        // what can lie in these bins, and a little more
+        float lo = -__builtin_inff(), hi = __builtin_inff();
+        if (r.s.eighths > 0.0 && most < __builtin_inff()) {
+            const double x = (r.from - low) / r.s.eighths, y = (r.from - high + 1) / r.s.eighths;
+            lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
+            hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
+        }
+        constexpr int BATCH = 8;                  // pieces of 4 a thread between two writes
+        for (int i0 = 4 * tid; i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
+            u32 mask = 0;
+#pragma unroll
+            for (int p = 0; p < BATCH; ++p) {
+                const int i = i0 + 4 * ROW_THREADS * p;
+                if (i + 4 <= a.V) {
+                    const f4 x = *(const f4u *)(r.l + i);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mask |= (u32)(x[j] >= lo && x[j] <= hi) << (4 * p + j);
+                } else {
+                    for (int j = 0; j < 4; ++j)
+                        if (i + j < a.V) mask |= (u32)(r.l[i + j] >= lo && r.l[i + j] <= hi) << (4 * p + j);
+                }
+            }
+            while (mask) {
+                const int bit = __builtin_ctz(mask), i = i0 + 4 * ROW_THREADS * (bit >> 2) + (bit & 3);
+                mask &= mask - 1;
+                const float x = r.l[i];
+                const u32 key = key_of(x);
+                const int b = key ? r.bin(x) : BINS;
+                if (b < high || b > low) continue;
+                const int n = atomicAdd(&m.n, 1);
+                if (n < LIST) m.list[n] = token_of(key, i);
+            }
+        }
+        __syncthreads();
+    }
+    // Weights of gathered tokens as integers: with one bin in units of its octave's
+    // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
+    // 2^20 tokens have to fit the sum).
+    const int finer = listed ? 14 : 7, base = one && listed ? r.octaves(low) : 0;
+    auto integer = [&](u64 token) {
+        const float x = logit_of((u32)(token >> 32));
+        const int b = r.bin(x), down = r.octaves(b) - base;
+        return b < BINS - 1 && down < 64 ? (r.s.mantissa(x) << finer) >> down : 0ull;
     };
-    u64 total = 0;
-    if (top_p < 1.f) {
-        sums(kept, false);
-        for (int c = 0; c < chunks; ++c) total += chunk_weight[c];
-        total += kept.ties * weigh(kept.key);
-        const double want = ceil((double)top_p * (double)total);
-        cut(kept, true, want >= 1.0 ? (want < (double)total ? (u64)want : total) : 1, &kept, &unused);
+    auto each = [&](auto &&f) {
+        if (listed) {
+            for (int i = tid; i < min(m.n, LIST); i += ROW_THREADS) f(m.list[i]);
+        } else {
+            for (int i = tid; i < a.V; i += ROW_THREADS) {
+                const u32 key = key_of(r.l[i]);
+                if (key) f(token_of(key, i));
+            }
+        }
+    };
+    u64 least = 0;                                // the last token that top_k and top_p keep
+    if (scan) {
+        if (by_k) {
+            cut<false>(m, [&](auto &&f) { each([&](u64 token) { f(token, 1ull); }); }, (u64)top_k, &least);
+        }
+        if (by_p && !(one && listed)) {
+            // of what top_k leaves (of the whole row where its bin was not gathered)
+            u64 sum = 0;
+            each([&](u64 token) { sum += token >= least ? integer(token) : 0; });
+            sum = block_sum(m, sum);
+            const double want = ceil((double)(top_p > 0.f ? top_p : 0.f) * (double)sum);
+            const u64 from = least;
+            cut<true>(m, [&](auto &&f) { each([&](u64 token) { if (token >= from) f(token, integer(token)); }); },
+                      want < 1.0 ? 1 : want < (double)sum ? (u64)want : sum, &least);
+        } else if (by_p && low == m.low) {
+            // within the bin
+            u64 sum = 0;
+            each([&](u64 token) { sum += integer(token); });
+            sum = block_sum(m, sum);
+            const double want = ceil(ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer));
+            cut<true>(m, [&](auto &&f) { each([&](u64 token) { f(token, integer(token)); }); },
+                      want < 1.0 ? 1 : want < (double)sum ? (u64)want : sum, &least);
+        }
+        __syncthreads();
+        // kept weight of the gathered tokens, by chunk
+        each([&](u64 token) {
+            if (token < least) return;
+            const u64 w = integer(token);
+            if (w && r.keeps(token, ldexp((double)w, -base - finer)))
+                atomicAdd((unsigned long long *)&m.chunk_list[(int)~(u32)token / CHUNK], w);
+        });
+        __syncthreads();
     }
-    sums(kept, true);
-    // the chunk and the token in it
-    const u64 tie = kept.key && kept.ties ? weigh(kept.key) : 0;
-    const u64 tie_kept = kept.key && keep(kept.key, tie) ? tie : 0;
+    // and of the bins above them
+    const int whole = !scan ? BINS : one && listed ? low : 0;
+    for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+        double w = 0.0;
+        const int off = whole ? below(c) : BINS;
+        if (off < whole) {
+            const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
+#pragma unroll
+            for (int i = 0; i < BINS / 64; ++i) {
+                const int d = lane + 64 * i;
+                if (d + off < min(whole, BINS - 1)) w += ldexp((double)(h[d] & ((1ull << COUNT_SHIFT) - 1)), -r.octaves(d + off));
+            }
+        }
+        w = sum_d<64>(w);
+        if (lane == 0) m.chunk_sum[c] = w + ldexp((double)m.chunk_list[c], -base - finer);
+    }
+    __syncthreads();
+    // the chunk
+    if (wave == 0) {
+        constexpr int EACH = MAX_CHUNKS / 64;
+        double s[EACH], mine = 0.0;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            s[i] = EACH * lane + i < a.chunks ? m.chunk_sum[EACH * lane + i] : 0.0;
+            mine += s[i];
+        }
+        const double upto = wave_scan(mine, lane), sum = __shfl(upto, 63);
+        const float u = a.u[row];
+        const double at = (u > 0.f ? fmin((double)u, 1.0) : 0.0) * sum;
+        // the first lane whose sum passes `at`, else the last that has any weight
+        const u64 past = __ballot(upto > at && mine > 0.0), some = __ballot(mine > 0.0);
+        const int who = past ? __builtin_ctzll(past) : 63 - __builtin_clzll(some);
+        if (lane == who) {
+            double b = upto - mine;
+            int i = 0;
+            for (int j = 1; j < EACH; ++j)
+                if (s[j] > 0.0 && (s[i] <= 0.0 || b + s[i] <= at)) {
+                    b += s[i];
+                    i = j;
+                }
+            m.n = EACH * lane + i;
+            m.picked[0] = at - b;
+            m.picked[1] = sum;
+            m.low = a.V;
+            m.high = -1;
+        }
+    }
+    __syncthreads();
+    // its token
+    constexpr int EACH = CHUNK / ROW_THREADS;
+    const int first = m.n * CHUNK + EACH * tid;
+    const double at = m.picked[0], sum = m.picked[1];
+    double w[EACH], mine = 0.0;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        const int i = first + j;
+        const float x = i < a.V ? r.l[i] : -__builtin_inff();
+        const u32 key = key_of(x);
+        const u64 token = token_of(key, i);
+        w[j] = 0.0;
+        if (key && token >= least) {
+            const double v = r.weight(x);
+            if (r.keeps(token, v)) w[j] = v;
+        }
+        mine += w[j];
+    }
+    double upto = wave_scan(mine, lane);
+    if (lane == 63) m.waves_d[wave] = upto;
+    __syncthreads();
+    for (int v = 0; v < wave; ++v) upto += m.waves_d[v];
+    double b = upto - mine;
+    int at_least = a.V, last = -1;
+#pragma unroll
+    for (int j = 0; j < EACH; ++j) {
+        b += w[j];
+        if (w[j] > 0.0) {
+            last = first + j;
+            if (b > at && at_least == a.V) at_least = first + j;
+        }
+    }
+    if (at_least < a.V) atomicMin(&m.low, at_least);
+    if (last >= 0) atomicMax(&m.high, last);
+    __syncthreads();
     if (tid == 0) {
-        u64 all = 0, ties = 0;
-        for (int c = 0; c < chunks; ++c) {
-            const u64 n = ties < kept.ties ? min((u64)chunk_ties[c], kept.ties - ties) : 0;
-            ties += chunk_ties[c];
-            chunk_weight[c] += n * tie_kept;
-            all += chunk_weight[c];
-        }
-        const double u = a.u[row] > 0.f ? (double)a.u[row] : 0.0;
-        const double at = u * (double)all;
-        const u64 thr = at < (double)all ? min((u64)at, all - 1) : all - 1;
-        u64 sum = 0, before = 0;
-        int c = 0;
-        for (; c < chunks - 1 && sum + chunk_weight[c] <= thr; ++c) {
-            sum += chunk_weight[c];
-            before += chunk_ties[c];
-        }
-        found[0] = (u64)c;
-        found[1] = thr - sum;
-        found[2] = before;
-        waves[0] = all;
+        const int token = m.low < a.V ? m.low : m.high >= 0 ? m.high : (int)~(u32)best;
+        a.tokens[row] = token;
+        if (a.probs) a.probs[row] = (float)(r.weight(r.l[token]) / sum);
     }
-    __syncthreads();
-    const int c0 = (int)found[0] * CHUNK;
-    const u64 thr = found[1], ties_before = found[2], all = waves[0];
-    __syncthreads();
-    // 4 tokens a thread, in order
-    u32 key[4];
-    u64 w[4], n = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int i = c0 + 4 * tid + j;
-        key[j] = i < a.V ? key_of(l[i]) : 0;
-        n += key[j] && key[j] == kept.key;
-    }
-    u64 s = wave_scan(n, lane);
-    if (lane == 63) waves[wave] = s;
-    __syncthreads();
-    u64 ties = ties_before + s - n;
-    for (int v = 0; v < wave; ++v) ties += waves[v];
-    __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        w[j] = 0;
-        if (key[j] > kept.key) {
-            w[j] = weigh(key[j]);
-            if (!keep(key[j], w[j])) w[j] = 0;
-        } else if (key[j] && key[j] == kept.key) {
-            if (ties++ < kept.ties) w[j] = tie_kept;
-        }
-        n += w[j];
-    }
-    s = wave_scan(n, lane);
-    if (lane == 63) waves[wave] = s;
-    __syncthreads();
-    u64 sum = s - n;
-    for (int v = 0; v < wave; ++v) sum += waves[v];
-    if (sum <= thr && sum + n > thr) {
-        int j = 0;
-        for (; j < 3 && sum + w[j] <= thr; ++j) sum += w[j];
-        a.tokens[row] = c0 + 4 * tid + j;
-        if (a.probs) a.probs[row] = (float)((double)w[j] / (double)all);
-    }
+}
+
+struct SampleSpace { size_t hist, end; };
+static SampleSpace sample_space(int M, int64_t V) {
+    const size_t n = (size_t)M * (size_t)((V + CHUNK - 1) / CHUNK);
+    SampleSpace s;
+    s.hist = (n * sizeof(u64) + 15) & ~(size_t)15;
+    s.end = s.hist + n * BINS * sizeof(u64);
+    return s;
 }
 
 } // namespace step
@@ -280,7 +590,7 @@ extern "C" {
 
 size_t kqstep_sample_workspace_bytes(int M, int64_t V) {
     if (M < 0 || M > 65536 || V < 1 || V > MAX_V) return 0;
-    return 16;
+    return sample_space(M, V).end;
 }
 
 int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float *temperature, const int32_t *top_k,
@@ -293,10 +603,17 @@ int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float
     for (const void *p : four)
         if (!aligned(p, 4)) return KQ_ERR_ALIGN;
     if (!aligned(workspace, 16)) return KQ_ERR_ALIGN;
-    if (workspace_bytes < kqstep_sample_workspace_bytes(M, V)) return KQ_ERR_SHAPE;
+    const SampleSpace s = sample_space(M, V);
+    if (workspace_bytes < s.end) return KQ_ERR_SHAPE;
     if (device_check()) return KQ_ERR_DEVICE;
-    const Sample a = {logits, temperature, top_p, min_p, u, top_k, tokens, probs, ld, (int)V};
-    hipLaunchKernelGGL(sample_kernel, dim3((unsigned)M), dim3(ROW_THREADS), 0, (hipStream_t)stream, a);
+    Sample a = {logits, temperature, top_p, min_p, u, top_k, tokens, probs, (u64 *)workspace, (u64 *)((uint8_t *)workspace + s.hist),
+                ld, (int)V, (int)((V + CHUNK - 1) / CHUNK), 0};
+    hipStream_t st = (hipStream_t)stream;
+    for (; a.row0 < M; a.row0 += SLICE) {
+        const int rows = std::min(M - a.row0, SLICE);
+        hipLaunchKernelGGL(chunk_kernel, dim3((unsigned)a.chunks, (unsigned)rows), dim3(CHUNK_THREADS), 0, st, a);
+        hipLaunchKernelGGL(row_kernel, dim3((unsigned)rows), dim3(ROW_THREADS), 0, st, a);
+    }
     return kv::launched();
 }
 
