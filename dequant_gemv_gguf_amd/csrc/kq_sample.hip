@@ -4,20 +4,21 @@
 // of (logit descending, index ascending), so a filter is a place in that order.
 //
 // Bound: for few rows the chain of two launches, for many the arithmetic of the
-// first (a 64-bit power of two a logit) and HBM.  Two launches:
+// first (a 64-bit power of two a logit), its LDS atomics and HBM.  Two launches:
 //  * chunk_kernel, a work-group a chunk of 8192 tokens of a row: the chunk's first
-//    token of the order, and a histogram over bins of an eighth of an octave of
-//    weight (counts and weights of 512 bins below the chunk's largest).  The bins
-//    lie at fixed places of l / t, so chunks need not know of each other.  A bin's
-//    count and the sum of its weights, integers, share one 64-bit LDS atomic: the
-//    sums do not depend on the order.
-//  * row_kernel, a work-group a row: the chunks' histograms added up give the bin
-//    in which each filter ends.  One scan of the row gathers that bin's tokens (with
-//    top_k: those of all bins down to it) in LDS, where the place is found digit by
-//    digit of the logits' keys.  The chunks' kept weights say which chunk holds the
-//    token; its logits are gone over once more.  Where the gathered tokens do not
-//    fit in LDS (thousands of equal logits, a very high temperature), the digits are
-//    found over the row itself.
+//    token of the order, a histogram over bins of an eighth of an octave of weight
+//    (counts and weights of 512 bins below the chunk's largest), and a list of its
+//    first tokens.  The bins lie at fixed places of l / t, so chunks need not know of
+//    each other.  A bin's count and the sum of its weights, integers, share one
+//    64-bit LDS atomic: the sums do not depend on the order.
+//  * row_kernel, a work-group a row: the chunks' histograms added up give the bin in
+//    which each filter ends.  Where few tokens are left down to that bin (hundreds,
+//    and all in the chunks' lists), every one of them is compared with every other
+//    and that is all.  Elsewhere one scan of the row gathers the bin's tokens in LDS,
+//    where the place is found digit by digit of the logits' keys, the chunks' kept
+//    weights say which chunk holds the token, and its logits are gone over once more.
+//    Where the gathered tokens do not fit in LDS (thousands of equal logits, a very
+//    high temperature), the digits are found over the row itself.
 // Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
 // the row's largest.
 #include "kq_step.h"
@@ -32,7 +33,9 @@ constexpr int ROW_THREADS = 1024, ROW_WAVES = ROW_THREADS / 64;
 constexpr int MAX_V = 1 << 20, MAX_CHUNKS = MAX_V / CHUNK;
 constexpr int BINS = 512, OCTAVE = 8;             // bins, and those of an octave
 constexpr int COUNT_SHIFT = 50;                   // a bin: count, and below it the sum of weights
-constexpr int LIST = 5888;                      // (all of row_kernel's LDS below 64 KB)
+constexpr int LIST = 5376;                        // (all of row_kernel's LDS below 64 KB)
+constexpr int NEAR = 512;                         // tokens of a chunk's list
+constexpr int FEW = 256;                          // tokens that are compared with each other
 constexpr int SLICE = 32768;                      // rows of a launch
 static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
 
@@ -41,7 +44,10 @@ struct Sample {
     const int32_t *top_k;
     int32_t *tokens;
     float *probs;
-    u64 *tops, *hist;       // [row][chunk], [row][chunk][BINS]
+    u64 *tops;              // [row][chunk] first token
+    u32 *near_n;            // [row][chunk] tokens of its list, and above them the bins it goes down
+    u64 *near;              // [row][chunk][NEAR]
+    u64 *hist;              // [row][chunk][BINS]
     int64_t ld;
     int V, chunks, row0;
 };
@@ -94,28 +100,66 @@ __device__ __forceinline__ Scale scale_of(float t) { return Scale{t < __builtin_
 
 __device__ __forceinline__ float temperature_of(const Sample &a, int row) { return a.temperature ? a.temperature[row] : 1.f; }
 
-__device__ __forceinline__ u64 wave_max(u64 x) {
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) {
-        const u64 o = (u64)__shfl_xor((long long)x, i);
-        x = o > x ? o : x;
-    }
+// Across lanes, by DPP: the value of another lane, or `none` where there is none.
+template <int CTRL, int ROWS> __device__ __forceinline__ u32 dpp_or(u32 none, u32 x) {
+    return (u32)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, ROWS, 0xF, false);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ u64 dpp_or(u64 none, u64 x) {
+    return (u64)dpp_or<CTRL, ROWS>((u32)(none >> 32), (u32)(x >> 32)) << 32 | dpp_or<CTRL, ROWS>((u32)none, (u32)x);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_or(double none, double x) {
+    return __builtin_bit_cast(double, dpp_or<CTRL, ROWS>(__builtin_bit_cast(u64, none), __builtin_bit_cast(u64, x)));
+}
+// Inclusive sums over a wave; op over a wave, in every lane.
+template <class N> __device__ __forceinline__ N wave_scan(N x) {
+    x += dpp_or<0x111, 0xF>(N(0), x);
+    x += dpp_or<0x112, 0xF>(N(0), x);
+    x += dpp_or<0x114, 0xF>(N(0), x);
+    x += dpp_or<0x118, 0xF>(N(0), x);
+    x += dpp_or<0x142, 0xA>(N(0), x);
+    x += dpp_or<0x143, 0xC>(N(0), x);
     return x;
 }
-template <class N> __device__ __forceinline__ N wave_scan(N x, int lane) {      // inclusive
-#pragma unroll
-    for (int i = 1; i < 64; i <<= 1) {
-        const N o = __shfl_up(x, i);
-        if (lane >= i) x += o;
-    }
-    return x;
+__device__ __forceinline__ u32 last_lane(u32 x) { return (u32)__builtin_amdgcn_readlane((int)x, 63); }
+__device__ __forceinline__ u64 last_lane(u64 x) { return (u64)last_lane((u32)(x >> 32)) << 32 | last_lane((u32)x); }
+__device__ __forceinline__ double last_lane(double x) { return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(u64, x))); }
+template <class N, class Op> __device__ __forceinline__ N wave_all(N x, Op op) {
+    x = op(x, dpp_or<0x111, 0xF>(x, x));
+    x = op(x, dpp_or<0x112, 0xF>(x, x));
+    x = op(x, dpp_or<0x114, 0xF>(x, x));
+    x = op(x, dpp_or<0x118, 0xF>(x, x));
+    x = op(x, dpp_or<0x142, 0xA>(x, x));
+    x = op(x, dpp_or<0x143, 0xC>(x, x));
+    return last_lane(x);
+}
+__device__ __forceinline__ u64 wave_max(u64 x) {
+    return wave_all(x, [](u64 p, u64 q) { return p > q ? p : q; });
+}
+// x summed over the lanes of a quad.
+__device__ __forceinline__ u64 quad_sum(u64 x) {
+    x += dpp_or<0xB1, 0xF>(0ull, x);
+    return x + dpp_or<0x4E, 0xF>(0ull, x);
 }
 
+// Room for n things of each lane in a list whose length is *count: where the lane's
+// begin.
+__device__ __forceinline__ int room(int *count, int n) {
+    const int upto = (int)wave_scan((u32)n), all = (int)last_lane((u32)upto);
+    int at = 0;
+    if (all && (threadIdx.x & 63) == 63) at = atomicAdd(count, all);
+    return __builtin_amdgcn_readlane(at, 63) + upto - n;
+}
+
+// Whether top_k limits the row (the same in both kernels).
+__device__ __forceinline__ bool limited(int top_k, int V) { return top_k > 0 && top_k < V; }
+
 __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
+    constexpr int PER = CHUNK / CHUNK_THREADS / 4, WAVES = CHUNK_THREADS / 64;
     // two histograms, of the even and the odd lanes: half the lanes of a wave meet in a bin
     __shared__ __align__(16) u64 hist[BINS][2];
-    __shared__ u64 waves[CHUNK_THREADS / 64];
-    constexpr int PER = CHUNK / CHUNK_THREADS / 4;
+    __shared__ u64 waves[WAVES], near[NEAR];
+    __shared__ u32 floors[WAVES], counts[WAVES];
+    __shared__ int n;
     const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
     const float t = temperature_of(a, row);
@@ -131,7 +175,10 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
             for (int j = 0; j < 4; ++j) v[p][j] = i + j < a.V ? l[min(i + j, a.V - 1)] : -__builtin_inff();
         }
     }
+    const int top_k = a.top_k ? a.top_k[row] : 0;
+    const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
     for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
+    if (tid == 0) n = 0;
     u64 best = 0;
 #pragma unroll
     for (int p = 0; p < PER; ++p)
@@ -140,37 +187,91 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
             const u64 x = token_of(key_of(v[p][j]), first + p * 4 * CHUNK_THREADS + j);
             best = x > best ? x : best;
         }
+    // Keys below `floor` cannot be among the first top_k tokens: so many groups of
+    // lanes (of 8 up to 64 tokens, of one up to 512) have a greater one.
+    const bool by_k = limited(top_k, a.V);
+    u32 floor_ = (u32)(best >> 32);
+    if (by_k && top_k <= CHUNK_THREADS / 8) {
+        floor_ = max(floor_, dpp_or<0xB1, 0xF>(floor_, floor_));
+        floor_ = max(floor_, dpp_or<0x4E, 0xF>(floor_, floor_));
+        floor_ = max(floor_, dpp_or<0x141, 0xF>(floor_, floor_));
+    }
+    floor_ = wave_all(floor_, [](u32 p, u32 q) { return min(p, q); });
     best = wave_max(best);
-    if (lane == 0) waves[tid >> 6] = best;
+    if (lane == 0) {
+        waves[tid >> 6] = best;
+        floors[tid >> 6] = floor_;
+    }
     __syncthreads();
-    best = wave_max(waves[lane & (CHUNK_THREADS / 64 - 1)]);
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        best = waves[w] > best ? waves[w] : best;
+        floor_ = min(floor_, floors[w]);
+    }
     const u32 top = (u32)(best >> 32);
     const int64_t at = (int64_t)row * a.chunks + chunk;
     if (tid == 0) a.tops[at] = best;
     if (!top || !(t > 0.f)) return;
     const Scale s = scale_of(t);
     const float most = logit_of(top);
+    if (by_k) {
+        floor_ = top_k <= CHUNK_THREADS ? floor_ : 0;
+    } else {
+        // with min_p alone: nor can keys of less than that part of the largest weight (and a little less)
+        floor_ = 0;
+        if (!(top_p < 1.f) && min_p > 0.f) {
+            const float x = most + t * fminf(logf(min_p), 0.f);
+            floor_ = key_of(x - (fabsf(most) + fabsf(x)) * 0x1p-18f - 1e-30f);
+        }
+    }
+    floor_ = max(floor_, 1u);
     const double from = s.bin(most);
+    int bin[4 * PER];
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float x = v[p][j];
-            if (x > -__builtin_inff()) {
+            int b = BINS;
+            if (key_of(x) >= floor_) {
                 const double d = from - s.bin(x);
-                const int b = x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
-                // (the last bin, 64 octaves below: its weights count as nothing)
-                const u64 w = b < BINS - 1 ? s.mantissa(x) : 0;
+                b = x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
+                // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
+                const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x) : 0;
                 atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
             }
+            bin[4 * p + j] = b;
         }
     __syncthreads();
-    for (int i = tid; i < BINS; i += CHUNK_THREADS) a.hist[at * BINS + i] = hist[i][0] + hist[i][1];
+    // the list: whole bins from the top, as many as fit
+    const u64 h = hist[tid][0] + hist[tid][1];
+    a.hist[at * BINS + tid] = h;
+    u32 upto = wave_scan((u32)(h >> COUNT_SHIFT));
+    if (lane == 63) counts[tid >> 6] = upto;
+    __syncthreads();
+    for (int w = 0; w < tid >> 6; ++w) upto += counts[w];
+    const int depth = __syncthreads_count(upto <= NEAR);
+    u32 mask = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * PER; ++i) mask |= (u32)(bin[i] < depth) << i;
+    int to = room(&n, __popc(mask));
+#pragma unroll
+    for (int p = 0; p < PER; ++p)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (mask >> (4 * p + j) & 1) near[to++] = token_of(key_of(v[p][j]), first + p * 4 * CHUNK_THREADS + j);
+    __syncthreads();
+    for (int i = tid; i < n; i += CHUNK_THREADS) a.near[at * NEAR + i] = near[i];
+    if (tid == 0) a.near_n[at] = (u32)n | (u32)depth << 16;
 }
+static_assert(CHUNK_THREADS == BINS, "a thread a bin");
 
 // What row_kernel shares between its threads.
 struct RowSpace {
-    u64 list[LIST];                 // gathered tokens
+    union {
+        u64 list[LIST];             // gathered tokens
+        struct { u64 token, weight; } few[FEW];
+    };
     u64 weight[BINS];               // of the row's bins
     double upto[BINS];              // summed weights up to and with a bin, in units of the top octave's mantissas
     u32 count[BINS], counts[BINS];  // tokens of a bin, and up to and with it
@@ -180,8 +281,10 @@ struct RowSpace {
     double chunk_sum[MAX_CHUNKS];
     u64 waves[ROW_WAVES];
     double waves_d[ROW_WAVES];
-    u64 found[4];
+    u64 found[4];                   // (0 .. 2 a digit, 3 a token)
     double picked[2];
+    u64 most, sum;
+    int off[MAX_CHUNKS];            // bins that a chunk's are below the row's (BINS: it has none)
     int n, low, high;
 };
 
@@ -206,26 +309,45 @@ struct Row {
         return b < BINS - 1 ? ldexp((double)s.mantissa(x), -octaves(b)) : 0.0;
     }
     __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
+    // as an integer, in units of the mantissas `base` octaves below, 2^finer to one
+    __device__ __forceinline__ u64 integer(u64 token, int finer, int base) const {
+        const float x = logit_of((u32)(token >> 32));
+        const int b = bin(x), down = octaves(b) - base;
+        return b < BINS - 1 && down < 64 ? (s.mantissa(x) << finer) >> down : 0;
+    }
 };
 
-// The shortest leading part of the tokens that `each` goes over (descending) of
-// which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the whole
-// sum): the tokens from *least on.  Returns the part's sum.
-template <bool WEIGHTS, class Each> __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 want, u64 *least) {
+// The shortest leading part (descending) of the tokens from `from` on that `each` goes
+// over, of which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the
+// whole sum): the part is the tokens from the returned one on.
+template <bool WEIGHTS, class Each, class Weight>
+__device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, Weight &&weight, u64 from, u64 want) {
     const int tid = threadIdx.x, lane = tid & 63;
-    u64 prefix = 0, before = 0, sum = 0;
-    for (int shift = 56; shift >= 0; shift -= 8) {
+    // digits that all tokens share are not looked at
+    u64 any = 0, differ = 0;
+    each([&](u64 token) { any = token >= from ? token : any; });
+    if (any) m.found[0] = any;
+    __syncthreads();
+    any = m.found[0];
+    each([&](u64 token) { differ |= token >= from ? token ^ any : 0; });
+    differ = wave_all(differ, [](u64 p, u64 q) { return p | q; });
+    if (lane == 0) m.waves[tid >> 6] = differ;
+    __syncthreads();
+    for (int w = 0; w < ROW_WAVES; ++w) differ |= m.waves[w];
+    const int first = differ ? (63 - __builtin_clzll(differ)) & ~7 : 0;
+    u64 prefix = first < 56 ? any >> (first + 8) : 0, before = 0;
+    for (int shift = first; shift >= 0; shift -= 8) {
         __syncthreads();
         if (tid < 256) {
             m.digit_weight[tid] = 0;
             m.digit_count[tid] = 0;
         }
         __syncthreads();
-        each([&](u64 token, u64 w) {
-            if (shift < 56 && token >> (shift + 8) != prefix) return;
+        each([&](u64 token) {
+            if (token < from || (shift < first && token >> (shift + 8) != prefix)) return;
             const int d = (int)(token >> shift) & 255;
             atomicAdd(&m.digit_count[d], 1u);
-            if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], w);
+            if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], weight(token));
         });
         __syncthreads();
         if (tid < 64) {
@@ -237,7 +359,7 @@ template <bool WEIGHTS, class Each> __device__ __forceinline__ u64 cut(RowSpace 
                 d[i] = WEIGHTS ? m.digit_weight[digit] : m.digit_count[digit];
                 s += d[i];
             }
-            const u64 upto = (u64)wave_scan((long long)s, lane);
+            const u64 upto = wave_scan(s);
             const u64 reach = __ballot(before + upto >= want);
             if (lane == (reach ? __builtin_ctzll(reach) : 63)) {
                 u64 b = before + upto - s;
@@ -245,30 +367,26 @@ template <bool WEIGHTS, class Each> __device__ __forceinline__ u64 cut(RowSpace 
                 for (; i < 3 && b + d[i] < want; ++i) b += d[i];
                 m.found[0] = (u64)(255 - (4 * lane + i));
                 m.found[1] = b;
-                m.found[2] = b + d[i];
-                m.found[3] = m.digit_count[255 - (4 * lane + i)];
+                m.found[2] = m.digit_count[255 - (4 * lane + i)];
             }
         }
         __syncthreads();
         prefix = prefix << 8 | m.found[0];
         before = m.found[1];
-        sum = m.found[2];
-        if (m.found[3] == 1 && shift) {     // one token has these digits: that one
-            each([&](u64 token, u64) {
-                if (token >> shift == prefix) m.found[3] = token;
+        if (m.found[2] == 1 && shift) {     // one token has these digits: that one
+            each([&](u64 token) {
+                if (token >= from && token >> shift == prefix) m.found[3] = token;
             });
             __syncthreads();
-            prefix = m.found[3];
-            break;
+            return m.found[3];
         }
     }
-    *least = prefix;
-    return sum;
+    return prefix;
 }
 
 __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
     const int tid = threadIdx.x, lane = tid & 63;
-    x = (u64)wave_scan((long long)x, lane);
+    x = wave_scan(x);
     __syncthreads();
     if (lane == 63) m.waves[tid >> 6] = x;
     __syncthreads();
@@ -279,11 +397,19 @@ __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
 
 __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     __shared__ RowSpace m;
-    const int row = a.row0 + blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int row = a.row0 + blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const float t = temperature_of(a, row);
     const u64 *tops = a.tops + (int64_t)row * a.chunks;
-    u64 best = 0;
-    for (int c = lane; c < a.chunks; c += 64) best = tops[c] > best ? tops[c] : best;
+    // a lane's chunks: c = lane, lane + 64
+    u64 first_of[MAX_CHUNKS / 64], best = 0;
+    u32 near_n[MAX_CHUNKS / 64];
+#pragma unroll
+    for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+        const int c = lane + 64 * i;
+        first_of[i] = c < a.chunks ? tops[c] : 0;
+        near_n[i] = c < a.chunks ? a.near_n[(int64_t)row * a.chunks + c] : 0;
+        best = first_of[i] > best ? first_of[i] : best;
+    }
     best = wave_max(best);
     if (!(best >> 32) || !(t > 0.f)) {
         if (tid == 0) {
@@ -315,19 +441,23 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         m.low = BINS;
         m.high = -1;
     }
-    for (int c = tid; c < MAX_CHUNKS; c += ROW_THREADS) m.chunk_list[c] = 0;
+    if (wave == 0) {
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+            const int c = lane + 64 * i;
+            const u32 key = (u32)(first_of[i] >> 32);
+            const float x = logit_of(key);
+            const double d = x == most ? 0.0 : r.from - r.s.bin(x);
+            m.off[c] = key && d < BINS ? (int)d : BINS;
+            m.chunk_list[c] = 0;
+        }
+        if (lane == 0) m.most = m.sum = 0;
+    }
     __syncthreads();
-    // bins that chunk c's are below the row's (BINS: it has none)
-    auto below = [&](int c) {
-        const u32 key = (u32)(tops[c] >> 32);
-        if (!key) return BINS;
-        const float x = logit_of(key);
-        const double d = x == most ? 0.0 : r.from - r.s.bin(x);
-        return d < BINS ? (int)d : BINS;
-    };
     for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-        const int off = below(c);
+        // (a chunk without a token has no histogram; one whose tokens lie below all bins is counted)
         if (!(tops[c] >> 32)) continue;
+        const int off = m.off[c];
         const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
         u64 x[BINS / 64];
 #pragma unroll
@@ -337,7 +467,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             const int d = lane + 64 * i, b = min(d + off, BINS - 1);
             if (!x[i]) continue;
             atomicAdd(&m.count[b], (u32)(x[i] >> COUNT_SHIFT));
-            if (b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], x[i] & ((1ull << COUNT_SHIFT) - 1));
+            const u64 w = x[i] & ((1ull << COUNT_SHIFT) - 1);
+            if (w && b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], w);
         }
     }
     __syncthreads();
@@ -346,8 +477,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         u32 n = 0;
         double w = 0.0;
         if (tid < BINS) {
-            n = (u32)wave_scan((int)m.count[tid], lane);
-            w = wave_scan(ldexp((double)m.weight[tid], -r.octaves(tid)), lane);
+            n = wave_scan(m.count[tid]);
+            w = wave_scan(ldexp((double)m.weight[tid], -r.octaves(tid)));
             if (lane == 63) {
                 m.waves[wave] = n;
                 m.waves_d[wave] = w;
@@ -365,14 +496,15 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         __syncthreads();
     }
     const int total = (int)m.counts[BINS - 1];
-    const bool by_k = top_k > 0 && top_k < total, by_p = top_p < 1.f;
+    const bool by_k = limited(top_k, a.V), by_p = top_p < 1.f;
+    const int keep_k = min(top_k, total);         // (fewer than top_k tokens may be above -infinity)
     const double all = m.upto[BINS - 1], want_p = (double)(top_p > 0.f ? top_p : 0.f) * all;
     // the bins in which top_k, top_p and min_p end
     if (tid < BINS) {
         const u32 n0 = tid ? m.counts[tid - 1] : 0, n1 = m.counts[tid];
         const double w0 = tid ? m.upto[tid - 1] : 0.0, w1 = m.upto[tid];
         if (by_k) {
-            if ((int)n0 < top_k && (int)n1 >= top_k) m.low = tid;
+            if ((int)n0 < keep_k && (int)n1 >= keep_k) m.low = tid;
         } else if (by_p && (tid == 0 || w0 < want_p) && (w1 >= want_p || tid == BINS - 1)) {
             atomicMin(&m.low, tid);
         }
@@ -390,10 +522,91 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             one = true;
         }
     }
+    // the chunks' lists go down to bin `low`
+    bool near = low < BINS - 1;
+#pragma unroll
+    for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+        const int depth = (int)(near_n[i] >> 16);
+        near = near && (!(first_of[i] >> 32) || depth == BINS || m.off[lane + 64 * i] + depth > low);
+    }
+    near = __ballot(!near) == 0;
+    auto list_length = [&](int c) {
+        return (int)((u32)__builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63) & 0xFFFF);
+    };
+    if (near && m.counts[low] <= FEW) {
+        // Few tokens: each with those before it (4 threads a token, a quarter of the others each).
+        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+            const int nc = list_length(c);
+            if (m.off[c] > low) continue;
+            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
+            for (int i = lane; i < NEAR && i - lane < nc; i += 64) {
+                const u64 token = i < nc ? from[i] : 0;
+                const bool in = i < nc && r.bin(logit_of((u32)(token >> 32))) <= low;
+                const int to = room(&m.n, in);
+                if (in && to < FEW) {
+                    m.few[to].token = token;
+                    m.few[to].weight = r.integer(token, 14, 0);
+                }
+            }
+        }
+        __syncthreads();
+        const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
+        const u64 token = m.few[min(i, n - 1)].token, weight = m.few[min(i, n - 1)].weight;
+        u64 upto = 0, place = 0;
+        for (int j = part; j < n; j += 4) {
+            const bool before = m.few[j].token >= token;
+            place += before;
+            upto += before ? m.few[j].weight : 0;
+        }
+        place = quad_sum(place);
+        upto = quad_sum(upto);
+        bool kept = i < n && (!by_k || (int)place <= keep_k);
+        u64 mine = wave_max(kept ? upto : 0);
+        if (lane == 0) atomicMax((unsigned long long *)&m.most, mine);
+        __syncthreads();
+        if (by_p) {
+            const double want = by_k ? (double)(top_p > 0.f ? top_p : 0.f) * (double)m.most : ldexp(want_p, 14);
+            kept = kept && (place == 1 || (double)(upto - weight) < want);
+        }
+        kept = kept && r.keeps(token, ldexp((double)weight, -14));
+        mine = wave_max(kept ? upto : 0);
+        if (lane == 0) atomicMax((unsigned long long *)&m.sum, mine);
+        __syncthreads();
+        if (i < n && part == 0 && !kept) m.few[i].weight = 0;
+        __syncthreads();
+        // the kept weights up to each token, by index
+        const u64 sum = m.sum;
+        const float u = a.u[row];
+        const double at = (u > 0.f ? (double)u : 0.0) * (double)sum;
+        const u64 past = at < (double)sum ? min((u64)at, sum - 1) : sum - 1;
+        u64 before = 0;
+        for (int j = part; j < n; j += 4) before += (u32)m.few[j].token > (u32)token ? m.few[j].weight : 0;
+        before = quad_sum(before);
+        if (part == 0 && kept && before <= past && past < before + weight) {
+            a.tokens[row] = (int)~(u32)token;
+            if (a.probs) a.probs[row] = (float)((double)weight / (double)sum);
+        }
+        return;
+    }
     const int high = by_k ? 0 : low;              // bins high .. low are gathered
     const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
-    const bool scan = low < BINS, listed = scan && low < BINS - 1 && gathered <= LIST;
-    if (listed) {
+    const bool scan = low < BINS;
+    bool listed = scan && low < BINS - 1 && gathered <= LIST;
+    if (listed && near) {
+        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+            const int nc = list_length(c);
+            if (m.off[c] > low) continue;
+            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
+            for (int i = lane; i < NEAR && i - lane < nc; i += 64) {
+                const u64 token = i < nc ? from[i] : 0;
+                const int b = i < nc ? r.bin(logit_of((u32)(token >> 32))) : BINS;
+                const bool in = b >= high && b <= low;
+                const int to = room(&m.n, in);
+                if (in && to < LIST) m.list[to] = token;
+            }
+        }
+        __syncthreads();
+    } else if (listed) {
         // what can lie in these bins, and a little more
         float lo = -__builtin_inff(), hi = __builtin_inff();
         if (r.s.eighths > 0.0 && most < __builtin_inff()) {
@@ -402,11 +615,11 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
         }
         constexpr int BATCH = 8;                  // pieces of 4 a thread between two writes
-        for (int i0 = 4 * tid; i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
+        for (int i0 = 4 * (tid - lane); i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
             u32 mask = 0;
 #pragma unroll
             for (int p = 0; p < BATCH; ++p) {
-                const int i = i0 + 4 * ROW_THREADS * p;
+                const int i = i0 + 4 * lane + 4 * ROW_THREADS * p;
                 if (i + 4 <= a.V) {
                     const f4 x = *(const f4u *)(r.l + i);
 #pragma unroll
@@ -416,28 +629,28 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
                         if (i + j < a.V) mask |= (u32)(r.l[i + j] >= lo && r.l[i + j] <= hi) << (4 * p + j);
                 }
             }
-            while (mask) {
-                const int bit = __builtin_ctz(mask), i = i0 + 4 * ROW_THREADS * (bit >> 2) + (bit & 3);
-                mask &= mask - 1;
-                const float x = r.l[i];
-                const u32 key = key_of(x);
-                const int b = key ? r.bin(x) : BINS;
-                if (b < high || b > low) continue;
-                const int n = atomicAdd(&m.n, 1);
-                if (n < LIST) m.list[n] = token_of(key, i);
+            // those that do
+            auto index = [&](int bit) { return i0 + 4 * lane + 4 * ROW_THREADS * (bit >> 2) + (bit & 3); };
+            for (u32 left = mask; left; left &= left - 1) {
+                const float x = r.l[index(__builtin_ctz(left))];
+                const int b = key_of(x) ? r.bin(x) : BINS;
+                if (b < high || b > low) mask &= ~(left & -left);
+            }
+            int to = room(&m.n, __popc(mask));
+            for (; mask; mask &= mask - 1, ++to) {
+                const int i = index(__builtin_ctz(mask));
+                if (to < LIST) m.list[to] = token_of(key_of(r.l[i]), i);
             }
         }
         __syncthreads();
+        // (with top_k the chunks did not count all of their tokens)
+        listed = m.n <= LIST;
     }
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
     // 2^20 tokens have to fit the sum).
     const int finer = listed ? 14 : 7, base = one && listed ? r.octaves(low) : 0;
-    auto integer = [&](u64 token) {
-        const float x = logit_of((u32)(token >> 32));
-        const int b = r.bin(x), down = r.octaves(b) - base;
-        return b < BINS - 1 && down < 64 ? (r.s.mantissa(x) << finer) >> down : 0ull;
-    };
+    auto integer = [&](u64 token) { return r.integer(token, finer, base); };
     auto each = [&](auto &&f) {
         if (listed) {
             for (int i = tid; i < min(m.n, LIST); i += ROW_THREADS) f(m.list[i]);
@@ -450,26 +663,16 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     };
     u64 least = 0;                                // the last token that top_k and top_p keep
     if (scan) {
-        if (by_k) {
-            cut<false>(m, [&](auto &&f) { each([&](u64 token) { f(token, 1ull); }); }, (u64)top_k, &least);
-        }
-        if (by_p && !(one && listed)) {
-            // of what top_k leaves (of the whole row where its bin was not gathered)
+        if (by_k && total >= top_k) least = cut<false>(m, each, integer, 0, (u64)top_k);
+        if (by_p && (by_k || !listed || low == m.low)) {
+            // Of what top_k leaves; in the one bin that decides, what the bins above it
+            // leave; over the row, of all its weight.
             u64 sum = 0;
             each([&](u64 token) { sum += token >= least ? integer(token) : 0; });
             sum = block_sum(m, sum);
-            const double want = ceil((double)(top_p > 0.f ? top_p : 0.f) * (double)sum);
-            const u64 from = least;
-            cut<true>(m, [&](auto &&f) { each([&](u64 token) { if (token >= from) f(token, integer(token)); }); },
-                      want < 1.0 ? 1 : want < (double)sum ? (u64)want : sum, &least);
-        } else if (by_p && low == m.low) {
-            // within the bin
-            u64 sum = 0;
-            each([&](u64 token) { sum += integer(token); });
-            sum = block_sum(m, sum);
-            const double want = ceil(ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer));
-            cut<true>(m, [&](auto &&f) { each([&](u64 token) { f(token, integer(token)); }); },
-                      want < 1.0 ? 1 : want < (double)sum ? (u64)want : sum, &least);
+            const double want = one && listed ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
+                                              : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
+            least = cut<true>(m, each, integer, least, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
         // kept weight of the gathered tokens, by chunk
@@ -485,7 +688,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const int whole = !scan ? BINS : one && listed ? low : 0;
     for (int c = wave; c < a.chunks; c += ROW_WAVES) {
         double w = 0.0;
-        const int off = whole ? below(c) : BINS;
+        const int off = whole && (tops[c] >> 32) ? m.off[c] : BINS;
         if (off < whole) {
             const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
 #pragma unroll
@@ -507,7 +710,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             s[i] = EACH * lane + i < a.chunks ? m.chunk_sum[EACH * lane + i] : 0.0;
             mine += s[i];
         }
-        const double upto = wave_scan(mine, lane), sum = __shfl(upto, 63);
+        const double upto = wave_scan(mine), sum = last_lane(upto);
         const float u = a.u[row];
         const double at = (u > 0.f ? fmin((double)u, 1.0) : 0.0) * sum;
         // the first lane whose sum passes `at`, else the last that has any weight
@@ -547,35 +750,42 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
         mine += w[j];
     }
-    double upto = wave_scan(mine, lane);
+    double upto = wave_scan(mine);
     if (lane == 63) m.waves_d[wave] = upto;
     __syncthreads();
-    for (int v = 0; v < wave; ++v) upto += m.waves_d[v];
+#pragma unroll
+    for (int v = 0; v < ROW_WAVES; ++v) upto += v < wave ? m.waves_d[v] : 0.0;
     double b = upto - mine;
-    int at_least = a.V, last = -1;
+    int token = a.V, last = -1;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
         b += w[j];
         if (w[j] > 0.0) {
             last = first + j;
-            if (b > at && at_least == a.V) at_least = first + j;
+            if (b > at && token == a.V) token = first + j;
         }
     }
-    if (at_least < a.V) atomicMin(&m.low, at_least);
+    if (token < a.V) atomicMin(&m.low, token);
     if (last >= 0) atomicMax(&m.high, last);
     __syncthreads();
-    if (tid == 0) {
-        const int token = m.low < a.V ? m.low : m.high >= 0 ? m.high : (int)~(u32)best;
+    token = m.low < a.V ? m.low : m.high;
+    if (token < 0 && tid == 0) token = (int)~(u32)best;      // (weights that differ by a rounding left none)
+    if (token >= first && token < first + EACH) {
+        double p = 0.0;
+#pragma unroll
+        for (int j = 0; j < EACH; ++j) p = first + j == token ? w[j] : p;
         a.tokens[row] = token;
-        if (a.probs) a.probs[row] = (float)(r.weight(r.l[token]) / sum);
+        if (a.probs) a.probs[row] = (float)(p / sum);
     }
 }
 
-struct SampleSpace { size_t hist, end; };
+struct SampleSpace { size_t near_n, near, hist, end; };
 static SampleSpace sample_space(int M, int64_t V) {
     const size_t n = (size_t)M * (size_t)((V + CHUNK - 1) / CHUNK);
     SampleSpace s;
-    s.hist = (n * sizeof(u64) + 15) & ~(size_t)15;
+    s.near_n = n * sizeof(u64);
+    s.near = (s.near_n + n * sizeof(u32) + 15) & ~(size_t)15;
+    s.hist = s.near + n * NEAR * sizeof(u64);
     s.end = s.hist + n * BINS * sizeof(u64);
     return s;
 }
@@ -606,8 +816,9 @@ int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float
     const SampleSpace s = sample_space(M, V);
     if (workspace_bytes < s.end) return KQ_ERR_SHAPE;
     if (device_check()) return KQ_ERR_DEVICE;
-    Sample a = {logits, temperature, top_p, min_p, u, top_k, tokens, probs, (u64 *)workspace, (u64 *)((uint8_t *)workspace + s.hist),
-                ld, (int)V, (int)((V + CHUNK - 1) / CHUNK), 0};
+    uint8_t *ws = (uint8_t *)workspace;
+    Sample a = {logits, temperature, top_p, min_p, u, top_k, tokens, probs, (u64 *)ws, (u32 *)(ws + s.near_n), (u64 *)(ws + s.near),
+                (u64 *)(ws + s.hist), ld, (int)V, (int)((V + CHUNK - 1) / CHUNK), 0};
     hipStream_t st = (hipStream_t)stream;
     for (; a.row0 < M; a.row0 += SLICE) {
         const int rows = std::min(M - a.row0, SLICE);
