@@ -33,8 +33,8 @@ constexpr int ROW_THREADS = 1024, ROW_WAVES = ROW_THREADS / 64;
 constexpr int MAX_V = 1 << 20, MAX_CHUNKS = MAX_V / CHUNK;
 constexpr int BINS = 512, OCTAVE = 8;             // bins, and those of an octave
 constexpr int COUNT_SHIFT = 50;                   // a bin: count, and below it the sum of weights
-constexpr int LIST = 5376;                        // (all of row_kernel's LDS below 64 KB)
-constexpr int NEAR = 512;                         // tokens of a chunk's list
+constexpr int LIST = 5120;                        // (all of row_kernel's LDS below 64 KB)
+constexpr int NEAR = 256;                         // tokens of a chunk's list
 constexpr int FEW = 256;                          // tokens that are compared with each other
 constexpr int SLICE = 32768;                      // rows of a launch
 static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
@@ -69,23 +69,17 @@ __device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 
 // mantissa, 2^35 .. 2^36.  An infinite logit lies above all others.
 struct Scale {
     double eighths;         // of an octave, per logit: 8 log2(e) / t
+    const double *steps;    // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
     __device__ __forceinline__ double at(float l) const {
         return l == __builtin_inff() ? __builtin_inf() : (double)l * eighths;
     }
     __device__ __forceinline__ double bin(float l) const { return floor(at(l)); }
-    __device__ __forceinline__ u64 mantissa(float l) const {
-        double y = at(l) * 0.125;
-        y -= floor(y);
-        const double x = l == __builtin_inff() ? 0.0 : y * 0.6931471805599453;
-        // e^x for 0 <= x < log 2: its series to x^13 / 13! (2^-40 is left)
-        double p = 1.0 / 6227020800.0;
-        p = fma(p, x, 1.0 / 479001600.0);
-        p = fma(p, x, 1.0 / 39916800.0);
-        p = fma(p, x, 1.0 / 3628800.0);
-        p = fma(p, x, 1.0 / 362880.0);
-        p = fma(p, x, 1.0 / 40320.0);
-        p = fma(p, x, 1.0 / 5040.0);
-        p = fma(p, x, 1.0 / 720.0);
+    // `of_octave`: the bin's place in its octave
+    __device__ __forceinline__ u64 mantissa(float l, int of_octave) const {
+        const double y = at(l);
+        // e^x for |x| <= log 2 / 16: its series to x^6 / 6! (2^-44 is left)
+        const double x = l == __builtin_inff() ? -0.04332169878499658 : (y - floor(y) - 0.5) * 0.08664339756999316;
+        double p = 1.0 / 720.0;
         p = fma(p, x, 1.0 / 120.0);
         p = fma(p, x, 1.0 / 24.0);
         p = fma(p, x, 1.0 / 6.0);
@@ -93,10 +87,19 @@ struct Scale {
         p = fma(p, x, 1.0);
         p = fma(p, x, 1.0);
         // to an integer: 2^52 in front leaves it in the low bits, rounded
-        return __builtin_bit_cast(u64, fma(p, 34359738368.0, 4503599627370496.0)) - 0x4330000000000000ull;
+        return __builtin_bit_cast(u64, fma(p, steps[of_octave], 4503599627370496.0)) - 0x4330000000000000ull;
     }
 };
-__device__ __forceinline__ Scale scale_of(float t) { return Scale{t < __builtin_inff() ? 8.0 * 1.4426950408889634 / (double)t : 0.0}; }
+__device__ __forceinline__ Scale scale_of(float t, const double *steps) {
+    return Scale{t < __builtin_inff() ? 8.0 * 1.4426950408889634 / (double)t : 0.0, steps};
+}
+__device__ __forceinline__ void make_steps(double *steps) {
+    if (threadIdx.x < OCTAVE) steps[threadIdx.x] = exp2(35.0 + (threadIdx.x + 0.5) / OCTAVE);
+}
+// from mod OCTAVE, of the first token's bin (an infinite one: the octave's last)
+__device__ __forceinline__ int phase_of(double from) {
+    return from < __builtin_inf() ? (int)(from - OCTAVE * floor(from / OCTAVE)) : OCTAVE - 1;
+}
 
 __device__ __forceinline__ float temperature_of(const Sample &a, int row) { return a.temperature ? a.temperature[row] : 1.f; }
 
@@ -159,6 +162,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     __shared__ __align__(16) u64 hist[BINS][2];
     __shared__ u64 waves[WAVES], near[NEAR];
     __shared__ u32 floors[WAVES], counts[WAVES];
+    __shared__ double steps[OCTAVE];
     __shared__ int n;
     const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
@@ -179,6 +183,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
     for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
     if (tid == 0) n = 0;
+    make_steps(steps);
     u64 best = 0;
 #pragma unroll
     for (int p = 0; p < PER; ++p)
@@ -212,7 +217,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     const int64_t at = (int64_t)row * a.chunks + chunk;
     if (tid == 0) a.tops[at] = best;
     if (!top || !(t > 0.f)) return;
-    const Scale s = scale_of(t);
+    const Scale s = scale_of(t, steps);
     const float most = logit_of(top);
     if (by_k) {
         floor_ = top_k <= CHUNK_THREADS ? floor_ : 0;
@@ -226,7 +231,8 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     }
     floor_ = max(floor_, 1u);
     const double from = s.bin(most);
-    int bin[4 * PER];
+    const int phase = phase_of(from);
+    u32 bins[2 * PER] = {};                       // two in one
 #pragma unroll
     for (int p = 0; p < PER; ++p)
 #pragma unroll
@@ -237,10 +243,10 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
                 const double d = from - s.bin(x);
                 b = x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
                 // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
-                const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x) : 0;
+                const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x, (phase - b) & (OCTAVE - 1)) : 0;
                 atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
             }
-            bin[4 * p + j] = b;
+            bins[2 * p + j / 2] |= (u32)b << (16 * (j & 1));
         }
     __syncthreads();
     // the list: whole bins from the top, as many as fit
@@ -253,7 +259,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     const int depth = __syncthreads_count(upto <= NEAR);
     u32 mask = 0;
 #pragma unroll
-    for (int i = 0; i < 4 * PER; ++i) mask |= (u32)(bin[i] < depth) << i;
+    for (int i = 0; i < 4 * PER; ++i) mask |= (u32)((int)(bins[i / 2] >> (16 * (i & 1)) & 0xFFFF) < depth) << i;
     int to = room(&n, __popc(mask));
 #pragma unroll
     for (int p = 0; p < PER; ++p)
@@ -284,7 +290,8 @@ struct RowSpace {
     u64 found[4];                   // (0 .. 2 a digit, 3 a token)
     double picked[2];
     u64 most, sum;
-    int off[MAX_CHUNKS];            // bins that a chunk's are below the row's (BINS: it has none)
+    double steps[OCTAVE];
+    int off[MAX_CHUNKS];            // bins that a chunk's are below the row's (BINS: all of them; -1: it has no token)
     int n, low, high;
 };
 
@@ -306,48 +313,52 @@ struct Row {
     // in units of the top octave's mantissas
     __device__ __forceinline__ double weight(float x) const {
         const int b = bin(x);
-        return b < BINS - 1 ? ldexp((double)s.mantissa(x), -octaves(b)) : 0.0;
+        return b < BINS - 1 ? ldexp((double)mantissa(x, b), -octaves(b)) : 0.0;
     }
+    __device__ __forceinline__ u64 mantissa(float x, int b) const { return s.mantissa(x, (phase - b) & (OCTAVE - 1)); }
     __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
     // as an integer, in units of the mantissas `base` octaves below, 2^finer to one
     __device__ __forceinline__ u64 integer(u64 token, int finer, int base) const {
         const float x = logit_of((u32)(token >> 32));
         const int b = bin(x), down = octaves(b) - base;
-        return b < BINS - 1 && down < 64 ? (s.mantissa(x) << finer) >> down : 0;
+        return b < BINS - 1 && down < 64 ? (mantissa(x, b) << finer) >> down : 0;
     }
 };
 
 // The shortest leading part (descending) of the tokens from `from` on that `each` goes
 // over, of which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the
-// whole sum): the part is the tokens from the returned one on.
-template <bool WEIGHTS, class Each, class Weight>
-__device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, Weight &&weight, u64 from, u64 want) {
+// whole sum): the part is the tokens from the returned one on.  Digits of 8 bits, from
+// the first bit in which two tokens differ.
+template <bool WEIGHTS, class Each>
+__device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 want) {
     const int tid = threadIdx.x, lane = tid & 63;
-    // digits that all tokens share are not looked at
     u64 any = 0, differ = 0;
-    each([&](u64 token) { any = token >= from ? token : any; });
+    each([&](u64 token, auto &&) { any = token >= from ? token : any; });
     if (any) m.found[0] = any;
     __syncthreads();
     any = m.found[0];
-    each([&](u64 token) { differ |= token >= from ? token ^ any : 0; });
+    each([&](u64 token, auto &&) { differ |= token >= from ? token ^ any : 0; });
     differ = wave_all(differ, [](u64 p, u64 q) { return p | q; });
     if (lane == 0) m.waves[tid >> 6] = differ;
     __syncthreads();
     for (int w = 0; w < ROW_WAVES; ++w) differ |= m.waves[w];
-    const int first = differ ? (63 - __builtin_clzll(differ)) & ~7 : 0;
-    u64 prefix = first < 56 ? any >> (first + 8) : 0, before = 0;
-    for (int shift = first; shift >= 0; shift -= 8) {
+    if (!differ) return any;
+    int above = 64 - __builtin_clzll(differ);           // bits from here on are `prefix`
+    u64 prefix = above < 64 ? any >> above : 0, before = 0;
+    while (above) {
+        const int shift = max(above - 8, 0);
+        const u32 digits = (1u << (above - shift)) - 1;
         __syncthreads();
         if (tid < 256) {
             m.digit_weight[tid] = 0;
             m.digit_count[tid] = 0;
         }
         __syncthreads();
-        each([&](u64 token) {
-            if (token < from || (shift < first && token >> (shift + 8) != prefix)) return;
-            const int d = (int)(token >> shift) & 255;
+        each([&](u64 token, auto &&weight) {
+            if (token < from || (above < 64 && token >> above != prefix)) return;
+            const u32 d = (u32)(token >> shift) & digits;
             atomicAdd(&m.digit_count[d], 1u);
-            if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], weight(token));
+            if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], weight());
         });
         __syncthreads();
         if (tid < 64) {
@@ -371,10 +382,11 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, Weight &&weight, u6
             }
         }
         __syncthreads();
-        prefix = prefix << 8 | m.found[0];
+        prefix = prefix << (above - shift) | m.found[0];
         before = m.found[1];
+        above = shift;
         if (m.found[2] == 1 && shift) {     // one token has these digits: that one
-            each([&](u64 token) {
+            each([&](u64 token, auto &&) {
                 if (token >= from && token >> shift == prefix) m.found[3] = token;
             });
             __syncthreads();
@@ -420,14 +432,13 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     }
     Row r;
     r.l = a.logits + row * a.ld;
-    r.s = scale_of(t);
+    r.s = scale_of(t, m.steps);
     r.best = best;
     r.V = a.V;
     const float most = logit_of((u32)(best >> 32));
     r.from = r.s.bin(most);
-    r.phase = most == __builtin_inff() ? OCTAVE - 1 : (int)(r.from - OCTAVE * floor(r.from / OCTAVE));
+    r.phase = phase_of(r.from);
     const float min_p = a.min_p ? a.min_p[row] : 0.f;
-    r.least = min_p > 0.f ? (double)min_p * (double)r.s.mantissa(most) : 0.0;
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const float top_p = a.top_p ? a.top_p[row] : 1.f;
 
@@ -448,16 +459,17 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             const u32 key = (u32)(first_of[i] >> 32);
             const float x = logit_of(key);
             const double d = x == most ? 0.0 : r.from - r.s.bin(x);
-            m.off[c] = key && d < BINS ? (int)d : BINS;
+            m.off[c] = !key ? -1 : d < BINS ? (int)d : BINS;
             m.chunk_list[c] = 0;
         }
         if (lane == 0) m.most = m.sum = 0;
     }
+    make_steps(m.steps);
     __syncthreads();
+    r.least = min_p > 0.f ? (double)min_p * (double)r.mantissa(most, 0) : 0.0;
     for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-        // (a chunk without a token has no histogram; one whose tokens lie below all bins is counted)
-        if (!(tops[c] >> 32)) continue;
         const int off = m.off[c];
+        if (off < 0) continue;                    // it has no histogram
         const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
         u64 x[BINS / 64];
 #pragma unroll
@@ -530,25 +542,34 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         near = near && (!(first_of[i] >> 32) || depth == BINS || m.off[lane + 64 * i] + depth > low);
     }
     near = __ballot(!near) == 0;
-    auto list_length = [&](int c) {
-        return (int)((u32)__builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63) & 0xFFFF);
+    // the tokens of bins high .. low in the chunks' lists, each with a place of its own
+    auto from_lists = [&](int high, int low, auto &&put) {
+        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+            if (m.off[c] < 0 || m.off[c] > low) continue;
+            const int n = (int)((u32)__builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63) & 0xFFFF);
+            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
+            u64 token[NEAR / 64];
+            u32 mask = 0;
+#pragma unroll
+            for (int i = 0; i < NEAR / 64; ++i) token[i] = lane + 64 * i < n ? from[lane + 64 * i] : 0;
+#pragma unroll
+            for (int i = 0; i < NEAR / 64; ++i) {
+                const int b = token[i] ? r.bin(logit_of((u32)(token[i] >> 32))) : BINS;
+                mask |= (u32)(b >= high && b <= low) << i;
+            }
+            int to = room(&m.n, __popc(mask));
+#pragma unroll
+            for (int i = 0; i < NEAR / 64; ++i)
+                if (mask >> i & 1) put(to++, token[i]);
+        }
     };
     if (near && m.counts[low] <= FEW) {
         // Few tokens: each with those before it (4 threads a token, a quarter of the others each).
-        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-            const int nc = list_length(c);
-            if (m.off[c] > low) continue;
-            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
-            for (int i = lane; i < NEAR && i - lane < nc; i += 64) {
-                const u64 token = i < nc ? from[i] : 0;
-                const bool in = i < nc && r.bin(logit_of((u32)(token >> 32))) <= low;
-                const int to = room(&m.n, in);
-                if (in && to < FEW) {
-                    m.few[to].token = token;
-                    m.few[to].weight = r.integer(token, 14, 0);
-                }
-            }
-        }
+        from_lists(0, low, [&](int to, u64 token) {
+            if (to >= FEW) return;
+            m.few[to].token = token;
+            m.few[to].weight = r.integer(token, 14, 0);
+        });
         __syncthreads();
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
         const u64 token = m.few[min(i, n - 1)].token, weight = m.few[min(i, n - 1)].weight;
@@ -591,20 +612,11 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const int high = by_k ? 0 : low;              // bins high .. low are gathered
     const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
     const bool scan = low < BINS;
-    bool listed = scan && low < BINS - 1 && gathered <= LIST;
+    bool listed = scan && low < BINS - 1 && gathered <= LIST - 64;
     if (listed && near) {
-        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-            const int nc = list_length(c);
-            if (m.off[c] > low) continue;
-            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
-            for (int i = lane; i < NEAR && i - lane < nc; i += 64) {
-                const u64 token = i < nc ? from[i] : 0;
-                const int b = i < nc ? r.bin(logit_of((u32)(token >> 32))) : BINS;
-                const bool in = b >= high && b <= low;
-                const int to = room(&m.n, in);
-                if (in && to < LIST) m.list[to] = token;
-            }
-        }
+        from_lists(high, low, [&](int to, u64 token) {
+            if (to < LIST) m.list[to] = token;
+        });
         __syncthreads();
     } else if (listed) {
         // what can lie in these bins, and a little more
@@ -614,82 +626,99 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
             hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
         }
-        constexpr int BATCH = 8;                  // pieces of 4 a thread between two writes
-        for (int i0 = 4 * (tid - lane); i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
-            u32 mask = 0;
+        constexpr int BATCH = 4;                  // pieces of 4 a thread; the next ones are on their way
+        f4 now[BATCH], next[BATCH];
+        auto ask = [&](f4 (&x)[BATCH], int i0) {
 #pragma unroll
             for (int p = 0; p < BATCH; ++p) {
-                const int i = i0 + 4 * lane + 4 * ROW_THREADS * p;
+                const int i = i0 + 4 * ROW_THREADS * p;
                 if (i + 4 <= a.V) {
-                    const f4 x = *(const f4u *)(r.l + i);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) mask |= (u32)(x[j] >= lo && x[j] <= hi) << (4 * p + j);
+                    x[p] = *(const f4u *)(r.l + i);
                 } else {
-                    for (int j = 0; j < 4; ++j)
-                        if (i + j < a.V) mask |= (u32)(r.l[i + j] >= lo && r.l[i + j] <= hi) << (4 * p + j);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) x[p][j] = i + j < a.V ? r.l[min(i + j, a.V - 1)] : -__builtin_inff();
                 }
             }
-            // those that do
-            auto index = [&](int bit) { return i0 + 4 * lane + 4 * ROW_THREADS * (bit >> 2) + (bit & 3); };
-            for (u32 left = mask; left; left &= left - 1) {
-                const float x = r.l[index(__builtin_ctz(left))];
-                const int b = key_of(x) ? r.bin(x) : BINS;
-                if (b < high || b > low) mask &= ~(left & -left);
-            }
+        };
+        ask(now, 4 * tid);
+        for (int i0 = 0; i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
+            if (i0 + 4 * ROW_THREADS * BATCH < a.V) ask(next, i0 + 4 * ROW_THREADS * BATCH + 4 * tid);
+            u32 mask = 0;
+#pragma unroll
+            for (int i = 0; i < 4 * BATCH; ++i) mask |= (u32)(now[i / 4][i % 4] >= lo && now[i / 4][i % 4] <= hi) << i;
             int to = room(&m.n, __popc(mask));
-            for (; mask; mask &= mask - 1, ++to) {
-                const int i = index(__builtin_ctz(mask));
-                if (to < LIST) m.list[to] = token_of(key_of(r.l[i]), i);
-            }
+#pragma unroll
+            for (int i = 0; i < 4 * BATCH; ++i)
+                if (mask >> i & 1) {
+                    if (to < LIST) m.list[to] = token_of(key_of(now[i / 4][i % 4]), i0 + 4 * tid + 4 * ROW_THREADS * (i / 4) + i % 4);
+                    ++to;
+                }
+#pragma unroll
+            for (int p = 0; p < BATCH; ++p) now[p] = next[p];
         }
         __syncthreads();
-        // (with top_k the chunks did not count all of their tokens)
+        // (more than the bins hold: what is a rounding away from them, and with top_k, of
+        // which the chunks did not count all of their tokens, any number)
         listed = m.n <= LIST;
     }
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
     // 2^20 tokens have to fit the sum).
     const int finer = listed ? 14 : 7, base = one && listed ? r.octaves(low) : 0;
-    auto integer = [&](u64 token) { return r.integer(token, finer, base); };
-    auto each = [&](auto &&f) {
-        if (listed) {
-            for (int i = tid; i < min(m.n, LIST); i += ROW_THREADS) f(m.list[i]);
-        } else {
-            for (int i = tid; i < a.V; i += ROW_THREADS) {
-                const u32 key = key_of(r.l[i]);
-                if (key) f(token_of(key, i));
-            }
-        }
-    };
     u64 least = 0;                                // the last token that top_k and top_p keep
-    if (scan) {
-        if (by_k && total >= top_k) least = cut<false>(m, each, integer, 0, (u64)top_k);
+    // each(f): f(token, weight()) for every gathered token
+    auto places = [&](auto &&each) {
+        if (by_k && total >= top_k) least = cut<false>(m, each, 0, (u64)top_k);
         if (by_p && (by_k || !listed || low == m.low)) {
             // Of what top_k leaves; in the one bin that decides, what the bins above it
             // leave; over the row, of all its weight.
             u64 sum = 0;
-            each([&](u64 token) { sum += token >= least ? integer(token) : 0; });
+            each([&](u64 token, auto &&weight) { sum += token >= least ? weight() : 0; });
             sum = block_sum(m, sum);
             const double want = one && listed ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
                                               : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
-            least = cut<true>(m, each, integer, least, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
+            least = cut<true>(m, each, least, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
         // kept weight of the gathered tokens, by chunk
-        each([&](u64 token) {
+        each([&](u64 token, auto &&weight) {
             if (token < least) return;
-            const u64 w = integer(token);
+            const u64 w = weight();
             if (w && r.keeps(token, ldexp((double)w, -base - finer)))
                 atomicAdd((unsigned long long *)&m.chunk_list[(int)~(u32)token / CHUNK], w);
         });
         __syncthreads();
+    };
+    if (listed) {
+        // a thread's tokens and their weights, in registers (0: none)
+        u64 token[LIST / ROW_THREADS], w[LIST / ROW_THREADS];
+#pragma unroll
+        for (int i = 0; i < LIST / ROW_THREADS; ++i) {
+            token[i] = tid + i * ROW_THREADS < m.n ? m.list[tid + i * ROW_THREADS] : 0;
+            const int b = token[i] >> 32 ? r.bin(logit_of((u32)(token[i] >> 32))) : BINS;
+            if (b < high || b > low) token[i] = 0;
+            w[i] = token[i] ? r.integer(token[i], finer, base) : 0;
+        }
+        places([&](auto &&f) {
+#pragma unroll
+            for (int i = 0; i < LIST / ROW_THREADS; ++i)
+                if (token[i]) f(token[i], [&] { return w[i]; });
+        });
+    } else if (scan) {
+        places([&](auto &&f) {
+            for (int i = tid; i < a.V; i += ROW_THREADS) {
+                const u32 key = key_of(r.l[i]);
+                const u64 token = token_of(key, i);
+                if (key) f(token, [&] { return r.integer(token, finer, base); });
+            }
+        });
     }
     // and of the bins above them
     const int whole = !scan ? BINS : one && listed ? low : 0;
     for (int c = wave; c < a.chunks; c += ROW_WAVES) {
         double w = 0.0;
-        const int off = whole && (tops[c] >> 32) ? m.off[c] : BINS;
-        if (off < whole) {
+        const int off = m.off[c];
+        if (off >= 0 && off < whole) {
             const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
 #pragma unroll
             for (int i = 0; i < BINS / 64; ++i) {
