@@ -35,6 +35,7 @@ constexpr int BINS = 512, OCTAVE = 8;             // bins, and those of an octav
 constexpr int COUNT_SHIFT = 50;                   // a bin: count, and below it the sum of weights
 constexpr int LIST = 5120;                        // (all of row_kernel's LDS below 64 KB)
 constexpr int NEAR = 256;                         // tokens of a chunk's list
+constexpr int SPARSE = 1024;                      // tokens of a chunk that can matter, where those are put together first
 constexpr int FEW = 256;                          // tokens that are compared with each other
 constexpr int SLICE = 32768;                      // rows of a launch
 static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
@@ -113,6 +114,9 @@ template <int CTRL, int ROWS> __device__ __forceinline__ u64 dpp_or(u64 none, u6
 template <int CTRL, int ROWS> __device__ __forceinline__ double dpp_or(double none, double x) {
     return __builtin_bit_cast(double, dpp_or<CTRL, ROWS>(__builtin_bit_cast(u64, none), __builtin_bit_cast(u64, x)));
 }
+template <int CTRL, int ROWS> __device__ __forceinline__ float dpp_or(float none, float x) {
+    return __builtin_bit_cast(float, dpp_or<CTRL, ROWS>(__builtin_bit_cast(u32, none), __builtin_bit_cast(u32, x)));
+}
 // Inclusive sums over a wave; op over a wave, in every lane.
 template <class N> __device__ __forceinline__ N wave_scan(N x) {
     x += dpp_or<0x111, 0xF>(N(0), x);
@@ -125,6 +129,7 @@ template <class N> __device__ __forceinline__ N wave_scan(N x) {
 }
 __device__ __forceinline__ u32 last_lane(u32 x) { return (u32)__builtin_amdgcn_readlane((int)x, 63); }
 __device__ __forceinline__ u64 last_lane(u64 x) { return (u64)last_lane((u32)(x >> 32)) << 32 | last_lane((u32)x); }
+__device__ __forceinline__ float last_lane(float x) { return __builtin_bit_cast(float, last_lane(__builtin_bit_cast(u32, x))); }
 __device__ __forceinline__ double last_lane(double x) { return __builtin_bit_cast(double, last_lane(__builtin_bit_cast(u64, x))); }
 template <class N, class Op> __device__ __forceinline__ N wave_all(N x, Op op) {
     x = op(x, dpp_or<0x111, 0xF>(x, x));
@@ -156,98 +161,136 @@ __device__ __forceinline__ int room(int *count, int n) {
 // Whether top_k limits the row (the same in both kernels).
 __device__ __forceinline__ bool limited(int top_k, int V) { return top_k > 0 && top_k < V; }
 
+// Bound: its arithmetic, some 30 instructions a token that can matter (the bin and the
+// mantissa in 64 bits) and 6 for the others.
 __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
-    constexpr int PER = CHUNK / CHUNK_THREADS / 4, WAVES = CHUNK_THREADS / 64;
+    constexpr int PER = CHUNK / CHUNK_THREADS, WAVES = CHUNK_THREADS / 64;
+    constexpr float LEAST = -3.402823466e38f;     // the least logit that counts
     // two histograms, of the even and the odd lanes: half the lanes of a wave meet in a bin
     __shared__ __align__(16) u64 hist[BINS][2];
-    __shared__ u64 waves[WAVES], near[NEAR];
-    __shared__ u32 floors[WAVES], counts[WAVES];
+    __shared__ u64 near[NEAR];
+    __shared__ uint16_t some[SPARSE];             // places in the chunk
+    __shared__ float tops[WAVES], floors[WAVES];
+    __shared__ u32 counts[WAVES];
     __shared__ double steps[OCTAVE];
-    __shared__ int n;
+    __shared__ int n_some, n_near, first_most;
     const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
     const float t = temperature_of(a, row);
-    const int first = chunk * CHUNK + 4 * tid;
-    f4 v[PER];
+    const int base = chunk * CHUNK;
+    auto place = [&](int i) { return 4 * tid + 4 * CHUNK_THREADS * (i / 4) + i % 4; };
+    float v[PER];
 #pragma unroll
-    for (int p = 0; p < PER; ++p) {
-        const int i = first + p * 4 * CHUNK_THREADS;
+    for (int p = 0; p < PER; p += 4) {
+        const int i = base + place(p);
         if (i + 4 <= a.V) {
-            v[p] = *(const f4u *)(l + i);
+            const f4 x = *(const f4u *)(l + i);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[p + j] = x[j];
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[p][j] = i + j < a.V ? l[min(i + j, a.V - 1)] : -__builtin_inff();
+            for (int j = 0; j < 4; ++j) v[p + j] = i + j < a.V ? l[min(i + j, a.V - 1)] : -__builtin_inff();
         }
     }
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
     for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
-    if (tid == 0) n = 0;
-    make_steps(steps);
-    u64 best = 0;
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const u64 x = token_of(key_of(v[p][j]), first + p * 4 * CHUNK_THREADS + j);
-            best = x > best ? x : best;
-        }
-    // Keys below `floor` cannot be among the first top_k tokens: so many groups of
-    // lanes (of 8 up to 64 tokens, of one up to 512) have a greater one.
-    const bool by_k = limited(top_k, a.V);
-    u32 floor_ = (u32)(best >> 32);
-    if (by_k && top_k <= CHUNK_THREADS / 8) {
-        floor_ = max(floor_, dpp_or<0xB1, 0xF>(floor_, floor_));
-        floor_ = max(floor_, dpp_or<0x4E, 0xF>(floor_, floor_));
-        floor_ = max(floor_, dpp_or<0x141, 0xF>(floor_, floor_));
+    if (tid == 0) {
+        n_some = n_near = 0;
+        first_most = INT32_MAX;
     }
-    floor_ = wave_all(floor_, [](u32 p, u32 q) { return min(p, q); });
-    best = wave_max(best);
+    make_steps(steps);
+    const float none = -__builtin_inff();
+    float mine = none;                            // (a NaN is never the larger one)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) mine = fmaxf(mine, v[i]);
+    // Logits below `floor` cannot be among the first top_k: so many groups of lanes
+    // have a greater one.
+    const bool by_k = limited(top_k, a.V);
+    float floor_ = mine;
+    if (by_k && top_k <= CHUNK_THREADS / 2) floor_ = fmaxf(floor_, dpp_or<0xB1, 0xF>(floor_, floor_));
+    if (by_k && top_k <= CHUNK_THREADS / 4) floor_ = fmaxf(floor_, dpp_or<0x4E, 0xF>(floor_, floor_));
+    if (by_k && top_k <= CHUNK_THREADS / 8) floor_ = fmaxf(floor_, dpp_or<0x141, 0xF>(floor_, floor_));
+    floor_ = wave_all(floor_, [](float p, float q) { return fminf(p, q); });
+    float most = wave_all(mine, [](float p, float q) { return fmaxf(p, q); });
     if (lane == 0) {
-        waves[tid >> 6] = best;
+        tops[tid >> 6] = most;
         floors[tid >> 6] = floor_;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-        best = waves[w] > best ? waves[w] : best;
-        floor_ = min(floor_, floors[w]);
+        most = fmaxf(most, tops[w]);
+        floor_ = fminf(floor_, floors[w]);
     }
-    const u32 top = (u32)(best >> 32);
     const int64_t at = (int64_t)row * a.chunks + chunk;
-    if (tid == 0) a.tops[at] = best;
-    if (!top || !(t > 0.f)) return;
-    const Scale s = scale_of(t, steps);
-    const float most = logit_of(top);
-    if (by_k) {
-        floor_ = top_k <= CHUNK_THREADS ? floor_ : 0;
-    } else {
-        // with min_p alone: nor can keys of less than that part of the largest weight (and a little less)
-        floor_ = 0;
-        if (!(top_p < 1.f) && min_p > 0.f) {
-            const float x = most + t * fminf(logf(min_p), 0.f);
-            floor_ = key_of(x - (fabsf(most) + fabsf(x)) * 0x1p-18f - 1e-30f);
-        }
+    if (!(most > none)) {
+        if (tid == 0) a.tops[at] = 0;
+        return;
     }
-    floor_ = max(floor_, 1u);
+    if (mine == most) {
+        int i = PER - 1;
+#pragma unroll
+        for (int j = PER - 2; j >= 0; --j) i = v[j] == most ? j : i;
+        atomicMin(&first_most, base + place(i));
+    }
+    if (!(t > 0.f)) {
+        __syncthreads();
+        if (tid == 0) a.tops[at] = token_of(key_of(most), first_most);
+        return;
+    }
+    const Scale s = scale_of(t, steps);
     const double from = s.bin(most);
     const int phase = phase_of(from);
-    u32 bins[2 * PER] = {};                       // two in one
+    bool sparse = by_k && top_k <= CHUNK_THREADS;
+    if (!by_k && !(top_p < 1.f) && min_p > 0.f) {
+        // with min_p alone: nor can logits of less than that part of the largest weight (and a little less)
+        const float x = most + t * fminf(logf(min_p), 0.f);
+        floor_ = x - (fabsf(most) + fabsf(x)) * 0x1p-18f - 1e-30f;
+        sparse = true;
+    }
+    floor_ = sparse ? fmaxf(floor_, LEAST) : LEAST;
+    auto bin_of = [&](float x) {
+        const double d = from - s.bin(x);
+        return x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
+    };
+    auto count = [&](float x) {
+        const int b = bin_of(x);
+        // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
+        const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x, (phase - b) & (OCTAVE - 1)) : 0;
+        atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
+    };
+    auto from_floor = [&](float floor) {
+        u32 mask = 0;
 #pragma unroll
-    for (int p = 0; p < PER; ++p)
+        for (int i = 0; i < PER; ++i) mask |= (u32)(v[i] >= floor) << i;
+        return mask;
+    };
+    if (sparse) {
+        u32 mask = from_floor(floor_);
+        int to = room(&n_some, __popc(mask));
+        for (; mask; mask &= mask - 1, ++to)
+            if (to < SPARSE) some[to] = (uint16_t)place(__builtin_ctz(mask));
+        __syncthreads();
+        sparse = n_some <= SPARSE;
+    }
+    float x[SPARSE / CHUNK_THREADS];              // (read again: a lane's logits cannot be picked by number)
+    int at_[SPARSE / CHUNK_THREADS];
+    if (sparse) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = v[p][j];
-            int b = BINS;
-            if (key_of(x) >= floor_) {
-                const double d = from - s.bin(x);
-                b = x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
-                // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
-                const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x, (phase - b) & (OCTAVE - 1)) : 0;
-                atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
-            }
-            bins[2 * p + j / 2] |= (u32)b << (16 * (j & 1));
+        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i) {
+            const bool in = tid + i * CHUNK_THREADS < n_some;
+            at_[i] = base + (in ? some[tid + i * CHUNK_THREADS] : 0);
+            x[i] = in ? l[at_[i]] : none;
         }
+#pragma unroll
+        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i)
+            if (x[i] > none) count(x[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (v[i] >= floor_) count(v[i]);
+    }
     __syncthreads();
     // the list: whole bins from the top, as many as fit
     const u64 h = hist[tid][0] + hist[tid][1];
@@ -255,20 +298,38 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     u32 upto = wave_scan((u32)(h >> COUNT_SHIFT));
     if (lane == 63) counts[tid >> 6] = upto;
     __syncthreads();
-    for (int w = 0; w < tid >> 6; ++w) upto += counts[w];
+#pragma unroll
+    for (int w = 0; w < WAVES - 1; ++w) upto += w < tid >> 6 ? counts[w] : 0;
     const int depth = __syncthreads_count(upto <= NEAR);
-    u32 mask = 0;
+    if (sparse) {
 #pragma unroll
-    for (int i = 0; i < 4 * PER; ++i) mask |= (u32)((int)(bins[i / 2] >> (16 * (i & 1)) & 0xFFFF) < depth) << i;
-    int to = room(&n, __popc(mask));
-#pragma unroll
-    for (int p = 0; p < PER; ++p)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (mask >> (4 * p + j) & 1) near[to++] = token_of(key_of(v[p][j]), first + p * 4 * CHUNK_THREADS + j);
+        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i) {
+            const bool in = x[i] > none && bin_of(x[i]) < depth;
+            const int to = room(&n_near, in);
+            if (in) near[to] = token_of(key_of(x[i]), at_[i]);
+        }
+    } else {
+        // what can lie in these bins, and a little more, and then what does
+        float lo = floor_;
+        if (depth < BINS && s.eighths > 0.0 && most < __builtin_inff()) {
+            const double y = (from - depth + 1) / s.eighths;
+            lo = fmaxf(lo, (float)(y - fabs(y) * 0x1p-22) - 1e-37f);
+        }
+        u32 mask = from_floor(lo), in = 0;
+        for (u32 left = mask; left; left &= left - 1)
+            if (bin_of(l[base + place(__builtin_ctz(left))]) < depth) in |= left & -left;
+        int to = room(&n_near, __popc(in));
+        for (; in; in &= in - 1, ++to) {
+            const int i = base + place(__builtin_ctz(in));
+            near[to] = token_of(key_of(l[i]), i);
+        }
+    }
     __syncthreads();
-    for (int i = tid; i < n; i += CHUNK_THREADS) a.near[at * NEAR + i] = near[i];
-    if (tid == 0) a.near_n[at] = (u32)n | (u32)depth << 16;
+    for (int i = tid; i < n_near; i += CHUNK_THREADS) a.near[at * NEAR + i] = near[i];
+    if (tid == 0) {
+        a.tops[at] = token_of(key_of(most), first_most);
+        a.near_n[at] = (u32)n_near | (u32)depth << 16;
+    }
 }
 static_assert(CHUNK_THREADS == BINS, "a thread a bin");
 
