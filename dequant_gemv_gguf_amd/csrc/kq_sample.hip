@@ -102,6 +102,18 @@ __device__ __forceinline__ int phase_of(double from) {
     return from < __builtin_inf() ? (int)(from - OCTAVE * floor(from / OCTAVE)) : OCTAVE - 1;
 }
 
+// Logits i .. i + 3 of a row, -infinity past its end.
+__device__ __forceinline__ f4 four(const float *l, int i, int V) {
+    f4 x;
+    if (i + 4 <= V) {
+        x = *(const f4u *)(l + i);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = i + j < V ? l[min(i + j, V - 1)] : -__builtin_inff();
+    }
+    return x;
+}
+
 __device__ __forceinline__ float temperature_of(const Sample &a, int row) { return a.temperature ? a.temperature[row] : 1.f; }
 
 // Across lanes, by DPP: the value of another lane, or `none` where there is none.
@@ -182,15 +194,9 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     float v[PER];
 #pragma unroll
     for (int p = 0; p < PER; p += 4) {
-        const int i = base + place(p);
-        if (i + 4 <= a.V) {
-            const f4 x = *(const f4u *)(l + i);
+        const f4 x = four(l, base + place(p), a.V);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[p + j] = x[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[p + j] = i + j < a.V ? l[min(i + j, a.V - 1)] : -__builtin_inff();
-        }
+        for (int j = 0; j < 4; ++j) v[p + j] = x[j];
     }
     const int top_k = a.top_k ? a.top_k[row] : 0;
     const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
@@ -346,7 +352,7 @@ struct RowSpace {
     u32 digit_count[256];
     u64 chunk_list[MAX_CHUNKS];     // kept weight of a chunk's gathered tokens
     double chunk_sum[MAX_CHUNKS];
-    u64 waves[ROW_WAVES];
+    u64 waves[ROW_WAVES], waves_all[ROW_WAVES];
     double waves_d[ROW_WAVES];
     u64 found[4];                   // (0 .. 2 a digit, 3 a token)
     double picked[2];
@@ -393,16 +399,24 @@ struct Row {
 template <bool WEIGHTS, class Each>
 __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 want) {
     const int tid = threadIdx.x, lane = tid & 63;
-    u64 any = 0, differ = 0;
-    each([&](u64 token, auto &&) { any = token >= from ? token : any; });
-    if (any) m.found[0] = any;
+    u64 any = 0, all = ~0ull;
+    each([&](u64 token, auto &&) {
+        if (token < from) return;
+        any |= token;
+        all &= token;
+    });
+    any = wave_all(any, [](u64 p, u64 q) { return p | q; });
+    all = wave_all(all, [](u64 p, u64 q) { return p & q; });
+    if (lane == 0) {
+        m.waves[tid >> 6] = any;
+        m.waves_all[tid >> 6] = all;
+    }
     __syncthreads();
-    any = m.found[0];
-    each([&](u64 token, auto &&) { differ |= token >= from ? token ^ any : 0; });
-    differ = wave_all(differ, [](u64 p, u64 q) { return p | q; });
-    if (lane == 0) m.waves[tid >> 6] = differ;
-    __syncthreads();
-    for (int w = 0; w < ROW_WAVES; ++w) differ |= m.waves[w];
+    for (int w = 0; w < ROW_WAVES; ++w) {
+        any |= m.waves[w];
+        all &= m.waves_all[w];
+    }
+    const u64 differ = any ^ all;
     if (!differ) return any;
     int above = 64 - __builtin_clzll(differ);           // bits from here on are `prefix`
     u64 prefix = above < 64 ? any >> above : 0, before = 0;
@@ -528,21 +542,28 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     make_steps(m.steps);
     __syncthreads();
     r.least = min_p > 0.f ? (double)min_p * (double)r.mantissa(most, 0) : 0.0;
-    for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-        const int off = m.off[c];
-        if (off < 0) continue;                    // it has no histogram
-        const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
-        u64 x[BINS / 64];
+    // (two chunks a wave at a time; one without a token has no histogram)
+    for (int c0 = wave; c0 < a.chunks; c0 += 2 * ROW_WAVES) {
+        u64 x[2][BINS / 64];
+        int off[2];
 #pragma unroll
-        for (int i = 0; i < BINS / 64; ++i) x[i] = h[lane + 64 * i];
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + k * ROW_WAVES;
+            off[k] = c < a.chunks ? m.off[c] : -1;
+            const u64 *h = a.hist + ((int64_t)row * a.chunks + (off[k] >= 0 ? c : 0)) * BINS;
 #pragma unroll
-        for (int i = 0; i < BINS / 64; ++i) {
-            const int d = lane + 64 * i, b = min(d + off, BINS - 1);
-            if (!x[i]) continue;
-            atomicAdd(&m.count[b], (u32)(x[i] >> COUNT_SHIFT));
-            const u64 w = x[i] & ((1ull << COUNT_SHIFT) - 1);
-            if (w && b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], w);
+            for (int i = 0; i < BINS / 64; ++i) x[k][i] = off[k] >= 0 ? h[lane + 64 * i] : 0;
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int i = 0; i < BINS / 64; ++i) {
+                if (!x[k][i]) continue;
+                const int b = min(lane + 64 * i + off[k], BINS - 1);
+                atomicAdd(&m.count[b], (u32)(x[k][i] >> COUNT_SHIFT));
+                const u64 w = x[k][i] & ((1ull << COUNT_SHIFT) - 1);
+                if (w && b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], w);
+            }
     }
     __syncthreads();
     {
@@ -635,6 +656,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
         const u64 token = m.few[min(i, n - 1)].token, weight = m.few[min(i, n - 1)].weight;
         u64 upto = 0, place = 0;
+#pragma unroll 4
         for (int j = part; j < n; j += 4) {
             const bool before = m.few[j].token >= token;
             place += before;
@@ -662,6 +684,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         const double at = (u > 0.f ? (double)u : 0.0) * (double)sum;
         const u64 past = at < (double)sum ? min((u64)at, sum - 1) : sum - 1;
         u64 before = 0;
+#pragma unroll 4
         for (int j = part; j < n; j += 4) before += (u32)m.few[j].token > (u32)token ? m.few[j].weight : 0;
         before = quad_sum(before);
         if (part == 0 && kept && before <= past && past < before + weight) {
@@ -687,19 +710,11 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
             hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
         }
-        constexpr int BATCH = 4;                  // pieces of 4 a thread; the next ones are on their way
+        constexpr int BATCH = 8;                  // pieces of 4 a thread; the next ones are on their way
         f4 now[BATCH], next[BATCH];
         auto ask = [&](f4 (&x)[BATCH], int i0) {
 #pragma unroll
-            for (int p = 0; p < BATCH; ++p) {
-                const int i = i0 + 4 * ROW_THREADS * p;
-                if (i + 4 <= a.V) {
-                    x[p] = *(const f4u *)(r.l + i);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x[p][j] = i + j < a.V ? r.l[min(i + j, a.V - 1)] : -__builtin_inff();
-                }
-            }
+            for (int p = 0; p < BATCH; ++p) x[p] = four(r.l, i0 + 4 * ROW_THREADS * p, a.V);
         };
         ask(now, 4 * tid);
         for (int i0 = 0; i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
@@ -826,13 +841,15 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     constexpr int EACH = CHUNK / ROW_THREADS;
     const int first = m.n * CHUNK + EACH * tid;
     const double at = m.picked[0], sum = m.picked[1];
+    f4 logits[EACH / 4];
+#pragma unroll
+    for (int j = 0; j < EACH / 4; ++j) logits[j] = four(r.l, first + 4 * j, a.V);
     double w[EACH], mine = 0.0;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
-        const int i = first + j;
-        const float x = i < a.V ? r.l[i] : -__builtin_inff();
+        const float x = logits[j / 4][j % 4];
         const u32 key = key_of(x);
-        const u64 token = token_of(key, i);
+        const u64 token = token_of(key, first + j);
         w[j] = 0.0;
         if (key && token >= least) {
             const double v = r.weight(x);
