@@ -14,8 +14,8 @@ struct Moe {
     const float *x, *add, *router, *bias;
     const uint8_t *gate, *up, *down;
     float *y;
-    int32_t *ids;               // [T][k], the caller's or scratch
-    float *weights;             // [T][k], or NULL
+    int32_t *ids;               // [T][k], the caller's or scratch, as weights
+    float *weights;             // [T][k]
     double *logits;             // [T][E] scratch
     float *inner;               // [T][k][inner] scratch
     int64_t ldx, ldadd, ldy;

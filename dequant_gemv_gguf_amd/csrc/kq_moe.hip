@@ -71,13 +71,14 @@ static int layer_check(const kqstep_moe_layer *l, int64_t *gate_bytes, int64_t *
 
 static size_t round16(size_t n) { return (n + 15) & ~(size_t)15; }
 
-// The parts of a workspace: logits, inner rows, ids.
-struct MoeSpace { size_t inner, ids, end; };
+// The parts of a workspace: logits, inner rows, ids, weights.
+struct MoeSpace { size_t inner, ids, weights, end; };
 static MoeSpace moe_space(const kqstep_moe_layer *l, int T) {
     MoeSpace s;
     s.inner = round16((size_t)T * l->E * sizeof(double));
     s.ids = s.inner + round16((size_t)T * l->k * l->inner * sizeof(float));
-    s.end = s.ids + round16((size_t)T * l->k * sizeof(int32_t));
+    s.weights = s.ids + round16((size_t)T * l->k * sizeof(int32_t));
+    s.end = s.weights + round16((size_t)T * l->k * sizeof(float));
     return s;
 }
 
@@ -126,7 +127,7 @@ int kqstep_moe(const kqstep_moe_layer *layer, int T, const float *x, int64_t ldx
     a.down = (const uint8_t *)layer->down;
     a.y = y;
     a.ids = ids ? ids : (int32_t *)(ws + s.ids);
-    a.weights = weights;
+    a.weights = weights ? weights : (float *)(ws + s.weights);
     a.logits = (double *)ws;
     a.inner = (float *)(ws + s.inner);
     a.ldx = ldx;

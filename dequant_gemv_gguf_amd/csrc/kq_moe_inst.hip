@@ -1,12 +1,15 @@
 // kq_moe_inst.hip -- the experts' products of kqstep_moe for one block format,
 // KQ_MOE_TYPE.
 //
-// Bound: HBM (a token's experts' weights, read once), for one token the chain of
-// logits, choice, weights.  One work-group a compute unit, for one token and a
-// tile of rows: a wave takes an expert and streams its rows through registers, two
-// steps of them on the way at a time.  Each lane holds the activations of its unit
-// of the rows (unit u on lane u % lanes_per_row of a lane group, see kq_impl.h) in
-// registers: they are read once for all rows, and the loop reads no LDS for them.
+// Bound: HBM (a token's experts' weights, read once) and, from four tokens on, the
+// vector units' work on them; for one token the chain of logits, choice, weights.
+// A work-group takes one token and a tile of rows, a wave one expert's rows of the
+// tile: it streams them through registers, DEPTH units of a lane on their way at a
+// time.  The activations are put into LDS once for the work-group (asked for by every
+// wave from the cache they took 3300 cycles before its first weights) and from there
+// into registers, those of a lane's unit (unit u on lane u % lanes_per_row of a lane
+// group, see kq_impl.h), while the first weights are on their way: the loop itself
+// reads no LDS.
 // An expert that several tokens chose is read once per token, but their
 // work-groups of one tile sit on one XCD and go through it side by side, so that
 // its L2 serves the second read.
@@ -15,18 +18,26 @@
 namespace kq {
 namespace step {
 
-constexpr int MOE_WAVES = 8, MOE_THREADS = 64 * MOE_WAVES;
-constexpr int MOE_RESULTS = 8192;      // floats of LDS for the rows' sums
+// Waves of a work-group, at most, and of a compute unit: as many as the kernel's
+// registers let on its SIMDs.
+constexpr int MOE_WAVES = 8;
+template <int T> constexpr int GATE_RESIDENT() { return BIG_UNIT<T>() || T == T_Q2_K ? 12 : 16; }
+template <int T> constexpr int DOWN_RESIDENT() { return Fmt<T>::QK == 32 ? 16 : 12; }
+constexpr int DEPTH = 2;
+constexpr int MOE_LDS = 54 * 1024 / 4;         // floats of LDS that a launch asks for, at most (64 KB with the kernels' own)
+constexpr int MOE_RESULTS = 2048;              // of them for the rows' sums
 
 // How a call's rows lie on the grid: `waves` a work-group, `parts` of them a
 // slot, `rows` of a matrix each; `tiles` work-groups a token.
 struct Split {
     int lpr, waves, parts, rows, tiles;
     u32 magic;          // i * magic >> 16 = i / k
+    u32 row_magic;      // i * row_magic >> 32 = i / (a staged row's length)
+    int staged;         // whether the activations go through LDS
 };
 
-// XReg::load in two steps: the loads, and (once other loads are on their way) the
-// sums, which wait for them.
+// XReg::load in two steps, for rows that do not fit LDS: the loads, and the sums,
+// which wait for them.
 template <int T> __device__ __forceinline__ void ask_unit(XReg<T> &xr, const float *x, int u) {
     typedef XReg<T> X;
     const float *p = x + unit_e0<T>(u);
@@ -37,40 +48,83 @@ template <int T> __device__ __forceinline__ void sum_unit(XReg<T> &xr) {
 #pragma unroll
     for (int r = 0; r < XReg<T>::NS; ++r) xr.s[r] = sum16(xr.v[4 * r], xr.v[4 * r + 1], xr.v[4 * r + 2], xr.v[4 * r + 3]);
 }
-template <int T> __device__ __forceinline__ void ask_first(XReg<T> &xr, const float *x, int n, int lpr) {
-    const int units = (n / Fmt<T>::QK) * Fmt<T>::UPB;
-    ask_unit<T>(xr, x, min((int)threadIdx.x & (lpr - 1), units - 1));
+
+// A row of n activations into LDS as stage_x leaves them, 4 a thread: asked for, and put.
+constexpr int ASK = 4;
+__device__ __forceinline__ void ask_row(f4 (&v)[ASK], const float *x, int n, int from, int threads) {
+#pragma unroll
+    for (int i = 0; i < ASK; ++i) {
+        const int e = 4 * (from + (int)threadIdx.x + i * threads);
+        v[i] = *reinterpret_cast<const f4 *>(x + (e < n ? e : 0));
+    }
+}
+__device__ __forceinline__ void put_row(const f4 (&v)[ASK], float *xs, float *ss, int n, int from, int threads) {
+#pragma unroll
+    for (int i = 0; i < ASK; ++i) {
+        const int e = 4 * (from + (int)threadIdx.x + i * threads);
+        // (n is a multiple of 32: the four lanes of 16 activations are here together)
+        float s = (v[i].x + v[i].y) + (v[i].z + v[i].w);
+        s = dpp_add(s, 0);
+        s = dpp_add(s, 1);
+        if (e < n) {
+            *reinterpret_cast<f4 *>(xs + xpad(e)) = v[i];
+            if ((e & 15) == 0) ss[e >> 4] = s;
+        }
+    }
+}
+__device__ __forceinline__ void stage_row(float *xs, float *ss, const float *x, int n, int from, int threads) {
+    for (; 4 * from < n; from += ASK * threads) {
+        f4 v[ASK];
+        ask_row(v, x, n, from, threads);
+        put_row(v, xs, ss, n, from, threads);
+    }
 }
 
+// The activations of a lane's unit: from LDS (xs: a staged row of n), or from x.
+struct Activations {
+    const float *xs, *x;
+    int n;
+    template <int T> __device__ __forceinline__ void unit(XReg<T> &xr, int u) const {
+        if (xs) {
+            const int e0 = unit_e0<T>(u);
+            xreg_from_lds<T>(xr, XLds{xs, xs + x_stride(n), 0, 0, xpad(e0), e0 >> 4, sum_run_stride<T>()});
+        } else {
+            ask_unit<T>(xr, x, u);
+            sum_unit<T>(xr);
+        }
+    }
+};
+
 // Sums of `count` rows (of row_bytes each, from the start of rs[m] + delta[m] on) of
-// N matrices with the activations of unit u, added to (ADD) or put into
-// out[m * count + row].  D units a lane are on their way, those of the N matrices
-// in turn; `meanwhile` runs when the first ones are asked for.
-template <int T, int N, int D, bool ADD, class Fn>
-__device__ __forceinline__ void stream_rows(const rsrc_t (&rs)[N], const u32 (&delta)[N], u32 row_bytes, int count, int lpr, int u,
-                                            bool in, XReg<T> &xr, float *out, Fn &&meanwhile) {
+// N matrices with the activations of units u0 + the lane's, added to (ADD) or put into
+// out[m * count + row].
+template <int T, int N, bool ADD>
+__device__ __forceinline__ void stream_rows(const rsrc_t (&rs)[N], const u32 (&delta)[N], u32 row_bytes, int count, int lpr, int u0,
+                                            const Activations &x, float *out) {
     typedef Fmt<T> F;
     typedef typename RawOf<T>::type Raw;
-    constexpr int R = D / N;               // rows of a lane group a turn
+    constexpr int R = DEPTH / N;           // rows of a lane group a turn
     const int lane = threadIdx.x & 63, slot = lane & (lpr - 1), sh = __builtin_ctz(lpr), grp = lane >> sh, G = 64 >> sh;
-    const int sub = u % F::UPB;
+    const int units = (x.n / F::QK) * F::UPB;
+    const bool in = u0 + slot < units;
+    const int u = in ? u0 + slot : 0, sub = u % F::UPB;
     const u32 boff = (u32)(u / F::UPB) * F::BYTES;
-    Raw ring[D][1];
+    Raw ring[DEPTH][1];
     // past the last row: zeros, and nothing is read
     auto issue = [&](int d, int row) {
         const int i = row + grp + G * (d / N);
         load_unit(ring[d][0], rs[d % N], in && i < count ? delta[d % N] + (u32)i * row_bytes + boff : OOB, sub);
     };
-    const int idx = scatter_idx<D>(lane), row_of = grp + G * (idx / N);
+    const int idx = scatter_idx<DEPTH>(lane), row_of = grp + G * (idx / N);
 #pragma unroll
-    for (int d = 0; d < D; ++d) issue(d, 0);
+    for (int d = 0; d < DEPTH; ++d) issue(d, 0);
     __builtin_amdgcn_sched_barrier(0);
-    meanwhile();
-    sum_unit<T>(xr);
+    XReg<T> xr;
+    x.unit<T>(xr, u);
     for (int row = 0; row < count; row += G * R) {
-        float w[D];
+        float w[DEPTH];
 #pragma unroll
-        for (int d = 0; d < D; ++d) {
+        for (int d = 0; d < DEPTH; ++d) {
             __builtin_amdgcn_sched_barrier(0);
             float v[1][1];
             val_unit<1, 1>(ring[d], sub, xr, v);
@@ -78,21 +132,20 @@ __device__ __forceinline__ void stream_rows(const rsrc_t (&rs)[N], const u32 (&d
             issue(d, row + G * R);
         }
         __builtin_amdgcn_sched_barrier(0);
-        const float s = reduce_scatter<D>(w, lane, lpr);
+        const float s = reduce_scatter<DEPTH>(w, lane, lpr);
         const int i = row + row_of;
-        if (slot < D && i < count) {
+        if (slot < DEPTH && i < count) {
             float *o = out + (idx % N) * count + i;
             *o = ADD ? *o + s : s;
         }
     }
 }
 
-// The same over whole rows of n activations at x; xr: those of the lane's first
-// unit, asked for (its last one's afterwards: two sets would not fit the registers).
-template <int T, int N, int D, class Fn>
-__device__ __forceinline__ void row_sums(const uint8_t *const (&W)[N], int64_t row_bytes, int count, int n, int lpr, const float *x,
-                                         XReg<T> &xr, float *out, Fn &&meanwhile) {
-    const int slot = threadIdx.x & (lpr - 1), units = (n / Fmt<T>::QK) * Fmt<T>::UPB;
+// The same over whole rows.
+template <int T, int N>
+__device__ __forceinline__ void row_sums(const uint8_t *const (&W)[N], int64_t row_bytes, int count, int lpr, const Activations &x,
+                                         float *out) {
+    const int units = (x.n / Fmt<T>::QK) * Fmt<T>::UPB;
     rsrc_t rs[N];
     u32 delta[N];
 #pragma unroll
@@ -101,12 +154,8 @@ __device__ __forceinline__ void row_sums(const uint8_t *const (&W)[N], int64_t r
         delta[m] = (u32)(at & 3u);
         rs[m] = make_rsrc((const void *)(at - delta[m]), delta[m] + (u32)(count * row_bytes));
     }
-    stream_rows<T, N, D, false>(rs, delta, (u32)row_bytes, count, lpr, min(slot, units - 1), slot < units, xr, out, meanwhile);
-    for (int u0 = lpr; u0 < units; u0 += lpr) {
-        const int u = min(u0 + slot, units - 1);
-        ask_unit<T>(xr, x, u);
-        stream_rows<T, N, D, true>(rs, delta, (u32)row_bytes, count, lpr, u, u0 + slot < units, xr, out, meanwhile);
-    }
+    stream_rows<T, N, false>(rs, delta, (u32)row_bytes, count, lpr, 0, x, out);
+    for (int u0 = lpr; u0 < units; u0 += lpr) stream_rows<T, N, true>(rs, delta, (u32)row_bytes, count, lpr, u0, x, out);
 }
 
 // Keys order like the 64-bit values; NaN is the lowest, 1, and 0 an expert that is
@@ -149,21 +198,22 @@ __device__ __forceinline__ Scores scores_of(const Moe &a, const double *l) {
     return s;
 }
 
-// The token's experts, by the whole work-group, into ids[0 .. k).
-// PER 0: up to 256 experts.  An expert's place is the number of those that come
-// before it; a thread counts them over a part of the experts.
-// PER > 0: the first wave alone, a lane with PER neighbouring experts, takes k
-// times the greatest of all that is left (its upper half first).  Counting takes
-// E^2 steps over all threads, this one k of about 500 cycles whatever E: 0.6 and 1.7
-// us for 8 of 128 experts.
+// The token's experts, by the whole work-group (`waves` of them), into ids[0 .. k);
+// `meanwhile` runs while the logits are on their way.
+// MANY false: up to as many experts as threads, and 256.  An expert's place is the
+// number of those that come before it; a thread counts them over a part of the
+// experts.  A key ends in the expert's own number, so that one comparison does: logits
+// that differ by less than 2^-44 of their size count as the same.
+// MANY: the first wave alone, a lane with every 64th expert, takes k times the
+// greatest of all that is left (its upper half first).  Counting takes E^2 steps over
+// all threads, this one k of about 500 cycles whatever E.
 constexpr int COUNTED = 256;
-template <int PER, class Fn> __device__ __forceinline__ void choose(const Moe &a, const double *l, int E, int *ids, Fn &&meanwhile) {
+template <bool MANY, class Fn> __device__ __forceinline__ void choose(const Moe &a, const double *l, int E, int waves, int *ids, Fn &&meanwhile) {
     const int tid = threadIdx.x, lane = tid & 63;
-    if constexpr (PER == 0) {
+    if constexpr (!MANY) {
         __shared__ __align__(16) u64 keys[COUNTED];
         __shared__ int before[COUNTED];
-        const int width = E <= 64 ? 64 : E <= 128 ? 128 : 256, e = tid & (width - 1), part = tid / width;
-        const int parts = (int)blockDim.x / width, each = ((E + parts - 1) / parts + 1) & ~1;
+        const int sh = E <= 64 ? 6 : E <= 128 ? 7 : 8, width = 1 << sh, e = tid & (width - 1), part = tid >> sh;
         const double mine = l[min(e, E - 1)];
         __builtin_amdgcn_sched_barrier(0);
         meanwhile();
@@ -174,67 +224,60 @@ template <int PER, class Fn> __device__ __forceinline__ void choose(const Moe &a
                 const Scores s = scores_of(a, l);
                 key = order_of(weight_of(a, s, mine) / s.sum + (double)a.bias[min(e, E - 1)]);
             }
-            keys[e] = e < E ? key : 0;
+            keys[e] = e < E ? (key & ~255ull) | (255 - e) : 0;
             before[e] = 0;
         }
         __syncthreads();
-        // (a key of 0 comes before none; those behind E are 0)
-        if (part < parts) {
+        // (keys past the last expert are 0; the parts past `width` have none)
+        const int parts = waves * 64 >> sh, each = width / (parts >= 4 ? 4 : parts >= 2 ? 2 : 1);
+        if (part * each < width) {
             const u64 mine = keys[e];
             int n = 0;
-            const int first = part * each, last = min(first + each, width);
-            // (past the part: counted as none)
-            for (int j0 = first; j0 < last; j0 += 16) {
+            for (int j0 = part * each; j0 < (part + 1) * each && j0 < E; j0 += 16) {
                 ulonglong2 two[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) two[i] = *(const ulonglong2 *)(keys + min(j0 + 2 * i, COUNTED - 2));
+                for (int i = 0; i < 8; ++i) two[i] = *(const ulonglong2 *)(keys + j0 + 2 * i);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const int j = j0 + 2 * i;
-                    n += j < last && ((u64)two[i].x > mine || ((u64)two[i].x == mine && j < e));
-                    n += j < last && ((u64)two[i].y > mine || ((u64)two[i].y == mine && j + 1 < e));
+                    n += (u64)two[i].x > mine;
+                    n += (u64)two[i].y > mine;
                 }
             }
-            if (parts > 1) atomicAdd(&before[e], n);
+            if (each < width) atomicAdd(&before[e], n);
             else before[e] = n;
         }
         __syncthreads();
         if (tid < E && before[tid] < a.k) ids[before[tid]] = tid;
     } else {
+        __shared__ u64 left[MOE_EXPERTS];
         meanwhile();
         if (tid < 64) {
-            const bool biased = a.bias != nullptr;
             Scores s = {0.0, 1.0};
-            if (biased) s = scores_of(a, l);
-            u64 key[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int e = lane * PER + i;
-                key[i] = 0;
-                if (e < E) key[i] = order_of(biased ? weight_of(a, s, l[e]) / s.sum + (double)a.bias[e] : l[e]);
+            if (a.bias) s = scores_of(a, l);
+            u64 best = 0;
+            int who = 0;
+            for (int e = lane; e < E; e += 64) {
+                const u64 key = order_of(a.bias ? weight_of(a, s, l[e]) / s.sum + (double)a.bias[e] : l[e]);
+                left[e] = key;
+                if (key > best) {
+                    best = key;
+                    who = e;
+                }
             }
             for (int j = 0; j < a.k; ++j) {
-                u64 best = key[0];
-                int at = 0;
-#pragma unroll
-                for (int i = 1; i < PER; ++i)
-                    if (key[i] > best) {
-                        best = key[i];
-                        at = i;
-                    }
                 const u32 hi = (u32)(best >> 32), lo = (u32)best;
-                const u32 top = wave_max_u32(hi);
-                u64 who = __ballot(hi == top);
-                if (who & (who - 1)) {
-                    const u32 low = wave_max_u32(hi == top ? lo : 0u);
-                    who = __ballot(hi == top && lo == low);
-                }
-                const int winner = __builtin_ctzll(who);                 // the lowest lane has the lowest expert
-                if (lane == winner) {
-                    ids[j] = lane * PER + at;
-#pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        if (i == at) key[i] = 0;
+                const u32 top = wave_max_u32(hi), low = wave_max_u32(hi == top ? lo : 0u);
+                // the lowest of those that have it
+                const u32 first = ~wave_max_u32(hi == top && lo == low ? ~(u32)who : 0u);
+                if ((u32)who == first && best) {
+                    ids[j] = who;
+                    left[who] = 0;
+                    best = 0;
+                    for (int e = lane; e < E; e += 64)
+                        if (left[e] > best) {
+                            best = left[e];
+                            who = e;
+                        }
                 }
             }
         }
@@ -269,22 +312,32 @@ __device__ __forceinline__ void wave_sync() {
     __builtin_amdgcn_wave_barrier();
 }
 
-template <int T, int D, int PER>
-__global__ __launch_bounds__(MOE_THREADS) void gate_up_kernel(const double *logits, const float *xs, int E, int lpr, int hidden, int tiles,
-                                                              const Moe a, const Split s) {
-    __shared__ float results[MOE_RESULTS];
+extern __shared__ __align__(16) float moe_lds[];
+
+// The work-group behind a token's last tile computes the weights of its experts.
+template <int T, bool MANY>
+__global__ __launch_bounds__(64 * MOE_WAVES) void gate_up_kernel(const double *logits, const float *xs, int64_t ldx, int E, int hidden,
+                                                                     const Moe a, const Split s) {
     __shared__ int ids[MOE_SLOTS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int t = blockIdx.y, tile = tile_of();
-    if (tile >= tiles) return;
-    XReg<T> xr;
-    const float *x = xs;
-    choose<PER>(a, logits + (int64_t)t * E, E, ids, [&] {
-        x += t * a.ldx;
-        ask_first<T>(xr, x, hidden, lpr);
+    const float *x = xs + t * ldx;
+    logits += (int64_t)t * E;
+    const Activations act = {s.staged ? moe_lds : nullptr, x, hidden};
+    choose<MANY>(a, logits, E, s.waves, ids, [&] {
+        if (s.staged && tile < s.tiles) stage_row(moe_lds, moe_lds + x_stride(hidden), x, hidden, 0, 64 * s.waves);
     });
-    if (tile == 0 && (int)threadIdx.x < a.k) a.ids[t * a.k + threadIdx.x] = ids[threadIdx.x];
-    float *mine = results + wave * s.rows * 2;
+    if (tile >= s.tiles) {
+        if (tile == s.tiles && wave == 0) {
+            const float w = weights_of(a, logits, ids);
+            if (lane < a.k) {
+                a.ids[t * a.k + lane] = ids[lane];
+                a.weights[t * a.k + lane] = w;
+            }
+        }
+        return;
+    }
+    float *mine = moe_lds + (s.staged ? x_stride(hidden) + s_stride(hidden) : 0) + wave * s.rows * 2;
     for (int i = wave; i < a.k * s.parts; i += s.waves) {
         const int part = (int)((u32)i * s.magic >> 16), j = i - part * a.k;
         const int first = (tile * s.parts + part) * s.rows, count = min(a.n_inner - first, s.rows);
@@ -292,8 +345,7 @@ __global__ __launch_bounds__(MOE_THREADS) void gate_up_kernel(const double *logi
         const int e = __builtin_amdgcn_readfirstlane(ids[j]);
         const int64_t base = ((int64_t)e * a.n_inner + first) * a.gate_bytes;
         const uint8_t *W[2] = {a.gate + base, a.up + base};
-        if (i != wave) ask_first<T>(xr, x, a.hidden, s.lpr);
-        row_sums<T, 2, D>(W, a.gate_bytes, count, a.hidden, s.lpr, x, xr, mine, [] {});
+        row_sums<T, 2>(W, a.gate_bytes, count, s.lpr, act, mine);
         wave_sync();
         float *out = a.inner + ((int64_t)t * a.k + j) * a.n_inner + first;
         for (int r = lane; r < count; r += 64) out[r] = act_of(a.act, mine[r]) * mine[count + r];
@@ -302,79 +354,112 @@ __global__ __launch_bounds__(MOE_THREADS) void gate_up_kernel(const double *logi
 }
 
 // The slots' sums meet in LDS and are added in their order.
-template <int T, int D>
-__global__ __launch_bounds__(MOE_THREADS) void down_kernel(const int32_t *ids, const float *inner, int k, int n_inner, int lpr, u32 magic,
-                                                           const Moe a, const Split s) {
-    __shared__ float results[MOE_RESULTS];
-    __shared__ float weights[MOE_SLOTS];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+template <int T>
+__global__ __launch_bounds__(64 * MOE_WAVES) void down_kernel(const int32_t *ids, const float *inner, int k, int n_inner, int waves, int staged,
+                                                                  const Moe a, const Split s) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int t = blockIdx.y, tile = tile_of();
     if (tile >= s.tiles) return;
-    const int rows = s.rows * s.parts;
-    for (int i = wave; i < a.k * s.parts; i += s.waves) {
-        const int part = (int)((u32)i * magic >> 16), j = i - part * k;
-        const int first = tile * rows + part * s.rows, count = min(a.hidden - first, s.rows);
-        if (count <= 0) break;
-        const float *x = inner + ((int64_t)t * k + j) * n_inner;
-        XReg<T> xr;
-        const int e = __builtin_amdgcn_readfirstlane(ids[t * k + j]);
-        ask_first<T>(xr, x, n_inner, lpr);
-        const uint8_t *W[1] = {a.down + ((int64_t)e * a.hidden + first) * a.down_bytes};
-        row_sums<T, 1, D>(W, a.down_bytes, count, n_inner, lpr, x, xr, results + j * rows + part * s.rows, [&] {
-            if (i == 0) {
-                const float w = weights_of(a, a.logits + (int64_t)t * a.E, ids + t * k);
-                if (lane < a.k) {
-                    weights[lane] = w;
-                    if (tile == 0 && a.weights) a.weights[t * a.k + lane] = w;
+    inner += (int64_t)t * k * n_inner;
+    ids += t * k;
+    const int stride = x_stride(n_inner) + s_stride(n_inner);
+    // the slots' rows (each a multiple of 32 long) as they lie behind each other
+    f4 v[ASK];
+    if (staged) ask_row(v, inner, k * n_inner, 0, 64 * waves);
+    // the wave's first expert, whose number is on its way as well
+    const int first_id = ids[wave < k ? wave : (int)((u32)wave % (u32)k)];
+    if (staged) {
+        const int threads = 64 * waves;
+        for (int from = 0;;) {
+#pragma unroll
+            for (int i = 0; i < ASK; ++i) {
+                const int e = 4 * (from + (int)threadIdx.x + i * threads), j = (int)__umulhi((u32)e, s.row_magic), at = e - j * n_inner;
+                float sum = (v[i].x + v[i].y) + (v[i].z + v[i].w);
+                sum = dpp_add(sum, 0);
+                sum = dpp_add(sum, 1);
+                if (j < k) {
+                    float *xs = moe_lds + j * stride;
+                    *reinterpret_cast<f4 *>(xs + xpad(at)) = v[i];
+                    if ((at & 15) == 0) xs[x_stride(n_inner) + (at >> 4)] = sum;
                 }
             }
-        });
+            from += ASK * threads;
+            if (4 * from >= k * n_inner) break;
+            ask_row(v, inner, k * n_inner, from, threads);
+        }
+        __syncthreads();
+    }
+    float *results = moe_lds + (staged ? k * stride : 0);
+    const int rows = s.rows * s.parts;
+    for (int i = wave; i < k * s.parts; i += waves) {
+        const int part = (int)((u32)i * s.magic >> 16), j = i - part * k;
+        const int first = tile * rows + part * s.rows, count = min(a.hidden - first, s.rows);
+        if (count <= 0) break;
+        const int e = __builtin_amdgcn_readfirstlane(i == wave ? first_id : ids[j]);
+        const uint8_t *W[1] = {a.down + ((int64_t)e * a.hidden + first) * a.down_bytes};
+        const Activations x = {staged ? moe_lds + j * stride : nullptr, inner + (int64_t)j * n_inner, n_inner};
+        row_sums<T, 1>(W, a.down_bytes, count, s.lpr, x, results + j * rows + part * s.rows);
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < rows; i += blockDim.x) {
+    for (int i = threadIdx.x; i < rows; i += 64 * waves) {
         const int row = tile * rows + i;
         if (row >= a.hidden) break;
         float sum = a.add ? a.add[t * a.ldadd + row] : 0.f;
-        for (int j = 0; j < a.k; ++j) sum = __builtin_fmaf(weights[j], results[j * rows + i], sum);
+        for (int j = 0; j < k; ++j) sum = __builtin_fmaf(a.weights[t * k + j], results[j * rows + i], sum);
         a.y[t * a.ldy + row] = sum;
     }
 }
 
-// A work-group a compute unit (as many as fit beside each other make no
-// difference to what is on its way), tiles of equal size.
-static Split split_of(const Moe &a, int rows, int lpr, int results) {
+// Tiles of equal size for all the work-groups that run at once; `matrices` of `rows`
+// rows of n weights, `units` units, `floats` of LDS for the activations of a work-group.
+static Split split_of(const Moe &a, int resident, int rows, int matrices, int units, int n, int64_t floats, int spare) {
     Split s;
-    s.lpr = lpr;
     s.parts = a.k >= MOE_WAVES ? 1 : MOE_WAVES / a.k;
-    s.waves = a.k > MOE_WAVES ? (a.k + 1) / 2 : a.k * s.parts;
+    // (waves of a work-group take the slots in equal rounds)
+    const int rounds = (a.k * s.parts + MOE_WAVES - 1) / MOE_WAVES;
+    s.waves = (a.k * s.parts + rounds - 1) / rounds;
     s.magic = (u32)((65536 + a.k - 1) / a.k);
-    const int wgs = std::max(1, cu_count() / a.T);
-    const int most = std::max(1, MOE_RESULTS / results);
+    // (exact below 2^32 / n: the rows staged have fewer than 2^14 activations in all)
+    s.row_magic = (u32)(((1ull << 32) + n - 1) / n);
+    const int wgs = std::max(1, resident / s.waves * cu_count() / a.T - spare);
+    const int slots = matrices == 2 ? s.waves : a.k * s.parts;          // that hold results at once
+    const int most = MOE_RESULTS / (matrices * slots);
     s.rows = std::min((rows + wgs * s.parts - 1) / (wgs * s.parts), most);
     s.tiles = (rows + s.rows * s.parts - 1) / (s.rows * s.parts);
+    s.staged = floats + MOE_RESULTS <= MOE_LDS;
+    // Lanes of a row: those with which a wave's rows take the fewest turns, where
+    // another part of a row costs about two thirds of a unit for its activations.
+    int best = 0;
+    for (int lpr = 16; lpr <= 64; lpr *= 2) {
+        const int stripes = (units + lpr - 1) / lpr, turns = (s.rows * matrices * lpr + 64 * DEPTH - 1) / (64 * DEPTH) * DEPTH;
+        const int cost = stripes * (3 * turns + 2);
+        if (!best || cost < best) {
+            best = cost;
+            s.lpr = lpr;
+        }
+    }
     return s;
 }
 
-// Units a lane has on their way.
-template <int T> constexpr int DEPTH() { return BIG_UNIT<T>() ? 2 : 4; }
+static dim3 moe_grid(const Moe &a, int tiles) { return dim3(8, (unsigned)a.T, (unsigned)((tiles + 7) / 8)); }
 
-template <int T, int PER> static void gate_up(const Moe &a, const Split &s, hipStream_t st) {
-    hipLaunchKernelGGL((gate_up_kernel<T, DEPTH<T>(), PER>), dim3(8, (unsigned)a.T, (unsigned)((s.tiles + 7) / 8)), dim3(64 * s.waves), 0, st,
-                       a.logits, a.x, a.E, s.lpr, a.hidden, s.tiles, a, s);
+template <int T, bool MANY> static void gate_up(const Moe &a, const Split &s, size_t lds, hipStream_t st) {
+    hipLaunchKernelGGL((gate_up_kernel<T, MANY>), moe_grid(a, s.tiles + 1), dim3(64 * s.waves), lds, st, a.logits, a.x, a.ldx, a.E, a.hidden, a, s);
 }
 template <int T> int launch_gate_up(const Moe &a, hipStream_t st) {
-    const int lpr = lanes_per_row(a.hidden / Fmt<T>::QK * Fmt<T>::UPB);
-    const int waves = a.k > MOE_WAVES ? (a.k + 1) / 2 : a.k * std::max(1, MOE_WAVES / a.k);
-    const Split s = split_of(a, a.n_inner, lpr, 2 * waves);
-    if (a.E <= COUNTED) gate_up<T, 0>(a, s, st);
-    else gate_up<T, MOE_EXPERTS / 64>(a, s, st);
+    const int64_t floats = x_stride(a.hidden) + s_stride(a.hidden);
+    const Split s = split_of(a, GATE_RESIDENT<T>(), a.n_inner, 2, a.hidden / Fmt<T>::QK * Fmt<T>::UPB, a.hidden, floats, 1);
+    const size_t lds = sizeof(float) * (size_t)((s.staged ? floats : 0) + 2 * s.rows * s.waves);
+    const int width = a.E <= 64 ? 64 : a.E <= 128 ? 128 : COUNTED;
+    if (a.E <= COUNTED && width <= 64 * s.waves) gate_up<T, false>(a, s, lds, st);
+    else gate_up<T, true>(a, s, lds, st);
     return kv::launched();
 }
 template <int T> int launch_down(const Moe &a, hipStream_t st) {
-    const int lpr = lanes_per_row(a.n_inner / Fmt<T>::QK * Fmt<T>::UPB);
-    const Split s = split_of(a, a.hidden, lpr, a.k * (a.k >= MOE_WAVES ? 1 : MOE_WAVES / a.k));
-    hipLaunchKernelGGL((down_kernel<T, DEPTH<T>()>), dim3(8, (unsigned)a.T, (unsigned)((s.tiles + 7) / 8)), dim3(64 * s.waves), 0, st,
-                       a.ids, a.inner, a.k, a.n_inner, s.lpr, s.magic, a, s);
+    const int64_t floats = (int64_t)a.k * (x_stride(a.n_inner) + s_stride(a.n_inner));
+    const Split s = split_of(a, DOWN_RESIDENT<T>(), a.hidden, 1, a.n_inner / Fmt<T>::QK * Fmt<T>::UPB, a.n_inner, floats, 0);
+    const size_t lds = sizeof(float) * (size_t)((s.staged ? floats : 0) + s.rows * s.parts * a.k);
+    hipLaunchKernelGGL(down_kernel<T>, moe_grid(a, s.tiles), dim3(64 * s.waves), lds, st, a.ids, a.inner, a.k, a.n_inner, s.waves, s.staged, a, s);
     return kv::launched();
 }
 
