@@ -20,16 +20,17 @@ KQ_MOE_LAUNCHERS(extern template, T_Q6_K)
 // bits, the sums' order does not depend on T.
 constexpr int ROUTER_THREADS = 256;
 
-// NT >= T tokens: their rows are asked for together (past T: the last one's again).
+// A work-group takes up to NT tokens: their rows are asked for together (past T: the
+// last one's again).
 template <int NT>
 __global__ __launch_bounds__(ROUTER_THREADS) void router_kernel(const Moe a) {
     __shared__ double waves[NT][ROUTER_THREADS / 64];
-    const int e = blockIdx.x, tid = threadIdx.x;
+    const int e = blockIdx.x, t0 = blockIdx.y * NT, tid = threadIdx.x;
     const float *w = a.router + (int64_t)e * a.hidden, *x[NT];
     double acc[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-        x[t] = a.x + min(t, a.T - 1) * a.ldx;
+        x[t] = a.x + min(t0 + t, a.T - 1) * a.ldx;
         acc[t] = 0.0;
     }
     for (int i = 4 * tid; i < a.hidden; i += 4 * ROUTER_THREADS) {
@@ -48,12 +49,24 @@ __global__ __launch_bounds__(ROUTER_THREADS) void router_kernel(const Moe a) {
         if ((tid & 63) == 0) waves[t][tid >> 6] = s;
     }
     __syncthreads();
-    if (tid < a.T) {
+    if (tid < NT && t0 + tid < a.T) {
         double s = 0.0;
 #pragma unroll
         for (int i = 0; i < ROUTER_THREADS / 64; ++i) s += waves[tid][i];
-        a.logits[tid * a.E + e] = s;
+        a.logits[(t0 + tid) * a.E + e] = s;
     }
+}
+
+template <int NT> static void launch_router(const Moe &a, hipStream_t st) {
+    hipLaunchKernelGGL(router_kernel<NT>, dim3((unsigned)a.E, (unsigned)((a.T + NT - 1) / NT)), dim3(ROUTER_THREADS), 0, st, a);
+}
+// Tokens of a work-group: as few as two work-groups a compute unit leave.
+static void launch_router(const Moe &a, hipStream_t st) {
+    const int groups = std::max(1, 2 * cu_count() / a.E), n = (a.T + groups - 1) / groups;
+    if (n <= 1) launch_router<1>(a, st);
+    else if (n <= 2) launch_router<2>(a, st);
+    else if (n <= 4) launch_router<4>(a, st);
+    else launch_router<8>(a, st);
 }
 
 static int layer_check(const kqstep_moe_layer *l, int64_t *gate_bytes, int64_t *down_bytes) {
@@ -145,8 +158,7 @@ int kqstep_moe(const kqstep_moe_layer *layer, int T, const float *x, int64_t ldx
     a.renorm = layer->renorm;
     a.act = layer->act;
     hipStream_t st = (hipStream_t)stream;
-    hipLaunchKernelGGL(T == 1 ? router_kernel<1> : T == 2 ? router_kernel<2> : T <= 4 ? router_kernel<4> : router_kernel<8>, dim3((unsigned)a.E),
-                       dim3(ROUTER_THREADS), 0, st, a);
+    launch_router(a, st);
     if ((r = kv::launched())) return r;
     if ((r = with_type(layer->gate_type, [&](auto tag) { return launch_gate_up<decltype(tag)::value>(a, st); }))) return r;
     return with_type(layer->down_type, [&](auto tag) { return launch_down<decltype(tag)::value>(a, st); });

@@ -4,8 +4,7 @@
 // Bound: HBM (a token's experts' weights, read once) and, from four tokens on, the
 // vector units' work on them; for one token the chain of logits, choice, weights.
 // A work-group takes one token and a tile of rows, a wave one expert's rows of the
-// tile: it streams them through registers, DEPTH units of a lane on their way at a
-// time.  The activations are put into LDS once for the work-group (asked for by every
+// tile: it streams them through registers.  The activations are put into LDS once for the work-group (asked for by every
 // wave from the cache they took 3300 cycles before its first weights) and from there
 // into registers, those of a lane's unit (unit u on lane u % lanes_per_row of a lane
 // group, see kq_impl.h), while the first weights are on their way: the loop itself
@@ -22,8 +21,10 @@ namespace step {
 // registers let on its SIMDs.
 constexpr int MOE_WAVES = 8;
 template <int T> constexpr int GATE_RESIDENT() { return BIG_UNIT<T>() || T == T_Q2_K ? 12 : 16; }
-template <int T> constexpr int DOWN_RESIDENT() { return Fmt<T>::QK == 32 ? 16 : 12; }
-constexpr int DEPTH = 2;
+template <int T> constexpr int DOWN_RESIDENT() { return BIG_UNIT<T>() ? 12 : 16; }
+// Units of a lane on their way in a wave.  (Two in the down kernel took a quarter of the
+// waves' registers and were slower: eight tokens 49.7 -> 48.3 us with one.)
+constexpr int GATE_DEPTH = 2, DOWN_DEPTH = 1;
 constexpr int MOE_LDS = 54 * 1024 / 4;         // floats of LDS that a launch asks for, at most (64 KB with the kernels' own)
 constexpr int MOE_RESULTS = 2048;              // of them for the rows' sums
 
@@ -98,7 +99,7 @@ struct Activations {
 // Sums of `count` rows (of row_bytes each, from the start of rs[m] + delta[m] on) of
 // N matrices with the activations of units u0 + the lane's, added to (ADD) or put into
 // out[m * count + row].
-template <int T, int N, bool ADD>
+template <int T, int N, int DEPTH, bool ADD>
 __device__ __forceinline__ void stream_rows(const rsrc_t (&rs)[N], const u32 (&delta)[N], u32 row_bytes, int count, int lpr, int u0,
                                             const Activations &x, float *out) {
     typedef Fmt<T> F;
@@ -142,7 +143,7 @@ __device__ __forceinline__ void stream_rows(const rsrc_t (&rs)[N], const u32 (&d
 }
 
 // The same over whole rows.
-template <int T, int N>
+template <int T, int N, int DEPTH>
 __device__ __forceinline__ void row_sums(const uint8_t *const (&W)[N], int64_t row_bytes, int count, int lpr, const Activations &x,
                                          float *out) {
     const int units = (x.n / Fmt<T>::QK) * Fmt<T>::UPB;
@@ -154,8 +155,8 @@ __device__ __forceinline__ void row_sums(const uint8_t *const (&W)[N], int64_t r
         delta[m] = (u32)(at & 3u);
         rs[m] = make_rsrc((const void *)(at - delta[m]), delta[m] + (u32)(count * row_bytes));
     }
-    stream_rows<T, N, false>(rs, delta, (u32)row_bytes, count, lpr, 0, x, out);
-    for (int u0 = lpr; u0 < units; u0 += lpr) stream_rows<T, N, true>(rs, delta, (u32)row_bytes, count, lpr, u0, x, out);
+    stream_rows<T, N, DEPTH, false>(rs, delta, (u32)row_bytes, count, lpr, 0, x, out);
+    for (int u0 = lpr; u0 < units; u0 += lpr) stream_rows<T, N, DEPTH, true>(rs, delta, (u32)row_bytes, count, lpr, u0, x, out);
 }
 
 // Keys order like the 64-bit values; NaN is the lowest, 1, and 0 an expert that is
@@ -345,7 +346,7 @@ __global__ __launch_bounds__(64 * MOE_WAVES) void gate_up_kernel(const double *l
         const int e = __builtin_amdgcn_readfirstlane(ids[j]);
         const int64_t base = ((int64_t)e * a.n_inner + first) * a.gate_bytes;
         const uint8_t *W[2] = {a.gate + base, a.up + base};
-        row_sums<T, 2>(W, a.gate_bytes, count, s.lpr, act, mine);
+        row_sums<T, 2, GATE_DEPTH>(W, a.gate_bytes, count, s.lpr, act, mine);
         wave_sync();
         float *out = a.inner + ((int64_t)t * a.k + j) * a.n_inner + first;
         for (int r = lane; r < count; r += 64) out[r] = act_of(a.act, mine[r]) * mine[count + r];
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(64 * MOE_WAVES) void down_kernel(const int32_t *ids
         const int e = __builtin_amdgcn_readfirstlane(i == wave ? first_id : ids[j]);
         const uint8_t *W[1] = {a.down + ((int64_t)e * a.hidden + first) * a.down_bytes};
         const Activations x = {staged ? moe_lds + j * stride : nullptr, inner + (int64_t)j * n_inner, n_inner};
-        row_sums<T, 1>(W, a.down_bytes, count, s.lpr, x, results + j * rows + part * s.rows);
+        row_sums<T, 1, DOWN_DEPTH>(W, a.down_bytes, count, s.lpr, x, results + j * rows + part * s.rows);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < rows; i += 64 * waves) {
@@ -412,7 +413,7 @@ __global__ __launch_bounds__(64 * MOE_WAVES) void down_kernel(const int32_t *ids
 
 // Tiles of equal size for all the work-groups that run at once; `matrices` of `rows`
 // rows of n weights, `units` units, `floats` of LDS for the activations of a work-group.
-static Split split_of(const Moe &a, int resident, int rows, int matrices, int units, int n, int64_t floats, int spare) {
+static Split split_of(const Moe &a, int depth, int resident, int rows, int matrices, int units, int n, int64_t floats, int spare) {
     Split s;
     s.parts = a.k >= MOE_WAVES ? 1 : MOE_WAVES / a.k;
     // (waves of a work-group take the slots in equal rounds)
@@ -431,7 +432,7 @@ static Split split_of(const Moe &a, int resident, int rows, int matrices, int un
     // another part of a row costs about two thirds of a unit for its activations.
     int best = 0;
     for (int lpr = 16; lpr <= 64; lpr *= 2) {
-        const int stripes = (units + lpr - 1) / lpr, turns = (s.rows * matrices * lpr + 64 * DEPTH - 1) / (64 * DEPTH) * DEPTH;
+        const int stripes = (units + lpr - 1) / lpr, turns = (s.rows * matrices * lpr + 64 * depth - 1) / (64 * depth) * depth;
         const int cost = stripes * (3 * turns + 2);
         if (!best || cost < best) {
             best = cost;
@@ -448,7 +449,7 @@ template <int T, bool MANY> static void gate_up(const Moe &a, const Split &s, si
 }
 template <int T> int launch_gate_up(const Moe &a, hipStream_t st) {
     const int64_t floats = x_stride(a.hidden) + s_stride(a.hidden);
-    const Split s = split_of(a, GATE_RESIDENT<T>(), a.n_inner, 2, a.hidden / Fmt<T>::QK * Fmt<T>::UPB, a.hidden, floats, 1);
+    const Split s = split_of(a, GATE_DEPTH, GATE_RESIDENT<T>(), a.n_inner, 2, a.hidden / Fmt<T>::QK * Fmt<T>::UPB, a.hidden, floats, 1);
     const size_t lds = sizeof(float) * (size_t)((s.staged ? floats : 0) + 2 * s.rows * s.waves);
     const int width = a.E <= 64 ? 64 : a.E <= 128 ? 128 : COUNTED;
     if (a.E <= COUNTED && width <= 64 * s.waves) gate_up<T, false>(a, s, lds, st);
@@ -457,7 +458,7 @@ template <int T> int launch_gate_up(const Moe &a, hipStream_t st) {
 }
 template <int T> int launch_down(const Moe &a, hipStream_t st) {
     const int64_t floats = (int64_t)a.k * (x_stride(a.n_inner) + s_stride(a.n_inner));
-    const Split s = split_of(a, DOWN_RESIDENT<T>(), a.hidden, 1, a.n_inner / Fmt<T>::QK * Fmt<T>::UPB, a.n_inner, floats, 0);
+    const Split s = split_of(a, DOWN_DEPTH, DOWN_RESIDENT<T>(), a.hidden, 1, a.n_inner / Fmt<T>::QK * Fmt<T>::UPB, a.n_inner, floats, 0);
     const size_t lds = sizeof(float) * (size_t)((s.staged ? floats : 0) + s.rows * s.parts * a.k);
     hipLaunchKernelGGL(down_kernel<T>, moe_grid(a, s.tiles), dim3(64 * s.waves), lds, st, a.ids, a.inner, a.k, a.n_inner, s.waves, s.staged, a, s);
     return kv::launched();
