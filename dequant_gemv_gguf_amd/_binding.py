@@ -643,11 +643,34 @@ def _step_call(fn, f, stream, tensors, dtypes, strides, struct, args):
 
 
 def kqstep_norm(T, heads, n, x, ldx, add, ldadd, sum, ldsum, weight, eps, y, ldy, y8=None, stream=None):
+    # (a small norm takes 2 us on the GPU: what most calls are, fp32 tensors of one device with whole rows, is looked over at once)
     if _torch_c is None:
         _load_torch()
+    C = (_lib or lib()).kqstep_norm
+    given = [t for t in (x, add, sum, weight, y) if t is not None]
+    count = len(given)
+    try:
+        device = x.get_device()
+        plain = (device >= 0 and list(map(_get_device, given)).count(device) == count and list(map(_dtype, given)).count(_float32) == count and
+                 (list(map(_is_contiguous, given)).count(True) == count or
+                  ((weight is None or weight.is_contiguous()) and
+                   all([t is None or t.is_contiguous() or (t.dim() == 2 and t.stride() == (ld, 1))
+                        for t, ld in ((x, ldx), (add, ldadd), (sum, ldsum), (y, ldy))]))) and
+                 (y8 is None or (y8.get_device() == device and y8.is_contiguous())))
+    except (AttributeError, TypeError):                # not all are tensors
+        plain = False
+    if plain:
+        if stream is None:
+            stream = _torch_c._cuda_getCurrentRawStream(device)
+        elif type(stream) is not int:
+            stream = stream.cuda_stream
+        _call("kqstep_norm", C, device,
+              (T, heads, n, x.data_ptr(), ldx, None if add is None else add.data_ptr(), ldadd, None if sum is None else sum.data_ptr(), ldsum,
+               None if weight is None else weight.data_ptr(), eps, None if y is None else y.data_ptr(), ldy,
+               None if y8 is None else y8.data_ptr(), stream))
+        return
     f = _float32
-    _step_call("kqstep_norm", (_lib or lib()).kqstep_norm, stream, (x, add, sum, weight, y, y8), [f, f, f, f, f],
-               (ldx, ldadd, ldsum, None, ldy, None), None,
+    _step_call("kqstep_norm", C, stream, (x, add, sum, weight, y, y8), [f, f, f, f, f], (ldx, ldadd, ldsum, None, ldy, None), None,
                lambda a, s: (T, heads, n, a[0], ldx, a[1], ldadd, a[2], ldsum, a[3], eps, a[4], ldy, a[5], s))
 
 
