@@ -76,7 +76,7 @@ struct Scale {
     }
     __device__ __forceinline__ double bin(float l) const { return floor(at(l)); }
     // `of_octave`: the bin's place in its octave
-    __device__ __forceinline__ u64 mantissa(float l, int of_octave) const {
+    __device__ __forceinline__ double mantissa_d(float l, int of_octave) const {
         const double y = at(l);
         // e^x for |x| <= log 2 / 16: its series to x^6 / 6! (2^-44 is left)
         const double x = l == __builtin_inff() ? -0.04332169878499658 : (y - floor(y) - 0.5) * 0.08664339756999316;
@@ -88,7 +88,10 @@ struct Scale {
         p = fma(p, x, 1.0);
         p = fma(p, x, 1.0);
         // to an integer: 2^52 in front leaves it in the low bits, rounded
-        return __builtin_bit_cast(u64, fma(p, steps[of_octave], 4503599627370496.0)) - 0x4330000000000000ull;
+        return fma(p, steps[of_octave], 0x1p52);
+    }
+    __device__ __forceinline__ u64 mantissa(float l, int of_octave) const {
+        return __builtin_bit_cast(u64, mantissa_d(l, of_octave)) - 0x4330000000000000ull;
     }
 };
 __device__ __forceinline__ Scale scale_of(float t, const double *steps) {
@@ -380,7 +383,8 @@ struct Row {
     // in units of the top octave's mantissas
     __device__ __forceinline__ double weight(float x) const {
         const int b = bin(x);
-        return b < BINS - 1 ? ldexp((double)mantissa(x, b), -octaves(b)) : 0.0;
+        const double w = ldexp(s.mantissa_d(x, (phase - b) & (OCTAVE - 1)) - 0x1p52, -octaves(b));
+        return b < BINS - 1 ? w : 0.0;
     }
     __device__ __forceinline__ u64 mantissa(float x, int b) const { return s.mantissa(x, (phase - b) & (OCTAVE - 1)); }
     __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
@@ -721,18 +725,24 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             if (i0 + 4 * ROW_THREADS * BATCH < a.V) ask(next, i0 + 4 * ROW_THREADS * BATCH + 4 * tid);
             u32 mask = 0;
 #pragma unroll
-            for (int i = 0; i < 4 * BATCH; ++i) mask |= (u32)(now[i / 4][i % 4] >= lo && now[i / 4][i % 4] <= hi) << i;
+            for (int i = 0; i < 4 * BATCH; ++i) {
+                const float x = now[i / 4][i % 4];
+                mask |= (u32)(x >= lo && x <= hi) << i;
+            }
+            // (places first: a lane's few are gone over by their bits, its logits read again)
             int to = room(&m.n, __popc(mask));
-#pragma unroll
-            for (int i = 0; i < 4 * BATCH; ++i)
-                if (mask >> i & 1) {
-                    if (to < LIST) m.list[to] = token_of(key_of(now[i / 4][i % 4]), i0 + 4 * tid + 4 * ROW_THREADS * (i / 4) + i % 4);
-                    ++to;
-                }
+            for (; mask; mask &= mask - 1, ++to) {
+                const int i = __builtin_ctz(mask);
+                if (to < LIST) m.list[to] = (u64)(u32)(i0 + 4 * tid + 4 * ROW_THREADS * (i / 4) + i % 4);
+            }
 #pragma unroll
             for (int p = 0; p < BATCH; ++p) now[p] = next[p];
         }
         __syncthreads();
+        for (int i = tid; i < min(m.n, LIST); i += ROW_THREADS) {
+            const int at = (int)m.list[i];
+            m.list[i] = token_of(key_of(r.l[at]), at);
+        }
         // (more than the bins hold: what is a rounding away from them, and with top_k, of
         // which the chunks did not count all of their tokens, any number)
         listed = m.n <= LIST;
@@ -847,14 +857,14 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     double w[EACH], mine = 0.0;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
+        // (a weight for every token, also those that are not kept: without branches the
+        // eight are computed side by side)
         const float x = logits[j / 4][j % 4];
         const u32 key = key_of(x);
         const u64 token = token_of(key, first + j);
-        w[j] = 0.0;
-        if (key && token >= least) {
-            const double v = r.weight(x);
-            if (r.keeps(token, v)) w[j] = v;
-        }
+        w[j] = r.weight(x);
+        const int kept = (key != 0) & (token >= least) & ((token == best) | (w[j] >= r.least));
+        w[j] = kept ? w[j] : 0.0;
         mine += w[j];
     }
     double upto = wave_scan(mine);
@@ -872,8 +882,10 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             if (b > at && token == a.V) token = first + j;
         }
     }
-    if (token < a.V) atomicMin(&m.low, token);
-    if (last >= 0) atomicMax(&m.high, last);
+    // (the wave's first and last ones: in LDS a thousand lanes would wait for one address)
+    const u64 here = __ballot(token < a.V), any = __ballot(last >= 0);
+    if (here && lane == __builtin_ctzll(here)) atomicMin(&m.low, token);
+    if (any && lane == 63 - __builtin_clzll(any)) atomicMax(&m.high, last);
     __syncthreads();
     token = m.low < a.V ? m.low : m.high;
     if (token < 0 && tid == 0) token = (int)~(u32)best;      // (weights that differ by a rounding left none)
