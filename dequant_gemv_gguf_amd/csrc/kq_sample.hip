@@ -97,9 +97,8 @@ struct Scale {
 __device__ __forceinline__ Scale scale_of(float t, const double *steps) {
     return Scale{t < __builtin_inff() ? 8.0 * 1.4426950408889634 / (double)t : 0.0, steps};
 }
-__device__ __forceinline__ void make_steps(double *steps) {
-    if (threadIdx.x < OCTAVE) steps[threadIdx.x] = exp2(35.0 + (threadIdx.x + 0.5) / OCTAVE);
-}
+__device__ const double STEPS[OCTAVE] = {0x1.0b5586cf9890fp+35, 0x1.2387a6e756238p+35, 0x1.3dea64c123422p+35, 0x1.5ab07dd485429p+35,
+                                         0x1.7a11473eb0187p+35, 0x1.9c49182a3f090p+35, 0x1.c199bdd85529cp+35, 0x1.ea4afa2a490dap+35};
 // from mod OCTAVE, of the first token's bin (an infinite one: the octave's last)
 __device__ __forceinline__ int phase_of(double from) {
     return from < __builtin_inf() ? (int)(from - OCTAVE * floor(from / OCTAVE)) : OCTAVE - 1;
@@ -117,7 +116,22 @@ __device__ __forceinline__ f4 four(const float *l, int i, int V) {
     return x;
 }
 
-__device__ __forceinline__ float temperature_of(const Sample &a, int row) { return a.temperature ? a.temperature[row] : 1.f; }
+// A load that stays where it is written: others are put off until past the first
+// return, and then wait behind what they could have been on their way with.
+template <class N> __device__ __forceinline__ N at_once(const N *p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WAVEFRONT);
+}
+
+// A row's settings, all on their way at once (what is not given is read where u is).
+struct Settings {
+    float t, top_p, min_p, u;
+    int top_k;
+};
+__device__ __forceinline__ Settings settings_of(const Sample &a, int row) {
+    const float t = (a.temperature ? a.temperature : a.u)[row], p = (a.top_p ? a.top_p : a.u)[row], m = (a.min_p ? a.min_p : a.u)[row];
+    const int k = (a.top_k ? a.top_k : (const int32_t *)a.u)[row];
+    return Settings{a.temperature ? t : 1.f, a.top_p ? p : 1.f, a.min_p ? m : 0.f, a.u[row], a.top_k ? k : 0};
+}
 
 // Across lanes, by DPP: the value of another lane, or `none` where there is none.
 template <int CTRL, int ROWS> __device__ __forceinline__ u32 dpp_or(u32 none, u32 x) {
@@ -191,7 +205,10 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     __shared__ int n_some, n_near, first_most;
     const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
-    const float t = temperature_of(a, row);
+    const Settings set = settings_of(a, row);
+    const double step = STEPS[tid & (OCTAVE - 1)];
+    const float t = set.t, top_p = set.top_p, min_p = set.min_p;
+    const int top_k = set.top_k;
     const int base = chunk * CHUNK;
     auto place = [&](int i) { return 4 * tid + 4 * CHUNK_THREADS * (i / 4) + i % 4; };
     float v[PER];
@@ -201,14 +218,12 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) v[p + j] = x[j];
     }
-    const int top_k = a.top_k ? a.top_k[row] : 0;
-    const float top_p = a.top_p ? a.top_p[row] : 1.f, min_p = a.min_p ? a.min_p[row] : 0.f;
     for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
     if (tid == 0) {
         n_some = n_near = 0;
         first_most = INT32_MAX;
     }
-    make_steps(steps);
+    if (tid < OCTAVE) steps[tid] = step;
     const float none = -__builtin_inff();
     float mine = none;                            // (a NaN is never the larger one)
 #pragma unroll
@@ -489,16 +504,44 @@ __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
 __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     __shared__ RowSpace m;
     const int row = a.row0 + blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const float t = temperature_of(a, row);
-    const u64 *tops = a.tops + (int64_t)row * a.chunks;
+    const Settings set = settings_of(a, row);
+    const double step = STEPS[tid & (OCTAVE - 1)];
+    const float t = set.t, top_p = set.top_p, min_p = set.min_p;
+    const int top_k = set.top_k;
+    const int64_t chunk0 = (int64_t)row * a.chunks;
+    // What a wave needs first is asked for at once: the histograms of two chunks, the
+    // list of one.  (Not all of it was written: a chunk without a token has neither, a
+    // list is as long as near_n says.)
+    u64 bins[2][BINS / 64], listed_[NEAR / 64];
+    auto ask_bins = [&](int k, int c) {
+        if (c >= a.chunks) return;
+        const u64 *h = a.hist + (chunk0 + c) * BINS;
+#pragma unroll
+        for (int i = 0; i < BINS / 64; ++i) bins[k][i] = at_once(h + lane + 64 * i);
+    };
+    auto ask_list = [&](int c) {
+        if (c >= a.chunks) return;
+        const u64 *from = a.near + (chunk0 + c) * NEAR;
+#pragma unroll
+        for (int i = 0; i < NEAR / 64; ++i) listed_[i] = at_once(from + lane + 64 * i);
+    };
     // a lane's chunks: c = lane, lane + 64
     u64 first_of[MAX_CHUNKS / 64], best = 0;
     u32 near_n[MAX_CHUNKS / 64];
 #pragma unroll
     for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-        const int c = lane + 64 * i;
-        first_of[i] = c < a.chunks ? tops[c] : 0;
-        near_n[i] = c < a.chunks ? a.near_n[(int64_t)row * a.chunks + c] : 0;
+        const int64_t c = chunk0 + min(lane + 64 * i, a.chunks - 1);
+        first_of[i] = at_once(a.tops + c);
+        near_n[i] = at_once(a.near_n + c);
+    }
+    if (t > 0.f) {
+        ask_bins(0, wave);
+        ask_bins(1, wave + ROW_WAVES);
+        ask_list(wave);
+    }
+#pragma unroll
+    for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+        if (lane + 64 * i >= a.chunks) first_of[i] = near_n[i] = 0;
         best = first_of[i] > best ? first_of[i] : best;
     }
     best = wave_max(best);
@@ -517,9 +560,6 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const float most = logit_of((u32)(best >> 32));
     r.from = r.s.bin(most);
     r.phase = phase_of(r.from);
-    const float min_p = a.min_p ? a.min_p[row] : 0.f;
-    const int top_k = a.top_k ? a.top_k[row] : 0;
-    const float top_p = a.top_p ? a.top_p[row] : 1.f;
 
     // the row's histogram
     for (int b = tid; b < BINS; b += ROW_THREADS) {
@@ -543,31 +583,26 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
         if (lane == 0) m.most = m.sum = 0;
     }
-    make_steps(m.steps);
+    if (tid < OCTAVE) m.steps[tid] = step;
     __syncthreads();
     r.least = min_p > 0.f ? (double)min_p * (double)r.mantissa(most, 0) : 0.0;
-    // (two chunks a wave at a time; one without a token has no histogram)
     for (int c0 = wave; c0 < a.chunks; c0 += 2 * ROW_WAVES) {
-        u64 x[2][BINS / 64];
-        int off[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const int c = c0 + k * ROW_WAVES;
-            off[k] = c < a.chunks ? m.off[c] : -1;
-            const u64 *h = a.hist + ((int64_t)row * a.chunks + (off[k] >= 0 ? c : 0)) * BINS;
-#pragma unroll
-            for (int i = 0; i < BINS / 64; ++i) x[k][i] = off[k] >= 0 ? h[lane + 64 * i] : 0;
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
+            const int c = c0 + k * ROW_WAVES, off = c < a.chunks ? m.off[c] : -1;
+            if (off < 0) continue;
 #pragma unroll
             for (int i = 0; i < BINS / 64; ++i) {
-                if (!x[k][i]) continue;
-                const int b = min(lane + 64 * i + off[k], BINS - 1);
-                atomicAdd(&m.count[b], (u32)(x[k][i] >> COUNT_SHIFT));
-                const u64 w = x[k][i] & ((1ull << COUNT_SHIFT) - 1);
+                const u64 x = bins[k][i];
+                if (!x) continue;
+                const int b = min(lane + 64 * i + off, BINS - 1);
+                atomicAdd(&m.count[b], (u32)(x >> COUNT_SHIFT));
+                const u64 w = x & ((1ull << COUNT_SHIFT) - 1);
                 if (w && b < BINS - 1) atomicAdd((unsigned long long *)&m.weight[b], w);
             }
+        }
+        ask_bins(0, c0 + 2 * ROW_WAVES);
+        ask_bins(1, c0 + 3 * ROW_WAVES);
     }
     __syncthreads();
     {
@@ -631,22 +666,19 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     // the tokens of bins high .. low in the chunks' lists, each with a place of its own
     auto from_lists = [&](int high, int low, auto &&put) {
         for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+            if (c != wave) ask_list(c);
             if (m.off[c] < 0 || m.off[c] > low) continue;
             const int n = (int)((u32)__builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63) & 0xFFFF);
-            const u64 *from = a.near + ((int64_t)row * a.chunks + c) * NEAR;
-            u64 token[NEAR / 64];
             u32 mask = 0;
 #pragma unroll
-            for (int i = 0; i < NEAR / 64; ++i) token[i] = lane + 64 * i < n ? from[lane + 64 * i] : 0;
-#pragma unroll
             for (int i = 0; i < NEAR / 64; ++i) {
-                const int b = token[i] ? r.bin(logit_of((u32)(token[i] >> 32))) : BINS;
+                const int b = lane + 64 * i < n ? r.bin(logit_of((u32)(listed_[i] >> 32))) : BINS;
                 mask |= (u32)(b >= high && b <= low) << i;
             }
             int to = room(&m.n, __popc(mask));
 #pragma unroll
             for (int i = 0; i < NEAR / 64; ++i)
-                if (mask >> i & 1) put(to++, token[i]);
+                if (mask >> i & 1) put(to++, listed_[i]);
         }
     };
     if (near && m.counts[low] <= FEW) {
@@ -654,11 +686,12 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         from_lists(0, low, [&](int to, u64 token) {
             if (to >= FEW) return;
             m.few[to].token = token;
-            m.few[to].weight = r.integer(token, 14, 0);
         });
         __syncthreads();
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
-        const u64 token = m.few[min(i, n - 1)].token, weight = m.few[min(i, n - 1)].weight;
+        const u64 token = m.few[min(i, n - 1)].token, weight = r.integer(token, 14, 0);
+        if (i < n && part == 0) m.few[i].weight = weight;
+        __syncthreads();
         u64 upto = 0, place = 0;
 #pragma unroll 4
         for (int j = part; j < n; j += 4) {
@@ -684,7 +717,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         __syncthreads();
         // the kept weights up to each token, by index
         const u64 sum = m.sum;
-        const float u = a.u[row];
+        const float u = set.u;
         const double at = (u > 0.f ? (double)u : 0.0) * (double)sum;
         const u64 past = at < (double)sum ? min((u64)at, sum - 1) : sum - 1;
         u64 before = 0;
@@ -826,7 +859,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             mine += s[i];
         }
         const double upto = wave_scan(mine), sum = last_lane(upto);
-        const float u = a.u[row];
+        const float u = set.u;
         const double at = (u > 0.f ? fmin((double)u, 1.0) : 0.0) * sum;
         // the first lane whose sum passes `at`, else the last that has any weight
         const u64 past = __ballot(upto > at && mine > 0.0), some = __ballot(mine > 0.0);
