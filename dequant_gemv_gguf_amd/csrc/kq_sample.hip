@@ -71,15 +71,17 @@ __device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 
 struct Scale {
     double eighths;         // of an octave, per logit: 8 log2(e) / t
     const double *steps;    // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
-    __device__ __forceinline__ double at(float l) const {
-        return l == __builtin_inff() ? __builtin_inf() : (double)l * eighths;
-    }
+    // (an infinite temperature's eighths are 0, so that an infinite logit lies at NaN: not
+    // among any bins, which is right for all but the first token, and that has bin 0)
+    __device__ __forceinline__ double at(float l) const { return (double)l * eighths; }
     __device__ __forceinline__ double bin(float l) const { return floor(at(l)); }
     // `of_octave`: the bin's place in its octave
     __device__ __forceinline__ double mantissa_d(float l, int of_octave) const {
         const double y = at(l);
         // e^x for |x| <= log 2 / 16: its series to x^6 / 6! (2^-44 is left)
-        const double x = l == __builtin_inff() ? -0.04332169878499658 : (y - floor(y) - 0.5) * 0.08664339756999316;
+        // (an infinite logit: the least mantissa.  y - floor(y) would become fma(l, eighths,
+        // -floor(y)), which where y is large is the rounding of y and no fraction)
+        const double x = fmax(__builtin_amdgcn_fract(y) - 0.5, -0.5) * 0.08664339756999316;
         double p = 1.0 / 720.0;
         p = fma(p, x, 1.0 / 120.0);
         p = fma(p, x, 1.0 / 24.0);
@@ -887,16 +889,17 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     f4 logits[EACH / 4];
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) logits[j] = four(r.l, first + 4 * j, a.V);
+    // (`least` as a logit and an index)
+    const float last_x = least ? logit_of((u32)(least >> 32)) : -__builtin_inff();
+    const int last_i = least ? (int)~(u32)least : -1, best_i = (int)~(u32)best;
     double w[EACH], mine = 0.0;
 #pragma unroll
     for (int j = 0; j < EACH; ++j) {
         // (a weight for every token, also those that are not kept: without branches the
         // eight are computed side by side)
         const float x = logits[j / 4][j % 4];
-        const u32 key = key_of(x);
-        const u64 token = token_of(key, first + j);
         w[j] = r.weight(x);
-        const int kept = (key != 0) & (token >= least) & ((token == best) | (w[j] >= r.least));
+        const int kept = ((x > last_x) | ((x == last_x) & (first + j <= last_i))) & ((first + j == best_i) | (w[j] >= r.least));
         w[j] = kept ? w[j] : 0.0;
         mine += w[j];
     }
