@@ -372,7 +372,7 @@ struct RowSpace {
     u32 digit_count[256];
     u64 chunk_list[MAX_CHUNKS];     // kept weight of a chunk's gathered tokens
     double chunk_sum[MAX_CHUNKS];
-    u64 waves[ROW_WAVES], waves_all[ROW_WAVES];
+    u64 waves[ROW_WAVES];
     double waves_d[ROW_WAVES];
     u64 found[4];                   // (0 .. 2 a digit, 3 a token)
     double picked[2];
@@ -415,32 +415,15 @@ struct Row {
 
 // The shortest leading part (descending) of the tokens from `from` on that `each` goes
 // over, of which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the
-// whole sum): the part is the tokens from the returned one on.  Digits of 8 bits, from
-// the first bit in which two tokens differ.
+// whole sum): the part is the tokens from the returned one on.  Digits of 8 bits of
+// what a token is above `from` (to find the bits in which they differ instead takes two
+// reductions and 1.5 us), from the first that one up to `top`, the most that
+// any is, can have.
 template <bool WEIGHTS, class Each>
-__device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 want) {
+__device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, u64 want) {
     const int tid = threadIdx.x, lane = tid & 63;
-    u64 any = 0, all = ~0ull;
-    each([&](u64 token, auto &&) {
-        if (token < from) return;
-        any |= token;
-        all &= token;
-    });
-    any = wave_all(any, [](u64 p, u64 q) { return p | q; });
-    all = wave_all(all, [](u64 p, u64 q) { return p & q; });
-    if (lane == 0) {
-        m.waves[tid >> 6] = any;
-        m.waves_all[tid >> 6] = all;
-    }
-    __syncthreads();
-    for (int w = 0; w < ROW_WAVES; ++w) {
-        any |= m.waves[w];
-        all &= m.waves_all[w];
-    }
-    const u64 differ = any ^ all;
-    if (!differ) return any;
-    int above = 64 - __builtin_clzll(differ);           // bits from here on are `prefix`
-    u64 prefix = above < 64 ? any >> above : 0, before = 0;
+    int above = top > from ? 64 - __builtin_clzll(top - from) : 0;       // bits from here on are `prefix`
+    u64 prefix = 0, before = 0;
     while (above) {
         const int shift = max(above - 8, 0);
         const u32 digits = (1u << (above - shift)) - 1;
@@ -451,8 +434,9 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 want)
         }
         __syncthreads();
         each([&](u64 token, auto &&weight) {
-            if (token < from || (above < 64 && token >> above != prefix)) return;
-            const u32 d = (u32)(token >> shift) & digits;
+            const u64 v = token - from;
+            if (token < from || (above < 64 && v >> above != prefix)) return;
+            const u32 d = (u32)(v >> shift) & digits;
             atomicAdd(&m.digit_count[d], 1u);
             if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], weight());
         });
@@ -483,13 +467,13 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 want)
         above = shift;
         if (m.found[2] == 1 && shift) {     // one token has these digits: that one
             each([&](u64 token, auto &&) {
-                if (token >= from && token >> shift == prefix) m.found[3] = token;
+                if (token >= from && (token - from) >> shift == prefix) m.found[3] = token;
             });
             __syncthreads();
             return m.found[3];
         }
     }
-    return prefix;
+    return from + prefix;
 }
 
 __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
@@ -735,6 +719,16 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const int high = by_k ? 0 : low;              // bins high .. low are gathered
     const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
     const bool scan = low < BINS;
+    // what can lie in these bins, and a little more
+    float lo = -__builtin_inff(), hi = __builtin_inff();
+    if (r.s.eighths > 0.0 && most < __builtin_inff()) {
+        if (low < BINS - 1) {
+            const double x = (r.from - low) / r.s.eighths;
+            lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
+        }
+        const double y = (r.from - high + 1) / r.s.eighths;
+        hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
+    }
     bool listed = scan && low < BINS - 1 && gathered <= LIST - 64;
     if (listed && near) {
         from_lists(high, low, [&](int to, u64 token) {
@@ -742,13 +736,6 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         });
         __syncthreads();
     } else if (listed) {
-        // what can lie in these bins, and a little more
-        float lo = -__builtin_inff(), hi = __builtin_inff();
-        if (r.s.eighths > 0.0 && most < __builtin_inff()) {
-            const double x = (r.from - low) / r.s.eighths, y = (r.from - high + 1) / r.s.eighths;
-            lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
-            hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
-        }
         constexpr int BATCH = 8;                  // pieces of 4 a thread; the next ones are on their way
         f4 now[BATCH], next[BATCH];
         auto ask = [&](f4 (&x)[BATCH], int i0) {
@@ -789,7 +776,9 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     u64 least = 0;                                // the last token that top_k and top_p keep
     // each(f): f(token, weight()) for every gathered token
     auto places = [&](auto &&each) {
-        if (by_k && total >= top_k) least = cut<false>(m, each, 0, (u64)top_k);
+        // (where the tokens of these bins lie; the whole row's begin at the first one)
+        const u64 lowest = (u64)key_of(lo) << 32, top = listed ? min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF) : best;
+        if (by_k && total >= top_k) least = cut<false>(m, each, lowest, top, (u64)top_k);
         if (by_p && (by_k || !listed || low == m.low)) {
             // Of what top_k leaves; in the one bin that decides, what the bins above it
             // leave; over the row, of all its weight.
@@ -798,7 +787,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             sum = block_sum(m, sum);
             const double want = one && listed ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
                                               : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
-            least = cut<true>(m, each, least, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
+            least = cut<true>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
         // kept weight of the gathered tokens, by chunk
