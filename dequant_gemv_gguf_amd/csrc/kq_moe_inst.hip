@@ -4,11 +4,11 @@
 // Bound: HBM (a token's experts' weights, read once) and, from four tokens on, the
 // vector units' work on them; for one token the chain of logits, choice, weights.
 // A work-group takes one token and a tile of rows, a wave one expert's rows of the
-// tile: it streams them through registers.  The activations are put into LDS once for the work-group (asked for by every
-// wave from the cache they took 3300 cycles before its first weights) and from there
-// into registers, those of a lane's unit (unit u on lane u % lanes_per_row of a lane
-// group, see kq_impl.h), while the first weights are on their way: the loop itself
-// reads no LDS.
+// tile: it streams them through registers.  The activations are put into LDS once for
+// the work-group (asked for by every wave from the cache they took 3300 cycles before
+// its first weights) and from there into registers, those of a lane's unit (unit u on
+// lane u % lanes_per_row of a lane group, see kq_impl.h), while the first weights are
+// on their way: the loop itself reads no LDS.
 // An expert that several tokens chose is read once per token, but their
 // work-groups of one tile sit on one XCD and go through it side by side, so that
 // its L2 serves the second read.
@@ -201,7 +201,7 @@ __device__ __forceinline__ Scores scores_of(const Moe &a, const double *l) {
 
 // The token's experts, by the whole work-group (`waves` of them), into ids[0 .. k);
 // `meanwhile` runs while the logits are on their way.
-// MANY false: up to as many experts as threads, and 256.  An expert's place is the
+// MANY false: up to 256 experts, which are no more than threads.  An expert's place is the
 // number of those that come before it; a thread counts them over a part of the
 // experts.  A key ends in the expert's own number, so that one comparison does: logits
 // that differ by less than 2^-44 of their size count as the same.
@@ -422,18 +422,25 @@ static Split split_of(const Moe &a, int depth, int resident, int rows, int matri
     s.magic = (u32)((65536 + a.k - 1) / a.k);
     // (exact below 2^32 / n: the rows staged have fewer than 2^14 activations in all)
     s.row_magic = (u32)(((1ull << 32) + n - 1) / n);
-    const int wgs = std::max(1, resident / s.waves * cu_count() / a.T - spare);
     const int slots = matrices == 2 ? s.waves : a.k * s.parts;          // that hold results at once
     const int most = MOE_RESULTS / (matrices * slots);
-    s.rows = std::min((rows + wgs * s.parts - 1) / (wgs * s.parts), most);
+    auto rows_of = [&](int T) {
+        const int wgs = std::max(1, resident / s.waves * cu_count() / T - spare);
+        return std::min((rows + wgs * s.parts - 1) / (wgs * s.parts), most);
+    };
+    s.rows = rows_of(a.T);
     s.tiles = (rows + s.rows * s.parts - 1) / (s.rows * s.parts);
     s.staged = floats + MOE_RESULTS <= MOE_LDS;
     // Lanes of a row: those with which a wave's rows take the fewest turns, where
-    // another part of a row costs about two thirds of a unit for its activations.
+    // another part of a row costs more than a unit for its activations (three tokens of 5120 x 1536, rows of 80
+    // units: three parts of 32 lanes 85 us, five of 16 lanes 88).  (As
+    // one token's call has them: a row's sum, whose order follows from it, is the same
+    // in every call.)
+    const int one = rows_of(1);
     int best = 0;
     for (int lpr = 16; lpr <= 64; lpr *= 2) {
-        const int stripes = (units + lpr - 1) / lpr, turns = (s.rows * matrices * lpr + 64 * depth - 1) / (64 * depth) * depth;
-        const int cost = stripes * (3 * turns + 2);
+        const int stripes = (units + lpr - 1) / lpr, turns = (one * matrices * lpr + 64 * depth - 1) / (64 * depth) * depth;
+        const int cost = stripes * (3 * turns + 4);
         if (!best || cost < best) {
             best = cost;
             s.lpr = lpr;
@@ -451,8 +458,7 @@ template <int T> int launch_gate_up(const Moe &a, hipStream_t st) {
     const int64_t floats = x_stride(a.hidden) + s_stride(a.hidden);
     const Split s = split_of(a, GATE_DEPTH, GATE_RESIDENT<T>(), a.n_inner, 2, a.hidden / Fmt<T>::QK * Fmt<T>::UPB, a.hidden, floats, 1);
     const size_t lds = sizeof(float) * (size_t)((s.staged ? floats : 0) + 2 * s.rows * s.waves);
-    const int width = a.E <= 64 ? 64 : a.E <= 128 ? 128 : COUNTED;
-    if (a.E <= COUNTED && width <= 64 * s.waves) gate_up<T, false>(a, s, lds, st);
+    if (a.E <= COUNTED) gate_up<T, false>(a, s, lds, st);      // (s.waves is 5 or more: a thread an expert)
     else gate_up<T, true>(a, s, lds, st);
     return kv::launched();
 }

@@ -26,7 +26,7 @@
  * side by side when they write different memory (each needs its own
  * workspace).  A workspace is scratch that needs no preparation and keeps
  * nothing between calls.  Reruns are bit-identical, and a token's (or row's)
- * results do not depend on the other tokens of its call.  Rows of fp32 are
+ * results do not depend on the other tokens of its call or on their number.  Rows of fp32 are
  * 16-byte aligned with strides that are multiples of 4 floats (kqstep_sample's
  * logits: any); int32 and float arrays 4-byte aligned, workspaces 16-byte.
  */
@@ -111,7 +111,8 @@ size_t kqstep_moe_workspace_bytes(const kqstep_moe_layer *layer, int T);
  *   y = add + sum_j p_j down[e_j] . (act(gate[e_j] . x) * (up[e_j] . x))
  *
  * Logits, scores and weights are computed in 64 bits (so that experts whose
- * logits differ by a rounding are not mistaken for each other), the weights
+ * logits differ by an fp32 rounding are not mistaken for each other; up to 256
+ * experts, those within 2^-44 of each other's size count as equal), the weights
  * rounded once; the products as in kq_qgemv, in fp32, each within 1e-4 *
  * sum|w*x| + 1e-6 of the exact one.
  *   x, add, y  [T] rows of `hidden` fp32, strides ldx, ldadd, ldy.  add NULL: 0.
@@ -149,8 +150,10 @@ size_t kqstep_sample_workspace_bytes(int M, int64_t V);
  *   tokens       [M] int32
  *   probs        [M] fp32 the token's part of the kept weight, or NULL
  *   workspace    kqstep_sample_workspace_bytes
- * Weights are computed in 64 bits and summed as multiples of 2^-42, exactly, so
- * that no sum depends on its order; weights below half of that are 0.
+ * Weights are computed in 64 bits and rounded to 36 of mantissa; those 64 octaves
+ * below the row's largest count as 0.  They are summed as integers over 8192
+ * tokens at a time, by parts of an octave, and those sums in 64 bits in a fixed
+ * order.
  * 0 <= M <= 65536, 1 <= V <= 2^20. */
 int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float *temperature, const int32_t *top_k,
                   const float *top_p, const float *min_p, const float *u, int32_t *tokens, float *probs, void *workspace,

@@ -108,6 +108,20 @@ def test_tokens(T):
     assert torch.equal(one[0], y[T - 1]) and torch.equal(i1[0], ids[T - 1]) and torch.equal(p1[0], p[T - 1])
 
 
+@pytest.mark.parametrize("k, hidden, inner, down", [(4, 2304, 256, Q4_K), (8, 2304, 512, Q6_K), (2, 512, 1184, Q8_0)])
+def test_results_are_the_same_in_calls_of_any_size(k, hidden, inner, down):
+    """Bit by bit, also where calls of other sizes split their rows differently."""
+    c, x, a = case([9, k], 8, E=9, k=k, hidden=hidden, inner=inner, gate_type=Q4_K, down_type=down)
+    layer = device_layer(c)
+    y, ids, p = call(c, dev(x), dev(a), layer)
+    check(c, x, a, (y, ids, p))
+    for T in range(1, 8):
+        for t0 in (0, 8 - T):
+            part = call(c, dev(x[t0:t0 + T]), dev(a[t0:t0 + T]), layer)
+            for one, all_ in zip(part, (y, ids, p)):
+                assert torch.equal(one, all_[t0:t0 + T]), (T, t0)
+
+
 def test_tokens_that_choose_the_same_experts():
     c, x, a = case([77], 6, E=20, k=6, hidden=256, inner=256, gate_type=Q5_K, down_type=Q4_0)
     x[1:] = x[0]
