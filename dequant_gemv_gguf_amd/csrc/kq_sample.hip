@@ -37,7 +37,7 @@ constexpr int LIST = 5120;                        // (all of row_kernel's LDS be
 constexpr int NEAR = 256;                         // tokens of a chunk's list
 constexpr int SPARSE = 1024;                      // tokens of a chunk that can matter, where those are put together first
 constexpr int FEW = 256;                          // tokens that are compared with each other
-constexpr int SLICE = 32768;                      // rows of a launch
+constexpr int SLICE = 16384;                      // chunks of a launch, or one row: 390 MB of workspace
 static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
 
 struct Sample {
@@ -46,11 +46,13 @@ struct Sample {
     int32_t *tokens;
     float *probs;
     u64 *tops;              // [row][chunk] first token
-    u32 *near_n;            // [row][chunk] tokens of its list, and above them the bins it goes down
+    u32 *near_n;            // [row][chunk] tokens of its list, from bit 16 the bins it goes down, bit 31 whether it is ordered
     u64 *near;              // [row][chunk][NEAR]
     u64 *hist;              // [row][chunk][BINS]
+    uint16_t *upto;         // [row][chunk][BINS] tokens of an ordered chunk down to and with a bin
+    uint16_t *order;        // [row][chunk][CHUNK] and their places, bin after bin
     int64_t ld;
-    int V, chunks, row0;
+    int V, chunks, row0;    // (the launch's first row; the workspace's rows are counted from it)
 };
 
 typedef float f4u __attribute__((ext_vector_type(4), aligned(4)));
@@ -204,7 +206,9 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     __shared__ float tops[WAVES], floors[WAVES];
     __shared__ u32 counts[WAVES];
     __shared__ double steps[OCTAVE];
-    __shared__ int n_some, n_near, first_most;
+    __shared__ __align__(16) uint16_t order[CHUNK];
+    __shared__ u32 starts[BINS];                  // where a bin's even lanes' tokens begin in `order`, and from bit 16 its odd lanes'
+    __shared__ int n_some, n_near, n_all, first_most;
     const int row = a.row0 + blockIdx.y, chunk = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
     const float *l = a.logits + row * a.ld;
     const Settings set = settings_of(a, row);
@@ -222,7 +226,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     }
     for (int i = tid; i < 2 * BINS; i += CHUNK_THREADS) (&hist[0][0])[i] = 0;
     if (tid == 0) {
-        n_some = n_near = 0;
+        n_some = n_near = n_all = 0;
         first_most = INT32_MAX;
     }
     if (tid < OCTAVE) steps[tid] = step;
@@ -249,7 +253,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
         most = fmaxf(most, tops[w]);
         floor_ = fminf(floor_, floors[w]);
     }
-    const int64_t at = (int64_t)row * a.chunks + chunk;
+    const int64_t at = (int64_t)blockIdx.y * a.chunks + chunk;
     if (!(most > none)) {
         if (tid == 0) a.tops[at] = 0;
         return;
@@ -280,20 +284,17 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
         const double d = from - s.bin(x);
         return x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
     };
+    // returns the bin, and below bit 16 the tokens that its half had before
     auto count = [&](float x) {
         const int b = bin_of(x);
         // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
         const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x, (phase - b) & (OCTAVE - 1)) : 0;
-        atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w);
-    };
-    auto from_floor = [&](float floor) {
-        u32 mask = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) mask |= (u32)(v[i] >= floor) << i;
-        return mask;
+        return (u32)b << 16 | (u32)(atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w) >> COUNT_SHIFT);
     };
     if (sparse) {
-        u32 mask = from_floor(floor_);
+        u32 mask = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mask |= (u32)(v[i] >= floor_) << i;
         int to = room(&n_some, __popc(mask));
         for (; mask; mask &= mask - 1, ++to)
             if (to < SPARSE) some[to] = (uint16_t)place(__builtin_ctz(mask));
@@ -312,20 +313,31 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
 #pragma unroll
         for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i)
             if (x[i] > none) count(x[i]);
-    } else {
+    }
+    const bool ordered = !sparse && (by_k || top_p < 1.f || min_p > 0.f);
+    u32 where[PER];
+    if (!sparse) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (v[i] >= floor_) count(v[i]);
+        for (int i = 0; i < PER; ++i) {
+            where[i] = ~0u;
+            if (v[i] >= floor_) where[i] = count(v[i]);
+        }
     }
     __syncthreads();
-    // the list: whole bins from the top, as many as fit
-    const u64 h = hist[tid][0] + hist[tid][1];
+    const u64 even = hist[tid][0], h = even + hist[tid][1];
     a.hist[at * BINS + tid] = h;
     u32 upto = wave_scan((u32)(h >> COUNT_SHIFT));
     if (lane == 63) counts[tid >> 6] = upto;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < WAVES - 1; ++w) upto += w < tid >> 6 ? counts[w] : 0;
+    if (ordered) {
+        const u32 start = upto - (u32)(h >> COUNT_SHIFT);
+        starts[tid] = start | (start + (u32)(even >> COUNT_SHIFT)) << 16;
+        a.upto[at * BINS + tid] = (uint16_t)upto;
+        if (tid == BINS - 1) n_all = (int)upto;
+    }
+    // the list: whole bins from the top, as many as fit
     const int depth = __syncthreads_count(upto <= NEAR);
     if (sparse) {
 #pragma unroll
@@ -334,29 +346,32 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
             const int to = room(&n_near, in);
             if (in) near[to] = token_of(key_of(x[i]), at_[i]);
         }
-    } else {
-        // what can lie in these bins, and a little more, and then what does
-        float lo = floor_;
-        if (depth < BINS && s.eighths > 0.0 && most < __builtin_inff()) {
-            const double y = (from - depth + 1) / s.eighths;
-            lo = fmaxf(lo, (float)(y - fabs(y) * 0x1p-22) - 1e-37f);
-        }
-        u32 mask = from_floor(lo), in = 0;
-        for (u32 left = mask; left; left &= left - 1)
-            if (bin_of(l[base + place(__builtin_ctz(left))]) < depth) in |= left & -left;
-        int to = room(&n_near, __popc(in));
-        for (; in; in &= in - 1, ++to) {
-            const int i = base + place(__builtin_ctz(in));
-            near[to] = token_of(key_of(l[i]), i);
-        }
+    } else if (ordered) {
+        // (a place for each token from its bin and the count that it found there)
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            if (where[i] != ~0u) {
+                const u32 from = starts[where[i] >> 16];
+                order[(lane & 1 ? from >> 16 : from & 0xFFFF) + (where[i] & 0xFFFF)] = (uint16_t)place(i);
+            }
+        if (tid == depth - 1) n_near = (int)upto;
     }
     __syncthreads();
-    for (int i = tid; i < n_near; i += CHUNK_THREADS) a.near[at * NEAR + i] = near[i];
+    if (ordered) {
+        for (int i = tid; 8 * i < n_all; i += CHUNK_THREADS) ((uint4 *)(a.order + at * CHUNK))[i] = ((const uint4 *)order)[i];
+        if (tid < n_near) {
+            const int i = base + order[tid];
+            a.near[at * NEAR + tid] = token_of(key_of(l[i]), i);
+        }
+    } else if (tid < n_near) {
+        a.near[at * NEAR + tid] = near[tid];
+    }
     if (tid == 0) {
         a.tops[at] = token_of(key_of(most), first_most);
-        a.near_n[at] = (u32)n_near | (u32)depth << 16;
+        a.near_n[at] = (u32)n_near | (u32)depth << 16 | (u32)ordered << 31;
     }
 }
+static_assert(NEAR <= CHUNK_THREADS, "a thread a token of the list");
 static_assert(CHUNK_THREADS == BINS, "a thread a bin");
 
 // What row_kernel shares between its threads.
@@ -494,7 +509,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const double step = STEPS[tid & (OCTAVE - 1)];
     const float t = set.t, top_p = set.top_p, min_p = set.min_p;
     const int top_k = set.top_k;
-    const int64_t chunk0 = (int64_t)row * a.chunks;
+    const int64_t chunk0 = (int64_t)blockIdx.x * a.chunks;
     // What a wave needs first is asked for at once: the histograms of two chunks, the
     // list of one.  (Not all of it was written: a chunk without a token has neither, a
     // list is as long as near_n says.)
@@ -641,14 +656,16 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             one = true;
         }
     }
-    // the chunks' lists go down to bin `low`
-    bool near = low < BINS - 1;
+    // the chunks' lists go down to bin `low`; or they are ordered
+    bool near = low < BINS - 1, ordered = true;
 #pragma unroll
     for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-        const int depth = (int)(near_n[i] >> 16);
+        const int depth = (int)(near_n[i] >> 16 & 0x7FFF);
+        ordered = ordered && (!(first_of[i] >> 32) || near_n[i] >> 31);
         near = near && (!(first_of[i] >> 32) || depth == BINS || m.off[lane + 64 * i] + depth > low);
     }
     near = __ballot(!near) == 0;
+    ordered = __ballot(!ordered) == 0;
     // the tokens of bins high .. low in the chunks' lists, each with a place of its own
     auto from_lists = [&](int high, int low, auto &&put) {
         for (int c = wave; c < a.chunks; c += ROW_WAVES) {
@@ -734,6 +751,41 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         from_lists(high, low, [&](int to, u64 token) {
             if (to < LIST) m.list[to] = token;
         });
+        __syncthreads();
+    } else if (listed && ordered) {
+        // bins high .. low of each chunk, behind each other in the list
+        u32 from[MAX_CHUNKS / 64], n[MAX_CHUNKS / 64], to[MAX_CHUNKS / 64], all = 0;
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+            const int c = lane + 64 * i, off = m.off[c];
+            const uint16_t *upto = a.upto + (chunk0 + c) * BINS;
+            const bool in = off >= 0 && off <= low;
+            from[i] = in && high > off ? upto[high - off - 1] : 0;
+            n[i] = (in ? upto[low - off] : 0) - from[i];
+        }
+#pragma unroll
+        for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+            const u32 upto = wave_scan(n[i]);
+            to[i] = all + upto - n[i];
+            all += last_lane(upto);
+        }
+        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+            auto of = [&](const u32 (&x)[MAX_CHUNKS / 64]) { return __builtin_amdgcn_readlane((int)(c < 64 ? x[0] : x[1]), c & 63); };
+            const int count = of(n), at = of(to);
+            const uint16_t *places = a.order + (chunk0 + c) * CHUNK + of(from);
+            for (int j0 = lane; j0 < count; j0 += 256) {
+                int i[4];
+                float x[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) i[j] = c * CHUNK + places[min(j0 + 64 * j, count - 1)];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = r.l[i[j]];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j0 + 64 * j < count) m.list[at + j0 + 64 * j] = token_of(key_of(x[j]), i[j]);
+            }
+        }
+        if (tid == 0) m.n = (int)all;
         __syncthreads();
     } else if (listed) {
         constexpr int BATCH = 8;                  // pieces of 4 a thread; the next ones are on their way
@@ -829,7 +881,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         double w = 0.0;
         const int off = m.off[c];
         if (off >= 0 && off < whole) {
-            const u64 *h = a.hist + ((int64_t)row * a.chunks + c) * BINS;
+            const u64 *h = a.hist + (chunk0 + c) * BINS;
 #pragma unroll
             for (int i = 0; i < BINS / 64; ++i) {
                 const int d = lane + 64 * i;
@@ -923,14 +975,19 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     }
 }
 
-struct SampleSpace { size_t near_n, near, hist, end; };
+// The parts of a workspace, for `rows` rows at a time.
+struct SampleSpace { size_t near_n, near, hist, upto, order, end; int chunks, rows; };
 static SampleSpace sample_space(int M, int64_t V) {
-    const size_t n = (size_t)M * (size_t)((V + CHUNK - 1) / CHUNK);
     SampleSpace s;
+    s.chunks = (int)((V + CHUNK - 1) / CHUNK);
+    s.rows = std::max(1, std::min(M, SLICE / s.chunks));
+    const size_t n = (size_t)(M ? s.rows : 0) * s.chunks;
     s.near_n = n * sizeof(u64);
     s.near = (s.near_n + n * sizeof(u32) + 15) & ~(size_t)15;
     s.hist = s.near + n * NEAR * sizeof(u64);
-    s.end = s.hist + n * BINS * sizeof(u64);
+    s.upto = s.hist + n * BINS * sizeof(u64);
+    s.order = s.upto + n * BINS * sizeof(uint16_t);
+    s.end = s.order + n * CHUNK * sizeof(uint16_t);
     return s;
 }
 
@@ -962,10 +1019,10 @@ int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float
     if (device_check()) return KQ_ERR_DEVICE;
     uint8_t *ws = (uint8_t *)workspace;
     Sample a = {logits, temperature, top_p, min_p, u, top_k, tokens, probs, (u64 *)ws, (u32 *)(ws + s.near_n), (u64 *)(ws + s.near),
-                (u64 *)(ws + s.hist), ld, (int)V, (int)((V + CHUNK - 1) / CHUNK), 0};
+                (u64 *)(ws + s.hist), (uint16_t *)(ws + s.upto), (uint16_t *)(ws + s.order), ld, (int)V, s.chunks, 0};
     hipStream_t st = (hipStream_t)stream;
-    for (; a.row0 < M; a.row0 += SLICE) {
-        const int rows = std::min(M - a.row0, SLICE);
+    for (; a.row0 < M; a.row0 += s.rows) {
+        const int rows = std::min(M - a.row0, s.rows);
         hipLaunchKernelGGL(chunk_kernel, dim3((unsigned)a.chunks, (unsigned)rows), dim3(CHUNK_THREADS), 0, st, a);
         hipLaunchKernelGGL(row_kernel, dim3((unsigned)rows), dim3(ROW_THREADS), 0, st, a);
     }
