@@ -69,33 +69,36 @@ __device__ __forceinline__ float logit_of(u32 key) {
 __device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 | (u32)~i; }
 
 // Where a logit's weight lies: the bin (counted upwards), its octave, and the
-// mantissa, 2^35 .. 2^36.  An infinite logit lies above all others.
+// mantissa, 2^35 .. 2^36.  (A bin is the nearest whole number to what is 1/2 less than
+// the eighths of an octave: what is left, at most 1/2 either way, the series takes.)
 struct Scale {
     double eighths;         // of an octave, per logit: 8 log2(e) / t
     const double *steps;    // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
-    // (an infinite temperature's eighths are 0, so that an infinite logit lies at NaN: not
-    // among any bins, which is right for all but the first token, and that has bin 0)
-    __device__ __forceinline__ double at(float l) const { return (double)l * eighths; }
-    __device__ __forceinline__ double bin(float l) const { return floor(at(l)); }
-    // `of_octave`: the bin's place in its octave
+    // (an infinite logit's mantissa is that of the largest number; its bin is given by
+    // what it is compared with)
+    __device__ __forceinline__ double at(float l) const {
+        return fma((double)__builtin_amdgcn_fmed3f(l, -3.402823466e38f, 3.402823466e38f), eighths, -0.5);
+    }
+    __device__ __forceinline__ double bin(float l) const { return rint(at(l)); }
+    // that of a first token: an infinite one lies above all others
+    __device__ __forceinline__ double top_bin(float l) const { return l < __builtin_inff() ? bin(l) : __builtin_inf(); }
+    // 2^52 more, in whose low bits it is rounded to an integer.  `of_octave`: the bin's
+    // place in its octave
     __device__ __forceinline__ double mantissa_d(float l, int of_octave) const {
-        const double y = at(l);
-        // e^x for |x| <= log 2 / 16: its series to x^6 / 6! (2^-44 is left)
-        // (an infinite logit: the least mantissa.  y - floor(y) would become fma(l, eighths,
-        // -floor(y)), which where y is large is the rounding of y and no fraction)
-        const double x = fmax(__builtin_amdgcn_fract(y) - 0.5, -0.5) * 0.08664339756999316;
-        double p = 1.0 / 720.0;
-        p = fma(p, x, 1.0 / 120.0);
-        p = fma(p, x, 1.0 / 24.0);
-        p = fma(p, x, 1.0 / 6.0);
-        p = fma(p, x, 0.5);
-        p = fma(p, x, 1.0);
-        p = fma(p, x, 1.0);
-        // to an integer: 2^52 in front leaves it in the low bits, rounded
+        const double y = at(l), z = y - rint(y);
+        // 2^(z / 8) by the polynomial through six Chebyshev nodes: off by 2^-41
+        double p = 0x1.5d8dfde822453p-25;
+        p = fma(p, z, 0x1.3b324944cbf5dp-19);
+        p = fma(p, z, 0x1.c6b08d5e4bb3bp-14);
+        p = fma(p, z, 0x1.ebfbdfcabe822p-9);
+        p = fma(p, z, 0x1.62e42fefa3aefp-4);
+        p = fma(p, z, 0x1.000000000050cp+0);
         return fma(p, steps[of_octave], 0x1p52);
     }
-    __device__ __forceinline__ u64 mantissa(float l, int of_octave) const {
-        return __builtin_bit_cast(u64, mantissa_d(l, of_octave)) - 0x4330000000000000ull;
+    // `plus` 2^32 more
+    __device__ __forceinline__ u64 mantissa(float l, int of_octave, u32 plus = 0) const {
+        const u64 b = __builtin_bit_cast(u64, mantissa_d(l, of_octave));
+        return (u64)((u32)(b >> 32) - 0x43300000u + plus) << 32 | (u32)b;
     }
 };
 __device__ __forceinline__ Scale scale_of(float t, const double *steps) {
@@ -270,7 +273,7 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
         return;
     }
     const Scale s = scale_of(t, steps);
-    const double from = s.bin(most);
+    const double from = s.top_bin(most);
     const int phase = phase_of(from);
     bool sparse = by_k && top_k <= CHUNK_THREADS;
     if (!by_k && !(top_p < 1.f) && min_p > 0.f) {
@@ -281,15 +284,16 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     }
     floor_ = sparse ? fmaxf(floor_, LEAST) : LEAST;
     auto bin_of = [&](float x) {
-        const double d = from - s.bin(x);
-        return x == most ? 0 : d < BINS - 1 ? (int)d : BINS - 1;
+        const double d = fmin(from - s.bin(x), BINS - 1.0);
+        return x == most ? 0 : (int)d;
     };
     // returns the bin, and below bit 16 the tokens that its half had before
     auto count = [&](float x) {
         const int b = bin_of(x);
-        // (the last bin, 64 octaves below: its weights count as nothing; with top_k none are asked for)
-        const u64 w = !by_k && b < BINS - 1 ? s.mantissa(x, (phase - b) & (OCTAVE - 1)) : 0;
-        return (u32)b << 16 | (u32)(atomicAdd((unsigned long long *)&hist[b][lane & 1], (1ull << COUNT_SHIFT) + w) >> COUNT_SHIFT);
+        // (with top_k no weights are asked for, and never those of the last bin, 64 octaves below)
+        constexpr u32 ONE = 1u << (COUNT_SHIFT - 32);
+        const u64 w = by_k ? (u64)ONE << 32 : s.mantissa(x, (phase - b) & (OCTAVE - 1), ONE);
+        return (u32)b << 16 | (u32)(atomicAdd((unsigned long long *)&hist[b][lane & 1], w) >> COUNT_SHIFT);
     };
     if (sparse) {
         u32 mask = 0;
@@ -409,8 +413,7 @@ struct Row {
     __device__ __forceinline__ int octaves(int b) const { return (b + OCTAVE - 1 - phase) >> 3; }
     __device__ __forceinline__ int bin(float x) const {
         if (x == logit_of((u32)(best >> 32))) return 0;
-        const double d = from - s.bin(x);
-        return d < BINS ? (int)d : BINS;
+        return (int)fmin(from - s.bin(x), (double)BINS);
     }
     // in units of the top octave's mantissas
     __device__ __forceinline__ double weight(float x) const {
@@ -559,7 +562,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     r.best = best;
     r.V = a.V;
     const float most = logit_of((u32)(best >> 32));
-    r.from = r.s.bin(most);
+    r.from = r.s.top_bin(most);
     r.phase = phase_of(r.from);
 
     // the row's histogram
@@ -578,8 +581,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             const int c = lane + 64 * i;
             const u32 key = (u32)(first_of[i] >> 32);
             const float x = logit_of(key);
-            const double d = x == most ? 0.0 : r.from - r.s.bin(x);
-            m.off[c] = !key ? -1 : d < BINS ? (int)d : BINS;
+            const double d = x == most ? 0.0 : r.from - r.s.top_bin(x);
+            m.off[c] = !key ? -1 : (int)fmin(d, (double)BINS);
             m.chunk_list[c] = 0;
         }
         if (lane == 0) m.most = m.sum = 0;
