@@ -1,13 +1,15 @@
 // kq_norm.hip -- the residual's addition and the root-mean-square norm of
 // include/kqstep.h.
 //
-// Bound: HBM (x and add read, sum and y written, once); for few rows the chain
-// of one row: a load, the sum of its squares, a store.  A row (a token's, or one
-// of its heads) stays in registers from the load to the stores.  Rows of up to
-// 1024 elements take 16, 32 or 64 lanes, so that a wave holds up to four heads;
-// longer ones a work-group.  The sum of squares and y are computed in 64 bits:
-// at one square and two products an element that costs nothing beside the
-// loads, and y is the correctly rounded result for all but ties of 2^-29.
+// Bound: HBM (x and add read, sum and y written, once): 8192 rows of 8192 with both
+// take 193 us, 5.6 TB/s; for few rows the chain of one row, a load, the sum of its
+// squares, a store: one row of 2048 takes 2.6 us, 250 x 32 heads of 128 3.3.  A row (a
+// token's, or one of its heads) stays in registers from the load to the stores.  Rows
+// of up to 512 elements take 16, 32 or 64 lanes, so that a wave holds up to four heads;
+// longer ones a work-group.  The sum of squares and y are computed in 64 bits: at one
+// square and two products an element that costs nothing beside the loads, and y is the
+// correctly rounded result for all but ties of 2^-29.  Q8_0 rows: 4099 of 4096 with
+// fp32 rows, sum and add take 58 us (5.0 TB/s), 49 without them (5.5 TB/s).
 #include "kq_step.h"
 
 #include <cmath>
@@ -217,14 +219,23 @@ extern "C" int kqstep_norm(int T, int heads, int n, const float *x, int64_t ldx,
     const Norm a = {x, add, weight, sum, y, (uint8_t *)y8, ldx, ldadd, ldsum, ldy, row / 32 * 34, eps, 1.0 / n, heads, n,
                     (u32)(T * heads), 0};
     hipStream_t st = (hipStream_t)stream;
+    // The threads of a row: fewer wait less for each other where there are many rows,
+    // more have a shorter chain each.  Measured, us, one row / many rows:
+    //   64 lanes with 2 of 4 idle for heads of 64, 128 (4096 x 64 and 32 heads): 75 and 43, as here 27 and 27
+    //   512: a work-group of 128 threads 2.1 / 67 (65536 rows), 64 lanes 2.2 / 49
+    //   1024: 64 lanes 2.6 / 48.9 (32768 rows), 128 threads 2.3 / 47.7, 256 2.0 / 48.0 (8192 rows: 11.8, 12.3, 12.9)
+    //   2048: 64 lanes 3.4 / 51.6 (16384 rows), 256 threads 2.3 / 48.3, 512 2.1 / 47.9 (4096 rows: 12.5, 13.1)
+    //   4096: 256 threads 3.0 / 48.7 (8192 rows), 512 2.6 / 47.9, 1024 2.7 / 57.0
+    //   8192: 256 threads 4.0 / 51.9 (4096 rows), 512 3.2 / 50.9, 1024 3.2 / 50.0 (rows of 5120: 35.5, 33.9, 37.3)
+    //   32768: in registers 5.6 / 57 (1024 rows), read twice 7.0 / 72
     if (n <= 64) launch_lanes<16, 1>(a, st);
     else if (n <= 128) launch_lanes<32, 1>(a, st);
     else if (n <= 256) launch_lanes<64, 1>(a, st);
     else if (n <= 512) launch_lanes<64, 2>(a, st);
-    else if (n <= 1024) launch_lanes<64, 4>(a, st);
+    else if (n <= 1024) launch_row<128, 2>(a, st);
     else if (n <= 2048) launch_row<256, 2>(a, st);
-    else if (n <= 4096) launch_row<256, 4>(a, st);
-    else if (n <= 8192) launch_row<256, 8>(a, st);
+    else if (n <= 4096) launch_row<512, 2>(a, st);
+    else if (n <= 8192) launch_row<512, 4>(a, st);
     else if (n <= 16384) launch_row<1024, 4>(a, st);
     else if (n <= 32768) launch_row<1024, 8>(a, st);
     else launch_row<1024, 0>(a, st);
