@@ -1,8 +1,11 @@
 // kq_moe_inst.hip -- the experts' products of kqstep_moe for one block format,
 // KQ_MOE_TYPE.
 //
-// Bound: HBM (a token's experts' weights, read once) and, from four tokens on, the
-// vector units' work on them; for one token the chain of logits, choice, weights.
+// Bound: HBM (a token's experts' weights, read once) and, from three tokens on, the
+// vector units' work on them (8 of 128 experts of 2048 x 768, Q4_K and Q6_K, one token:
+// 16 us; eight tokens 47, 3.4 TB/s of the distinct experts' bytes; three tokens, 6 of 160
+// of 5120 x 1536, Q5_K and Q4_K: 85, 3.1 TB/s, the vector units busy half the time with
+// three waves a SIMD); for one token the chain of logits, choice, weights.
 // A work-group takes one token and a tile of rows, a wave one expert's rows of the
 // tile: it streams them through registers.  The activations are put into LDS once for
 // the work-group (asked for by every wave from the cache they took 3300 cycles before

@@ -3,22 +3,28 @@
 // Everything that the filters leave is a leading part of the tokens in the order
 // of (logit descending, index ascending), so a filter is a place in that order.
 //
-// Bound: for few rows the chain of two launches, for many the arithmetic of the
-// first (a 64-bit power of two a logit), its LDS atomics and HBM.  Two launches:
+// Bound: for few rows the chain of two launches (one row of 32000 tokens, top_k 40,
+// top_p and min_p: 13.6 us); for many the arithmetic of the first (256 rows of 151937,
+// settings of each row: 76 us, of which it takes 52; 3.0 TB/s there, 6.8 where all rows
+// are greedy).  Two launches:
 //  * chunk_kernel, a work-group a chunk of 8192 tokens of a row: the chunk's first
 //    token of the order, a histogram over bins of an eighth of an octave of weight
 //    (counts and weights of 512 bins below the chunk's largest), and a list of its
 //    first tokens.  The bins lie at fixed places of l / t, so chunks need not know of
 //    each other.  A bin's count and the sum of its weights, integers, share one
-//    64-bit LDS atomic: the sums do not depend on the order.
+//    64-bit LDS atomic: the sums do not depend on the order.  The count that a token
+//    finds there is its place in its bin, so that the chunk can also leave its tokens
+//    ordered by bins.
 //  * row_kernel, a work-group a row: the chunks' histograms added up give the bin in
 //    which each filter ends.  Where few tokens are left down to that bin (hundreds,
 //    and all in the chunks' lists), every one of them is compared with every other
-//    and that is all.  Elsewhere one scan of the row gathers the bin's tokens in LDS,
-//    where the place is found digit by digit of the logits' keys, the chunks' kept
-//    weights say which chunk holds the token, and its logits are gone over once more.
-//    Where the gathered tokens do not fit in LDS (thousands of equal logits, a very
-//    high temperature), the digits are found over the row itself.
+//    and that is all (one row of 32000 13.6 us; by digits, as below, 20.4).  Elsewhere
+//    the bin's tokens are gathered in LDS, from the lists or the ordered chunks (256 rows
+//    76 us; by a scan of the row, which is left for a list that is too short in a chunk
+//    that is not ordered, 84), where the place is found digit by digit of the logits'
+//    keys, the chunks' kept weights say which chunk holds the token, and its logits are
+//    gone over once more.  Where the gathered tokens do not fit in LDS (thousands of
+//    equal logits, a very high temperature), the digits are found over the row itself.
 // Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
 // the row's largest.
 #include "kq_step.h"
@@ -197,8 +203,11 @@ __device__ __forceinline__ int room(int *count, int n) {
 // Whether top_k limits the row (the same in both kernels).
 __device__ __forceinline__ bool limited(int top_k, int V) { return top_k > 0 && top_k < V; }
 
-// Bound: its arithmetic, some 30 instructions a token that can matter (the bin and the
-// mantissa in 64 bits) and 6 for the others.
+// Bound: its arithmetic, some 30 instructions a token whose weight is asked for, 14 of
+// them in 64 bits (256 rows of 151937 that all sum weights: 58 us, without the weights
+// 44, greedy 23).  top_k up to the threads of a work-group, and min_p alone, first take
+// out the tokens that cannot matter and count the others, put together in LDS (256 rows
+// 76 us, 84 where top_k counts them all; top_k 50 alone 39 and 60).
 __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     constexpr int PER = CHUNK / CHUNK_THREADS, WAVES = CHUNK_THREADS / 64;
     constexpr float LEAST = -3.402823466e38f;     // the least logit that counts
