@@ -402,7 +402,7 @@ struct RowSpace {
     double chunk_sum[MAX_CHUNKS];
     u64 waves[ROW_WAVES];
     double waves_d[ROW_WAVES];
-    u64 found[4];                   // (0 .. 2 a digit, 3 a token)
+    u64 found[3];                   // a digit, what lies above it, its tokens
     double picked[2];
     u64 most, sum;
     double steps[OCTAVE];
@@ -425,10 +425,11 @@ struct Row {
         return (int)fmin(from - s.bin(x), (double)BINS);
     }
     // in units of the top octave's mantissas
-    __device__ __forceinline__ double weight(float x) const {
+    // (0 past the bin `last`, at most BINS - 2)
+    __device__ __forceinline__ double weight(float x, int last) const {
         const int b = bin(x);
         const double w = ldexp(s.mantissa_d(x, (phase - b) & (OCTAVE - 1)) - 0x1p52, -octaves(b));
-        return b < BINS - 1 ? w : 0.0;
+        return b <= last ? w : 0.0;
     }
     __device__ __forceinline__ u64 mantissa(float x, int b) const { return s.mantissa(x, (phase - b) & (OCTAVE - 1)); }
     __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
@@ -442,10 +443,10 @@ struct Row {
 
 // The shortest leading part (descending) of the tokens from `from` on that `each` goes
 // over, of which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the
-// whole sum): the part is the tokens from the returned one on.  Digits of 8 bits of
-// what a token is above `from` (to find the bits in which they differ instead takes two
-// reductions and 1.5 us), from the first that one up to `top`, the most that
-// any is, can have.
+// whole sum): the part is the tokens from the returned place on (which need not be a
+// token).  Digits of 8 bits of what a token is above `from` (to find the bits in which
+// they differ instead takes two reductions and 1.5 us), from the first that one up to
+// `top`, the most that any is, can have.  The digits' sums are 0 before and after.
 template <bool WEIGHTS, class Each>
 __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, u64 want) {
     const int tid = threadIdx.x, lane = tid & 63;
@@ -454,12 +455,6 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, 
     while (above) {
         const int shift = max(above - 8, 0);
         const u32 digits = (1u << (above - shift)) - 1;
-        __syncthreads();
-        if (tid < 256) {
-            m.digit_weight[tid] = 0;
-            m.digit_count[tid] = 0;
-        }
-        __syncthreads();
         each([&](u64 token, auto &&weight) {
             const u64 v = token - from;
             if (token < from || (above < 64 && v >> above != prefix)) return;
@@ -470,37 +465,42 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, 
         __syncthreads();
         if (tid < 64) {
             // 4 digits a lane, descending
+            u32 n[4];
             u64 d[4], s = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int digit = 255 - (4 * lane + i);
-                d[i] = WEIGHTS ? m.digit_weight[digit] : m.digit_count[digit];
+                n[i] = m.digit_count[digit];
+                d[i] = WEIGHTS ? m.digit_weight[digit] : n[i];
+                m.digit_count[digit] = 0;
+                if (WEIGHTS) m.digit_weight[digit] = 0;
                 s += d[i];
             }
             const u64 upto = wave_scan(s);
             const u64 reach = __ballot(before + upto >= want);
             if (lane == (reach ? __builtin_ctzll(reach) : 63)) {
                 u64 b = before + upto - s;
-                int i = 0;
-                for (; i < 3 && b + d[i] < want; ++i) b += d[i];
-                m.found[0] = (u64)(255 - (4 * lane + i));
+                int at = 0;
+                u32 count = n[0];
+#pragma unroll
+                for (int i = 0; i < 3; ++i)
+                    if (at == i && b + d[i] < want) {
+                        b += d[i];
+                        at = i + 1;
+                        count = n[i + 1];
+                    }
+                m.found[0] = (u64)(255 - (4 * lane + at));
                 m.found[1] = b;
-                m.found[2] = m.digit_count[255 - (4 * lane + i)];
+                m.found[2] = count;
             }
         }
         __syncthreads();
         prefix = prefix << (above - shift) | m.found[0];
         before = m.found[1];
         above = shift;
-        if (m.found[2] == 1 && shift) {     // one token has these digits: that one
-            each([&](u64 token, auto &&) {
-                if (token >= from && (token - from) >> shift == prefix) m.found[3] = token;
-            });
-            __syncthreads();
-            return m.found[3];
-        }
+        if (m.found[2] == 1) break;         // one token has these digits: none lies between it and them
     }
-    return from + prefix;
+    return from + (prefix << above);
 }
 
 __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
@@ -578,6 +578,10 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     for (int b = tid; b < BINS; b += ROW_THREADS) {
         m.weight[b] = 0;
         m.count[b] = 0;
+    }
+    if (tid < 256) {
+        m.digit_weight[tid] = 0;
+        m.digit_count[tid] = 0;
     }
     if (tid == 0) {
         m.n = 0;
@@ -781,11 +785,13 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             to[i] = all + upto - n[i];
             all += last_lane(upto);
         }
-        for (int c = wave; c < a.chunks; c += ROW_WAVES) {
+        // (several waves a chunk where there are few)
+        const int ways = max(1, ROW_WAVES / a.chunks), way = a.chunks < ROW_WAVES ? wave / a.chunks : 0;
+        for (int c = wave - way * a.chunks; c < a.chunks && way < ways; c += ROW_WAVES) {
             auto of = [&](const u32 (&x)[MAX_CHUNKS / 64]) { return __builtin_amdgcn_readlane((int)(c < 64 ? x[0] : x[1]), c & 63); };
             const int count = of(n), at = of(to);
             const uint16_t *places = a.order + (chunk0 + c) * CHUNK + of(from);
-            for (int j0 = lane; j0 < count; j0 += 256) {
+            for (int j0 = 256 * way + lane; j0 < count; j0 += 256 * ways) {
                 int i[4];
                 float x[4];
 #pragma unroll
@@ -837,7 +843,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
     // 2^20 tokens have to fit the sum).
     const int finer = listed ? 14 : 7, base = one && listed ? r.octaves(low) : 0;
-    u64 least = 0;                                // the last token that top_k and top_p keep
+    u64 least = 0;                                // top_k and top_p keep the tokens from here on
     // each(f): f(token, weight()) for every gathered token
     auto places = [&](auto &&each) {
         // (where the tokens of these bins lie; the whole row's begin at the first one)
@@ -866,9 +872,12 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     if (listed) {
         // a thread's tokens and their weights, in registers (0: none)
         u64 token[LIST / ROW_THREADS], w[LIST / ROW_THREADS];
+        const int n = m.n;
 #pragma unroll
         for (int i = 0; i < LIST / ROW_THREADS; ++i) {
-            token[i] = tid + i * ROW_THREADS < m.n ? m.list[tid + i * ROW_THREADS] : 0;
+            token[i] = w[i] = 0;
+            if (i * ROW_THREADS >= n) continue;
+            token[i] = tid + i * ROW_THREADS < n ? m.list[tid + i * ROW_THREADS] : 0;
             const int b = token[i] >> 32 ? r.bin(logit_of((u32)(token[i] >> 32))) : BINS;
             if (b < high || b > low) token[i] = 0;
             w[i] = token[i] ? r.integer(token[i], finer, base) : 0;
@@ -876,7 +885,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         places([&](auto &&f) {
 #pragma unroll
             for (int i = 0; i < LIST / ROW_THREADS; ++i)
-                if (token[i]) f(token[i], [&] { return w[i]; });
+                if (i * ROW_THREADS < n && token[i]) f(token[i], [&] { return w[i]; });
         });
     } else if (scan) {
         places([&](auto &&f) {
@@ -942,19 +951,29 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     f4 logits[EACH / 4];
 #pragma unroll
     for (int j = 0; j < EACH / 4; ++j) logits[j] = four(r.l, first + 4 * j, a.V);
-    // (`least` as a logit and an index)
-    const float last_x = least ? logit_of((u32)(least >> 32)) : -__builtin_inff();
-    const int last_i = least ? (int)~(u32)least : -1, best_i = (int)~(u32)best;
-    double w[EACH], mine = 0.0;
+    // (`least` as a logit and an index; no token's key lies below that of the lowest
+    // number, or at that of -0)
+    u32 last_key = (u32)(least >> 32), last_low = (u32)least;
+    if (last_key == 0x7FFFFFFF) {
+        last_key = 0x80000000;
+        last_low = 0;
+    }
+    const float last_x = last_key >= 0x00800000 ? logit_of(last_key) : -__builtin_inff();
+    const int last_i = last_key >= 0x00800000 ? (int)min(~last_low, 0x7FFFFFFFu) : -1, best_i = (int)~(u32)best;
+    // (nothing past bin `low` is kept, also where `least` lies there)
+    const int last_bin = min(low, BINS - 2);
+    double w[EACH] = {}, mine = 0.0;
+    if (m.n * CHUNK + EACH * 64 * wave < a.V) {
 #pragma unroll
-    for (int j = 0; j < EACH; ++j) {
-        // (a weight for every token, also those that are not kept: without branches the
-        // eight are computed side by side)
-        const float x = logits[j / 4][j % 4];
-        w[j] = r.weight(x);
-        const int kept = ((x > last_x) | ((x == last_x) & (first + j <= last_i))) & ((first + j == best_i) | (w[j] >= r.least));
-        w[j] = kept ? w[j] : 0.0;
-        mine += w[j];
+        for (int j = 0; j < EACH; ++j) {
+            // (a weight for every token, also those that are not kept: without branches the
+            // eight are computed side by side)
+            const float x = logits[j / 4][j % 4];
+            w[j] = r.weight(x, last_bin);
+            const int kept = ((x > last_x) | ((x == last_x) & (first + j <= last_i))) & ((first + j == best_i) | (w[j] >= r.least));
+            w[j] = kept ? w[j] : 0.0;
+            mine += w[j];
+        }
     }
     double upto = wave_scan(mine);
     if (lane == 63) m.waves_d[wave] = upto;
