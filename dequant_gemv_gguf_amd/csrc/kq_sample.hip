@@ -52,10 +52,10 @@ struct Sample {
     int32_t *tokens;
     float *probs;
     u64 *tops;              // [row][chunk] first token
-    u32 *near_n;            // [row][chunk] tokens of its list, from bit 16 the bins it goes down, bit 31 whether it is ordered
+    u32 *near_n;            // [row][chunk] tokens of its list, from bit 16 the bins it goes down
     u64 *near;              // [row][chunk][NEAR]
     u64 *hist;              // [row][chunk][BINS]
-    uint16_t *upto;         // [row][chunk][BINS] tokens of an ordered chunk down to and with a bin
+    uint16_t *upto;         // [row][chunk][BINS] tokens down to and with a bin
     uint16_t *order;        // [row][chunk][CHUNK] and their places, bin after bin
     int64_t ld;
     int V, chunks, row0;    // (the launch's first row; the workspace's rows are counted from it)
@@ -213,7 +213,6 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     constexpr float LEAST = -3.402823466e38f;     // the least logit that counts
     // two histograms, of the even and the odd lanes: half the lanes of a wave meet in a bin
     __shared__ __align__(16) u64 hist[BINS][2];
-    __shared__ u64 near[NEAR];
     __shared__ uint16_t some[SPARSE];             // places in the chunk
     __shared__ float tops[WAVES], floors[WAVES];
     __shared__ u32 counts[WAVES];
@@ -315,27 +314,29 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
         sparse = n_some <= SPARSE;
     }
     float x[SPARSE / CHUNK_THREADS];              // (read again: a lane's logits cannot be picked by number)
-    int at_[SPARSE / CHUNK_THREADS];
+    int some_at[SPARSE / CHUNK_THREADS];
+    u32 where[PER];                               // what `count` returned; ~0: not counted
     if (sparse) {
 #pragma unroll
         for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i) {
             const bool in = tid + i * CHUNK_THREADS < n_some;
-            at_[i] = base + (in ? some[tid + i * CHUNK_THREADS] : 0);
-            x[i] = in ? l[at_[i]] : none;
+            some_at[i] = in ? some[tid + i * CHUNK_THREADS] : 0;
+            x[i] = in ? l[base + some_at[i]] : none;
         }
 #pragma unroll
-        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i)
-            if (x[i] > none) count(x[i]);
-    }
-    const bool ordered = !sparse && (by_k || top_p < 1.f || min_p > 0.f);
-    u32 where[PER];
-    if (!sparse) {
+        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i) {
+            where[i] = ~0u;
+            if (x[i] > none) where[i] = count(x[i]);
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
             where[i] = ~0u;
             if (v[i] >= floor_) where[i] = count(v[i]);
         }
     }
+    // (a row without filters needs neither its chunks' order nor their lists)
+    const bool ordered = by_k || top_p < 1.f || min_p > 0.f;
     __syncthreads();
     const u64 even = hist[tid][0], h = even + hist[tid][1];
     a.hist[at * BINS + tid] = h;
@@ -352,36 +353,39 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     }
     // the list: whole bins from the top, as many as fit
     const int depth = __syncthreads_count(upto <= NEAR);
-    if (sparse) {
+    if (ordered) {
+        // a place for each token from its bin and the count that it found there
+        auto put = [&](u32 where, int i) {
+            const u32 from = starts[where >> 16];
+            const int to = (int)(lane & 1 ? from >> 16 : from & 0xFFFF) + (int)(where & 0xFFFF);
+            order[to] = (uint16_t)i;
+            return to;
+        };
+        if (sparse) {
 #pragma unroll
-        for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i) {
-            const bool in = x[i] > none && bin_of(x[i]) < depth;
-            const int to = room(&n_near, in);
-            if (in) near[to] = token_of(key_of(x[i]), at_[i]);
+            for (int i = 0; i < SPARSE / CHUNK_THREADS; ++i)
+                if (where[i] != ~0u) {
+                    const int to = put(where[i], some_at[i]);
+                    if ((int)(where[i] >> 16) < depth) a.near[at * NEAR + to] = token_of(key_of(x[i]), base + some_at[i]);
+                }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (where[i] != ~0u) put(where[i], place(i));
         }
-    } else if (ordered) {
-        // (a place for each token from its bin and the count that it found there)
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (where[i] != ~0u) {
-                const u32 from = starts[where[i] >> 16];
-                order[(lane & 1 ? from >> 16 : from & 0xFFFF) + (where[i] & 0xFFFF)] = (uint16_t)place(i);
-            }
         if (tid == depth - 1) n_near = (int)upto;
     }
     __syncthreads();
     if (ordered) {
         for (int i = tid; 8 * i < n_all; i += CHUNK_THREADS) ((uint4 *)(a.order + at * CHUNK))[i] = ((const uint4 *)order)[i];
-        if (tid < n_near) {
+        if (!sparse && tid < n_near) {
             const int i = base + order[tid];
             a.near[at * NEAR + tid] = token_of(key_of(l[i]), i);
         }
-    } else if (tid < n_near) {
-        a.near[at * NEAR + tid] = near[tid];
     }
     if (tid == 0) {
         a.tops[at] = token_of(key_of(most), first_most);
-        a.near_n[at] = (u32)n_near | (u32)depth << 16 | (u32)ordered << 31;
+        a.near_n[at] = (u32)n_near | (u32)depth << 16;
     }
 }
 static_assert(NEAR <= CHUNK_THREADS, "a thread a token of the list");
@@ -672,16 +676,14 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             one = true;
         }
     }
-    // the chunks' lists go down to bin `low`; or they are ordered
-    bool near = low < BINS - 1, ordered = true;
+    // the chunks' lists go down to bin `low`
+    bool near = low < BINS - 1;
 #pragma unroll
     for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-        const int depth = (int)(near_n[i] >> 16 & 0x7FFF);
-        ordered = ordered && (!(first_of[i] >> 32) || near_n[i] >> 31);
+        const int depth = (int)(near_n[i] >> 16);
         near = near && (!(first_of[i] >> 32) || depth == BINS || m.off[lane + 64 * i] + depth > low);
     }
     near = __ballot(!near) == 0;
-    ordered = __ballot(!ordered) == 0;
     // the tokens of bins high .. low in the chunks' lists, each with a place of its own
     auto from_lists = [&](int high, int low, auto &&put) {
         for (int c = wave; c < a.chunks; c += ROW_WAVES) {
@@ -762,13 +764,13 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         const double y = (r.from - high + 1) / r.s.eighths;
         hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
     }
-    bool listed = scan && low < BINS - 1 && gathered <= LIST - 64;
+    const bool listed = scan && low < BINS - 1 && gathered <= LIST - 64;
     if (listed && near) {
         from_lists(high, low, [&](int to, u64 token) {
             if (to < LIST) m.list[to] = token;
         });
         __syncthreads();
-    } else if (listed && ordered) {
+    } else if (listed) {
         // bins high .. low of each chunk, behind each other in the list
         u32 from[MAX_CHUNKS / 64], n[MAX_CHUNKS / 64], to[MAX_CHUNKS / 64], all = 0;
 #pragma unroll
@@ -805,39 +807,6 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
         if (tid == 0) m.n = (int)all;
         __syncthreads();
-    } else if (listed) {
-        constexpr int BATCH = 8;                  // pieces of 4 a thread; the next ones are on their way
-        f4 now[BATCH], next[BATCH];
-        auto ask = [&](f4 (&x)[BATCH], int i0) {
-#pragma unroll
-            for (int p = 0; p < BATCH; ++p) x[p] = four(r.l, i0 + 4 * ROW_THREADS * p, a.V);
-        };
-        ask(now, 4 * tid);
-        for (int i0 = 0; i0 < a.V; i0 += 4 * ROW_THREADS * BATCH) {
-            if (i0 + 4 * ROW_THREADS * BATCH < a.V) ask(next, i0 + 4 * ROW_THREADS * BATCH + 4 * tid);
-            u32 mask = 0;
-#pragma unroll
-            for (int i = 0; i < 4 * BATCH; ++i) {
-                const float x = now[i / 4][i % 4];
-                mask |= (u32)(x >= lo && x <= hi) << i;
-            }
-            // (places first: a lane's few are gone over by their bits, its logits read again)
-            int to = room(&m.n, __popc(mask));
-            for (; mask; mask &= mask - 1, ++to) {
-                const int i = __builtin_ctz(mask);
-                if (to < LIST) m.list[to] = (u64)(u32)(i0 + 4 * tid + 4 * ROW_THREADS * (i / 4) + i % 4);
-            }
-#pragma unroll
-            for (int p = 0; p < BATCH; ++p) now[p] = next[p];
-        }
-        __syncthreads();
-        for (int i = tid; i < min(m.n, LIST); i += ROW_THREADS) {
-            const int at = (int)m.list[i];
-            m.list[i] = token_of(key_of(r.l[at]), at);
-        }
-        // (more than the bins hold: what is a rounding away from them, and with top_k, of
-        // which the chunks did not count all of their tokens, any number)
-        listed = m.n <= LIST;
     }
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
