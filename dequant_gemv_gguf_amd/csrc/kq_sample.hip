@@ -39,7 +39,7 @@ constexpr int ROW_THREADS = 1024, ROW_WAVES = ROW_THREADS / 64;
 constexpr int MAX_V = 1 << 20, MAX_CHUNKS = MAX_V / CHUNK;
 constexpr int BINS = 512, OCTAVE = 8;             // bins, and those of an octave
 constexpr int COUNT_SHIFT = 50;                   // a bin: count, and below it the sum of weights
-constexpr int LIST = 5120;                        // (all of row_kernel's LDS below 64 KB)
+constexpr int LIST = 6144;                        // tokens that row_kernel keeps in registers
 constexpr int NEAR = 256;                         // tokens of a chunk's list
 constexpr int SPARSE = 1024;                      // tokens of a chunk that can matter, where those are put together first
 constexpr int FEW = 256;                          // tokens that are compared with each other
@@ -52,7 +52,7 @@ struct Sample {
     int32_t *tokens;
     float *probs;
     u64 *tops;              // [row][chunk] first token
-    u32 *near_n;            // [row][chunk] tokens of its list, from bit 16 the bins it goes down
+    u32 *near_n;            // [row][chunk] tokens of its list
     u64 *near;              // [row][chunk][NEAR]
     u64 *hist;              // [row][chunk][BINS]
     uint16_t *upto;         // [row][chunk][BINS] tokens down to and with a bin
@@ -385,18 +385,17 @@ __global__ __launch_bounds__(CHUNK_THREADS) void chunk_kernel(const Sample a) {
     }
     if (tid == 0) {
         a.tops[at] = token_of(key_of(most), first_most);
-        a.near_n[at] = (u32)n_near | (u32)depth << 16;
+        a.near_n[at] = (u32)n_near;
     }
 }
 static_assert(NEAR <= CHUNK_THREADS, "a thread a token of the list");
+static_assert(FEW <= NEAR, "where a row has so few down to a bin, its chunks' lists go down to it");
 static_assert(CHUNK_THREADS == BINS, "a thread a bin");
 
 // What row_kernel shares between its threads.
 struct RowSpace {
-    union {
-        u64 list[LIST];             // gathered tokens
-        struct { u64 token, weight; } few[FEW];
-    };
+    struct { u64 token, weight; } few[FEW];
+    u32 begin[MAX_CHUNKS], skip[MAX_CHUNKS];        // of a chunk's gathered tokens among all; and to their places in its order
     u64 weight[BINS];               // of the row's bins
     double upto[BINS];              // summed weights up to and with a bin, in units of the top octave's mantissas
     u32 count[BINS], counts[BINS];  // tokens of a bin, and up to and with it
@@ -676,38 +675,24 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             one = true;
         }
     }
-    // the chunks' lists go down to bin `low`
-    bool near = low < BINS - 1;
-#pragma unroll
-    for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-        const int depth = (int)(near_n[i] >> 16);
-        near = near && (!(first_of[i] >> 32) || depth == BINS || m.off[lane + 64 * i] + depth > low);
-    }
-    near = __ballot(!near) == 0;
-    // the tokens of bins high .. low in the chunks' lists, each with a place of its own
-    auto from_lists = [&](int high, int low, auto &&put) {
+    if (low < BINS - 1 && m.counts[low] <= FEW) {
+        // Few tokens, all of them in the chunks' lists: each with those before it (4 threads
+        // a token, a quarter of the others each).
         for (int c = wave; c < a.chunks; c += ROW_WAVES) {
             if (c != wave) ask_list(c);
             if (m.off[c] < 0 || m.off[c] > low) continue;
-            const int n = (int)((u32)__builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63) & 0xFFFF);
+            const int n = __builtin_amdgcn_readlane((int)(c < 64 ? near_n[0] : near_n[1]), c & 63);
             u32 mask = 0;
 #pragma unroll
-            for (int i = 0; i < NEAR / 64; ++i) {
-                const int b = lane + 64 * i < n ? r.bin(logit_of((u32)(listed_[i] >> 32))) : BINS;
-                mask |= (u32)(b >= high && b <= low) << i;
-            }
+            for (int i = 0; i < NEAR / 64; ++i) mask |= (u32)(lane + 64 * i < n && r.bin(logit_of((u32)(listed_[i] >> 32))) <= low) << i;
             int to = room(&m.n, __popc(mask));
 #pragma unroll
             for (int i = 0; i < NEAR / 64; ++i)
-                if (mask >> i & 1) put(to++, listed_[i]);
+                if (mask >> i & 1) {
+                    if (to < FEW) m.few[to].token = listed_[i];
+                    ++to;
+                }
         }
-    };
-    if (near && m.counts[low] <= FEW) {
-        // Few tokens: each with those before it (4 threads a token, a quarter of the others each).
-        from_lists(0, low, [&](int to, u64 token) {
-            if (to >= FEW) return;
-            m.few[to].token = token;
-        });
         __syncthreads();
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
         const u64 token = m.few[min(i, n - 1)].token, weight = r.integer(token, 14, 0);
@@ -764,50 +749,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         const double y = (r.from - high + 1) / r.s.eighths;
         hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
     }
-    const bool listed = scan && low < BINS - 1 && gathered <= LIST - 64;
-    if (listed && near) {
-        from_lists(high, low, [&](int to, u64 token) {
-            if (to < LIST) m.list[to] = token;
-        });
-        __syncthreads();
-    } else if (listed) {
-        // bins high .. low of each chunk, behind each other in the list
-        u32 from[MAX_CHUNKS / 64], n[MAX_CHUNKS / 64], to[MAX_CHUNKS / 64], all = 0;
-#pragma unroll
-        for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-            const int c = lane + 64 * i, off = m.off[c];
-            const uint16_t *upto = a.upto + (chunk0 + c) * BINS;
-            const bool in = off >= 0 && off <= low;
-            from[i] = in && high > off ? upto[high - off - 1] : 0;
-            n[i] = (in ? upto[low - off] : 0) - from[i];
-        }
-#pragma unroll
-        for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
-            const u32 upto = wave_scan(n[i]);
-            to[i] = all + upto - n[i];
-            all += last_lane(upto);
-        }
-        // (several waves a chunk where there are few)
-        const int ways = max(1, ROW_WAVES / a.chunks), way = a.chunks < ROW_WAVES ? wave / a.chunks : 0;
-        for (int c = wave - way * a.chunks; c < a.chunks && way < ways; c += ROW_WAVES) {
-            auto of = [&](const u32 (&x)[MAX_CHUNKS / 64]) { return __builtin_amdgcn_readlane((int)(c < 64 ? x[0] : x[1]), c & 63); };
-            const int count = of(n), at = of(to);
-            const uint16_t *places = a.order + (chunk0 + c) * CHUNK + of(from);
-            for (int j0 = 256 * way + lane; j0 < count; j0 += 256 * ways) {
-                int i[4];
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) i[j] = c * CHUNK + places[min(j0 + 64 * j, count - 1)];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = r.l[i[j]];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j0 + 64 * j < count) m.list[at + j0 + 64 * j] = token_of(key_of(x[j]), i[j]);
-            }
-        }
-        if (tid == 0) m.n = (int)all;
-        __syncthreads();
-    }
+    const bool listed = scan && low < BINS - 1 && gathered <= LIST;
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
     // 2^20 tokens have to fit the sum).
@@ -839,17 +781,54 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         __syncthreads();
     };
     if (listed) {
-        // a thread's tokens and their weights, in registers (0: none)
-        u64 token[LIST / ROW_THREADS], w[LIST / ROW_THREADS];
-        const int n = m.n;
+        // Bins high .. low of each chunk, one behind the other: where each begins, and
+        // where the chunk's order has it.
+        if (wave == 0) {
+            u32 before = 0;
 #pragma unroll
-        for (int i = 0; i < LIST / ROW_THREADS; ++i) {
-            token[i] = w[i] = 0;
-            if (i * ROW_THREADS >= n) continue;
-            token[i] = tid + i * ROW_THREADS < n ? m.list[tid + i * ROW_THREADS] : 0;
-            const int b = token[i] >> 32 ? r.bin(logit_of((u32)(token[i] >> 32))) : BINS;
-            if (b < high || b > low) token[i] = 0;
-            w[i] = token[i] ? r.integer(token[i], finer, base) : 0;
+            for (int i = 0; i < MAX_CHUNKS / 64; ++i) {
+                const int c = lane + 64 * i, off = m.off[c];
+                const uint16_t *upto = a.upto + (chunk0 + c) * BINS;
+                const bool in = off >= 0 && off <= low;
+                const u32 from = in && high > off ? upto[high - off - 1] : 0, n = (in ? upto[low - off] : 0) - from;
+                const u32 all = wave_scan(n);
+                m.begin[c] = before + all - n;
+                m.skip[c] = from - m.begin[c];
+                before += last_lane(all);
+            }
+        }
+        __syncthreads();
+        // A thread's tokens and their weights, in registers (0: none).  (Of 1024 tokens the
+        // lanes of a wave take those 65 apart, which lie in several chunks: their sums
+        // below would wait for one address.)
+        constexpr int TOKENS = LIST / ROW_THREADS, HALF = TOKENS / 2;
+        u64 token[TOKENS], w[TOKENS];
+        const int n = (int)gathered;
+#pragma unroll
+        for (int h = 0; h < TOKENS; h += HALF) {
+#pragma unroll
+            for (int i = h; i < h + HALF; ++i) token[i] = w[i] = 0;
+            if (h * ROW_THREADS >= n) continue;
+            int at[HALF];
+            float x[HALF];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                const int first = (h + i) * ROW_THREADS, p = min(first + (first + ROW_THREADS <= n ? (tid * 65) & (ROW_THREADS - 1) : tid), n - 1);
+                int c = 0;
+#pragma unroll
+                for (int step = MAX_CHUNKS / 2; step; step >>= 1)
+                    if (step < a.chunks && c + step < a.chunks && (int)m.begin[c + step] <= p) c += step;
+                at[i] = c * CHUNK + a.order[(chunk0 + c) * CHUNK + p + (int)m.skip[c]];
+            }
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) x[i] = r.l[at[i]];
+#pragma unroll
+            for (int i = 0; i < HALF; ++i) {
+                const int first = (h + i) * ROW_THREADS;
+                if (first >= n || (first + ROW_THREADS > n && first + tid >= n)) continue;
+                token[h + i] = token_of(key_of(x[i]), at[i]);
+                w[h + i] = r.integer(token[h + i], finer, base);
+            }
         }
         places([&](auto &&f) {
 #pragma unroll
@@ -867,19 +846,32 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     }
     // and of the bins above them
     const int whole = !scan ? BINS : one && listed ? low : 0;
-    for (int c = wave; c < a.chunks; c += ROW_WAVES) {
-        double w = 0.0;
-        const int off = m.off[c];
-        if (off >= 0 && off < whole) {
-            const u64 *h = a.hist + (chunk0 + c) * BINS;
+    for (int c0 = wave; c0 < a.chunks; c0 += 2 * ROW_WAVES) {
+        int off[2];
+        u64 h[2][BINS / 64];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + k * ROW_WAVES;
+            off[k] = c < a.chunks ? __builtin_amdgcn_readfirstlane(m.off[c]) : -1;
+            if (off[k] < 0) off[k] = BINS;
+#pragma unroll
+            for (int i = 0; i < BINS / 64; ++i) h[k][i] = off[k] + 64 * i < whole ? a.hist[(chunk0 + c) * BINS + lane + 64 * i] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int c = c0 + k * ROW_WAVES;
+            if (c >= a.chunks) break;
+            double w = 0.0;
 #pragma unroll
             for (int i = 0; i < BINS / 64; ++i) {
-                const int d = lane + 64 * i;
-                if (d + off < min(whole, BINS - 1)) w += ldexp((double)(h[d] & ((1ull << COUNT_SHIFT) - 1)), -r.octaves(d + off));
+                if (off[k] + 64 * i >= whole) break;
+                const int b = off[k] + 64 * i + lane;
+                const double x = ldexp((double)(h[k][i] & ((1ull << COUNT_SHIFT) - 1)), -r.octaves(b));
+                w += b < min(whole, BINS - 1) ? x : 0.0;
             }
+            w = sum_d<64>(w);
+            if (lane == 0) m.chunk_sum[c] = w + ldexp((double)m.chunk_list[c], -base - finer);
         }
-        w = sum_d<64>(w);
-        if (lane == 0) m.chunk_sum[c] = w + ldexp((double)m.chunk_list[c], -base - finer);
     }
     __syncthreads();
     // the chunk
