@@ -19,12 +19,11 @@
 //    which each filter ends.  Where few tokens are left down to that bin (hundreds,
 //    and all in the chunks' lists), every one of them is compared with every other
 //    and that is all (one row of 32000 13.6 us; by digits, as below, 20.4).  Elsewhere
-//    the bin's tokens are gathered in LDS, from the lists or the ordered chunks (256 rows
-//    76 us; by a scan of the row, which is left for a list that is too short in a chunk
-//    that is not ordered, 84), where the place is found digit by digit of the logits'
-//    keys, the chunks' kept weights say which chunk holds the token, and its logits are
-//    gone over once more.  Where the gathered tokens do not fit in LDS (thousands of
-//    equal logits, a very high temperature), the digits are found over the row itself.
+//    the bin's tokens are gathered from the ordered chunks into registers (256 rows
+//    76 us; by a scan of the row 84), the place among them is found digit by digit of the
+//    logits' keys, the chunks' kept weights say which chunk holds the token, and its
+//    logits are gone over once more.  Bins of more than 6144 tokens (thousands of equal
+//    logits, a very high temperature) are not kept: the row is read for every digit.
 // Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
 // the row's largest.
 #include "kq_step.h"
@@ -740,34 +739,33 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
     const bool scan = low < BINS;
     // what can lie in these bins, and a little more
-    float lo = -__builtin_inff(), hi = __builtin_inff();
+    float lo = -3.402823466e38f, hi = __builtin_inff();
     if (r.s.eighths > 0.0 && most < __builtin_inff()) {
         if (low < BINS - 1) {
             const double x = (r.from - low) / r.s.eighths;
-            lo = (float)(x - fabs(x) * 0x1p-22) - 1e-37f;
+            lo = fmaxf(lo, (float)(x - fabs(x) * 0x1p-22) - 1e-37f);
         }
         const double y = (r.from - high + 1) / r.s.eighths;
         hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
     }
     const bool listed = scan && low < BINS - 1 && gathered <= LIST;
     // Weights of gathered tokens as integers: with one bin in units of its octave's
-    // mantissas, else of the top's, both 14 bits finer (7 over the whole row, whose
-    // 2^20 tokens have to fit the sum).
-    const int finer = listed ? 14 : 7, base = one && listed ? r.octaves(low) : 0;
+    // mantissas, else of the top's, both 14 bits finer (7 where up to 2^20 tokens have to
+    // fit the sum).
+    const int finer = listed ? 14 : 7, base = one ? r.octaves(low) : 0;
     u64 least = 0;                                // top_k and top_p keep the tokens from here on
     // each(f): f(token, weight()) for every gathered token
     auto places = [&](auto &&each) {
-        // (where the tokens of these bins lie; the whole row's begin at the first one)
-        const u64 lowest = (u64)key_of(lo) << 32, top = listed ? min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF) : best;
+        // (where the tokens of these bins lie)
+        const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
         if (by_k && total >= top_k) least = cut<false>(m, each, lowest, top, (u64)top_k);
-        if (by_p && (by_k || !listed || low == m.low)) {
-            // Of what top_k leaves; in the one bin that decides, what the bins above it
-            // leave; over the row, of all its weight.
+        if (by_p && (by_k || low == m.low)) {
+            // of what top_k leaves; in the one bin that decides, what the bins above it leave
             u64 sum = 0;
             each([&](u64 token, auto &&weight) { sum += token >= least ? weight() : 0; });
             sum = block_sum(m, sum);
-            const double want = one && listed ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
-                                              : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
+            const double want = one ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
+                                    : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
             least = cut<true>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
@@ -836,16 +834,25 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
                 if (i * ROW_THREADS < n && token[i]) f(token[i], [&] { return w[i]; });
         });
     } else if (scan) {
+        // (the next logits are on their way)
         places([&](auto &&f) {
-            for (int i = tid; i < a.V; i += ROW_THREADS) {
-                const u32 key = key_of(r.l[i]);
-                const u64 token = token_of(key, i);
-                if (key) f(token, [&] { return r.integer(token, finer, base); });
+            f4 now = four(r.l, 4 * tid, a.V);
+            for (int i = 4 * tid; i < a.V; i += 4 * ROW_THREADS) {
+                const f4 next = four(r.l, i + 4 * ROW_THREADS, a.V);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = now[j];
+                    if (!(x >= lo && x <= hi)) continue;
+                    const int b = min(r.bin(x), BINS - 1);
+                    const u64 token = token_of(key_of(x), i + j);
+                    if (b >= high && b <= low) f(token, [&] { return r.integer(token, finer, base); });
+                }
+                now = next;
             }
         });
     }
     // and of the bins above them
-    const int whole = !scan ? BINS : one && listed ? low : 0;
+    const int whole = !scan ? BINS : one ? low : 0;
     for (int c0 = wave; c0 < a.chunks; c0 += 2 * ROW_WAVES) {
         int off[2];
         u64 h[2][BINS / 64];
