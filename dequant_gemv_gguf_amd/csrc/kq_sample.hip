@@ -391,6 +391,15 @@ static_assert(NEAR <= CHUNK_THREADS, "a thread a token of the list");
 static_assert(FEW <= NEAR, "where a row has so few down to a bin, its chunks' lists go down to it");
 static_assert(CHUNK_THREADS == BINS, "a thread a bin");
 
+// Bits by which the sum of n weights of 36 bits of mantissa can be finer than these.
+constexpr int FINEST = 27;
+__host__ __device__ constexpr int finer_for(int n) {
+    int bits = 0;
+    while (n > 1 << bits) ++bits;
+    return FINEST - bits;
+}
+constexpr int FEW_FINER = finer_for(FEW);
+
 // What row_kernel shares between its threads.
 struct RowSpace {
     struct { u64 token, weight; } few[FEW];
@@ -434,7 +443,10 @@ struct Row {
         return b <= last ? w : 0.0;
     }
     __device__ __forceinline__ u64 mantissa(float x, int b) const { return s.mantissa(x, (phase - b) & (OCTAVE - 1)); }
-    __device__ __forceinline__ bool keeps(u64 token, double w) const { return token == best || w >= least; }
+    // whether min_p keeps it (by its whole weight: `integer` loses bits of small ones)
+    __device__ __forceinline__ bool keeps(u64 token) const {
+        return !(least > 0.0) || token == best || weight(logit_of((u32)(token >> 32)), BINS - 2) >= least;
+    }
     // as an integer, in units of the mantissas `base` octaves below, 2^finer to one
     __device__ __forceinline__ u64 integer(u64 token, int finer, int base) const {
         const float x = logit_of((u32)(token >> 32));
@@ -694,7 +706,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
         __syncthreads();
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
-        const u64 token = m.few[min(i, n - 1)].token, weight = r.integer(token, 14, 0);
+        const u64 token = m.few[min(i, n - 1)].token, weight = r.integer(token, FEW_FINER, 0);
         if (i < n && part == 0) m.few[i].weight = weight;
         __syncthreads();
         u64 upto = 0, place = 0;
@@ -711,10 +723,10 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         if (lane == 0) atomicMax((unsigned long long *)&m.most, mine);
         __syncthreads();
         if (by_p) {
-            const double want = by_k ? (double)(top_p > 0.f ? top_p : 0.f) * (double)m.most : ldexp(want_p, 14);
+            const double want = by_k ? (double)(top_p > 0.f ? top_p : 0.f) * (double)m.most : ldexp(want_p, FEW_FINER);
             kept = kept && (place == 1 || (double)(upto - weight) < want);
         }
-        kept = kept && r.keeps(token, ldexp((double)weight, -14));
+        kept = kept && r.keeps(token);
         mine = wave_max(kept ? upto : 0);
         if (lane == 0) atomicMax((unsigned long long *)&m.sum, mine);
         __syncthreads();
@@ -731,7 +743,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         before = quad_sum(before);
         if (part == 0 && kept && before <= past && past < before + weight) {
             a.tokens[row] = (int)~(u32)token;
-            if (a.probs) a.probs[row] = (float)((double)weight / (double)sum);
+            if (a.probs) a.probs[row] = (float)(r.weight(logit_of((u32)(token >> 32)), BINS - 2) / ldexp((double)sum, -FEW_FINER));
         }
         return;
     }
@@ -750,15 +762,23 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     }
     const bool listed = scan && low < BINS - 1 && gathered <= LIST;
     // Weights of gathered tokens as integers: with one bin in units of its octave's
-    // mantissas, else of the top's, both 14 bits finer (7 where up to 2^20 tokens have to
-    // fit the sum).
-    const int finer = listed ? 14 : 7, base = one ? r.octaves(low) : 0;
+    // mantissas, which hold them whole; else of the top's, and finer by the bits that the
+    // sum of so many of at most 2^36 leaves of 63.
+    const int base = one ? r.octaves(low) : 0, summed = by_k ? min((int)gathered, top_k) : (int)gathered;
+    int finer = finer_for(listed ? LIST : summed);
     u64 least = 0;                                // top_k and top_p keep the tokens from here on
     // each(f): f(token, weight()) for every gathered token
     auto places = [&](auto &&each) {
         // (where the tokens of these bins lie)
         const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
         if (by_k && total >= top_k) least = cut<false>(m, each, lowest, top, (u64)top_k);
+        if (by_k && !listed) {
+            // (many tokens may weigh little together: as fine as their sum lets)
+            u64 sum = 0;
+            each([&](u64 token, auto &&weight) { sum += token >= least ? weight() : 0; });
+            sum = block_sum(m, sum);
+            if (sum) finer = min(finer + __builtin_clzll(sum) - 1, FINEST);
+        }
         if (by_p && (by_k || low == m.low)) {
             // of what top_k leaves; in the one bin that decides, what the bins above it leave
             u64 sum = 0;
@@ -773,7 +793,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         each([&](u64 token, auto &&weight) {
             if (token < least) return;
             const u64 w = weight();
-            if (w && r.keeps(token, ldexp((double)w, -base - finer)))
+            if (w && r.keeps(token))
                 atomicAdd((unsigned long long *)&m.chunk_list[(int)~(u32)token / CHUNK], w);
         });
         __syncthreads();

@@ -168,6 +168,22 @@ def test_settings_out_of_their_ranges():
     assert list(edge) == [0, 0, 0, last, last]
 
 
+@pytest.mark.parametrize("V", [40, 3000, 30000])
+def test_min_p_far_below_the_largest(V):
+    """Borders 20 to 30 octaves down, with logits a few 2^-20 of a weight to each side of them: what is kept shows in the probability of
+    the last token at u near 1 (the largest is the first)."""
+    M = 8
+    l = np.full((M, V), -np.inf, np.float32)
+    l[:, 0] = 0
+    mp = np.exp(-np.linspace(14, 21, M)).astype(np.float32)
+    below = np.log(mp.astype(np.float64))
+    for i in range(M):
+        # steps of fp32 around the border, at least 2^-19 of it each: none within 2^-24 of it but by chance, which `check` would show
+        l[i, 1:] = (below[i] + np.linspace(-3e-5, 3e-5, V - 1)).astype(np.float32)
+    for k in (None, np.full(M, min(V - 1, 25)), np.full(M, min(V - 1, 2000))):
+        check(l, t=np.ones(M), k=k, mp=mp, u=np.full(M, np.float32(1 - 2.0 ** -24)))
+
+
 def test_u_at_the_borders_of_tokens():
     """Four tokens of exactly a quarter each: u of a border belongs to the next one."""
     l = np.zeros((8, 4), np.float32)
