@@ -4,7 +4,7 @@
 // of (logit descending, index ascending), so a filter is a place in that order.
 //
 // Bound: for few rows the chain of two launches (one row of 32000 tokens, top_k 40,
-// top_p and min_p: 13.6 us); for many the arithmetic of the first (256 rows of 151937,
+// top_p and min_p: 13 us); for many the arithmetic of the first (256 rows of 151937,
 // settings of each row: 76 us, of which it takes 52; 3.0 TB/s there, 6.8 where all rows
 // are greedy).  Two launches:
 //  * chunk_kernel, a work-group a chunk of 8192 tokens of a row: the chunk's first
@@ -18,7 +18,7 @@
 //  * row_kernel, a work-group a row: the chunks' histograms added up give the bin in
 //    which each filter ends.  Where few tokens are left down to that bin (hundreds,
 //    and all in the chunks' lists), every one of them is compared with every other
-//    and that is all (one row of 32000 13.6 us; by digits, as below, 20.4).  Elsewhere
+//    and that is all (one row of 32000 13 us; by digits, as below, 20).  Elsewhere
 //    the bin's tokens are gathered from the ordered chunks into registers (256 rows
 //    76 us; by a scan of the row 84), the place among them is found digit by digit of the
 //    logits' keys, the chunks' kept weights say which chunk holds the token, and its
@@ -705,33 +705,43 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
                 }
         }
         __syncthreads();
+        // (a wave has 16 tokens; those without any only wait)
         const int n = min(m.n, FEW), i = tid >> 2, part = tid & 3;
-        const u64 token = m.few[min(i, n - 1)].token, weight = r.integer(token, FEW_FINER, 0);
-        if (i < n && part == 0) m.few[i].weight = weight;
+        const bool any = 16 * wave < n;
+        u64 token = 0, weight = 0, upto = 0, place = 0;
+        if (any) {
+            token = m.few[min(i, n - 1)].token;
+            weight = r.integer(token, FEW_FINER, 0);
+            if (i < n && part == 0) m.few[i].weight = weight;
+        }
         __syncthreads();
-        u64 upto = 0, place = 0;
+        bool kept = false;
+        if (any) {
 #pragma unroll 4
-        for (int j = part; j < n; j += 4) {
-            const bool before = m.few[j].token >= token;
-            place += before;
-            upto += before ? m.few[j].weight : 0;
+            for (int j = part; j < n; j += 4) {
+                const bool before = m.few[j].token >= token;
+                place += before;
+                upto += before ? m.few[j].weight : 0;
+            }
+            place = quad_sum(place);
+            upto = quad_sum(upto);
+            kept = i < n && (!by_k || (int)place <= keep_k);
+            const u64 mine = wave_max(kept ? upto : 0);
+            if (lane == 0) atomicMax((unsigned long long *)&m.most, mine);
         }
-        place = quad_sum(place);
-        upto = quad_sum(upto);
-        bool kept = i < n && (!by_k || (int)place <= keep_k);
-        u64 mine = wave_max(kept ? upto : 0);
-        if (lane == 0) atomicMax((unsigned long long *)&m.most, mine);
         __syncthreads();
-        if (by_p) {
-            const double want = by_k ? (double)(top_p > 0.f ? top_p : 0.f) * (double)m.most : ldexp(want_p, FEW_FINER);
-            kept = kept && (place == 1 || (double)(upto - weight) < want);
+        if (any) {
+            if (by_p) {
+                const double want = by_k ? (double)(top_p > 0.f ? top_p : 0.f) * (double)m.most : ldexp(want_p, FEW_FINER);
+                kept = kept && (place == 1 || (double)(upto - weight) < want);
+            }
+            kept = kept && r.keeps(token);
+            const u64 mine = wave_max(kept ? upto : 0);
+            if (lane == 0) atomicMax((unsigned long long *)&m.sum, mine);
+            if (i < n && part == 0 && !kept) m.few[i].weight = 0;
         }
-        kept = kept && r.keeps(token);
-        mine = wave_max(kept ? upto : 0);
-        if (lane == 0) atomicMax((unsigned long long *)&m.sum, mine);
         __syncthreads();
-        if (i < n && part == 0 && !kept) m.few[i].weight = 0;
-        __syncthreads();
+        if (!any) return;
         // the kept weights up to each token, by index
         const u64 sum = m.sum;
         const float u = set.u;
