@@ -29,6 +29,7 @@
 #include "kq_step.h"
 
 #include <cmath>
+#include <type_traits>
 
 namespace kq {
 namespace step {
@@ -400,6 +401,10 @@ __host__ __device__ constexpr int finer_for(int n) {
 }
 constexpr int FEW_FINER = finer_for(FEW);
 
+// Bits of a digit where the tokens are in registers, and where the row is read for each.
+constexpr int DIGIT = 8, WIDE_DIGIT = 11;
+static_assert(1 << WIDE_DIGIT == 2 * ROW_THREADS, "two digits a thread");
+
 // What row_kernel shares between its threads.
 struct RowSpace {
     struct { u64 token, weight; } few[FEW];
@@ -407,8 +412,8 @@ struct RowSpace {
     u64 weight[BINS];               // of the row's bins
     double upto[BINS];              // summed weights up to and with a bin, in units of the top octave's mantissas
     u32 count[BINS], counts[BINS];  // tokens of a bin, and up to and with it
-    u64 digit_weight[256];
-    u32 digit_count[256];
+    u64 digit_weight[1 << WIDE_DIGIT];
+    u32 digit_count[1 << WIDE_DIGIT];
     u64 chunk_list[MAX_CHUNKS];     // kept weight of a chunk's gathered tokens
     double chunk_sum[MAX_CHUNKS];
     u64 waves[ROW_WAVES];
@@ -458,55 +463,96 @@ struct Row {
 // The shortest leading part (descending) of the tokens from `from` on that `each` goes
 // over, of which the counts, or the weights (WEIGHTS), sum to at least `want` (1 .. the
 // whole sum): the part is the tokens from the returned place on (which need not be a
-// token).  Digits of 8 bits of what a token is above `from` (to find the bits in which
-// they differ instead takes two reductions and 1.5 us), from the first that one up to
-// `top`, the most that any is, can have.  The digits' sums are 0 before and after.
-template <bool WEIGHTS, class Each>
+// token).  Digits of what a token is above `from` (to find the bits in which they differ
+// instead takes two reductions and 1.5 us), from the first that one up to `top`, the
+// most that any is, can have.  The digits' sums are 0 before and after.
+template <bool WEIGHTS, bool WIDE, class Each>
 __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, u64 want) {
+    constexpr int BITS = WIDE ? WIDE_DIGIT : DIGIT, INDEX = 20;
+    static_assert(MAX_V == 1 << INDEX, "");
     const int tid = threadIdx.x, lane = tid & 63;
-    int above = top > from ? 64 - __builtin_clzll(top - from) : 0;       // bits from here on are `prefix`
+    if (WIDE) {
+        // (equal logits are common, and would all meet in a digit: the first of the bits
+        // in which the keys differ)
+        u32 most = 0, least = 0;
+        each([&](u64 token, auto &&) {
+            if (token < from) return;
+            most = max(most, (u32)(token >> 32));
+            least = max(least, ~(u32)(token >> 32));
+        });
+        auto larger = [](u32 p, u32 q) { return max(p, q); };
+        most = wave_all(most, larger);
+        least = wave_all(least, larger);
+        if (lane == 0) m.waves[tid >> 6] = (u64)most << 32 | least;
+        __syncthreads();
+        for (int w = 0; w < ROW_WAVES; ++w) {
+            most = max(most, (u32)(m.waves[w] >> 32));
+            least = max(least, (u32)m.waves[w]);
+        }
+        from = max(from, (u64)~least << 32);
+        top = min(top, (u64)most << 32 | 0xFFFFFFFF);
+        __syncthreads();
+    }
+    // (wide, with the index in 20 bits: fewer digits)
+    auto over = [&](u64 token) {
+        return WIDE ? (u64)((u32)(token >> 32) - (u32)(from >> 32)) << INDEX | (token & (MAX_V - 1)) : token - from;
+    };
+    const u64 most = top > from ? over(top) : 0;
+    int above = most ? 64 - __builtin_clzll(most) : 0;                     // bits from here on are `prefix`
     u64 prefix = 0, before = 0;
     while (above) {
-        const int shift = max(above - 8, 0);
+        const int shift = max(above - BITS, 0);
         const u32 digits = (1u << (above - shift)) - 1;
         each([&](u64 token, auto &&weight) {
-            const u64 v = token - from;
+            const u64 v = over(token);
             if (token < from || (above < 64 && v >> above != prefix)) return;
             const u32 d = (u32)(v >> shift) & digits;
             atomicAdd(&m.digit_count[d], 1u);
             if (WEIGHTS) atomicAdd((unsigned long long *)&m.digit_weight[d], weight());
         });
         __syncthreads();
-        if (tid < 64) {
-            // 4 digits a lane, descending
-            u32 n[4];
-            u64 d[4], s = 0;
+        // EACH digits a lane, descending, by one wave or by all
+        constexpr int EACH = WIDE ? 2 : 4;
+        u32 n[EACH];
+        u64 d[EACH], s = 0, upto = 0;
+        if (WIDE || tid < 64) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int digit = 255 - (4 * lane + i);
+            for (int i = 0; i < EACH; ++i) {
+                const int digit = (1 << BITS) - 1 - (EACH * tid + i);
                 n[i] = m.digit_count[digit];
                 d[i] = WEIGHTS ? m.digit_weight[digit] : n[i];
                 m.digit_count[digit] = 0;
                 if (WEIGHTS) m.digit_weight[digit] = 0;
                 s += d[i];
             }
-            const u64 upto = wave_scan(s);
-            const u64 reach = __ballot(before + upto >= want);
-            if (lane == (reach ? __builtin_ctzll(reach) : 63)) {
-                u64 b = before + upto - s;
-                int at = 0;
-                u32 count = n[0];
+            upto = wave_scan(s);
+        }
+        bool here;
+        if (WIDE) {
+            if (lane == 63) m.waves[tid >> 6] = upto;
+            __syncthreads();
+            for (int w = 0; w < tid >> 6; ++w) upto += m.waves[w];
+            upto += before;
+            here = upto >= want ? upto - s < want : tid == ROW_THREADS - 1;
+        } else {
+            upto += before;
+            const u64 reach = __ballot(upto >= want);
+            here = tid < 64 && lane == (reach ? __builtin_ctzll(reach) : 63);
+        }
+        if (here) {
+            u64 b = upto - s;
+            int at = 0;
+            u32 count = n[0];
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (at == i && b + d[i] < want) {
-                        b += d[i];
-                        at = i + 1;
-                        count = n[i + 1];
-                    }
-                m.found[0] = (u64)(255 - (4 * lane + at));
-                m.found[1] = b;
-                m.found[2] = count;
-            }
+            for (int i = 0; i < EACH - 1; ++i)
+                if (at == i && b + d[i] < want) {
+                    b += d[i];
+                    at = i + 1;
+                    count = n[i + 1];
+                }
+            m.found[0] = (u64)((1 << BITS) - 1 - (EACH * tid + at));
+            m.found[1] = b;
+            m.found[2] = count;
         }
         __syncthreads();
         prefix = prefix << (above - shift) | m.found[0];
@@ -514,7 +560,9 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, 
         above = shift;
         if (m.found[2] == 1) break;         // one token has these digits: none lies between it and them
     }
-    return from + (prefix << above);
+    const u64 v = prefix << above;
+    if (!WIDE) return from + v;
+    return max(from, (u64)((u32)(from >> 32) + (u32)(v >> INDEX)) << 32 | (0xFFFFFFFFu - (MAX_V - 1)) | (v & (MAX_V - 1)));
 }
 
 __device__ __forceinline__ u64 block_sum(RowSpace &m, u64 x) {
@@ -593,7 +641,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         m.weight[b] = 0;
         m.count[b] = 0;
     }
-    if (tid < 256) {
+    if (tid < 1 << DIGIT) {
         m.digit_weight[tid] = 0;
         m.digit_count[tid] = 0;
     }
@@ -777,26 +825,32 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     const int base = one ? r.octaves(low) : 0, summed = by_k ? min((int)gathered, top_k) : (int)gathered;
     int finer = finer_for(listed ? LIST : summed);
     u64 least = 0;                                // top_k and top_p keep the tokens from here on
-    // each(f): f(token, weight()) for every gathered token
-    auto places = [&](auto &&each) {
+    // each(f): f(token, weight()) for every gathered token; wide: from the row
+    auto places = [&](auto &&each, auto wide) {
+        constexpr bool WIDE = decltype(wide)::value;
         // (where the tokens of these bins lie)
         const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
-        if (by_k && total >= top_k) least = cut<false>(m, each, lowest, top, (u64)top_k);
-        if (by_k && !listed) {
-            // (many tokens may weigh little together: as fine as their sum lets)
-            u64 sum = 0;
-            each([&](u64 token, auto &&weight) { sum += token >= least ? weight() : 0; });
-            sum = block_sum(m, sum);
-            if (sum) finer = min(finer + __builtin_clzll(sum) - 1, FINEST);
+        if (by_k && total >= top_k) least = cut<false, WIDE>(m, each, lowest, top, (u64)top_k);
+        u64 sum = one && low < BINS - 1 ? m.weight[low] << finer : 0;
+        if (by_k && (WIDE || by_p)) {
+            auto all = [&] {
+                u64 mine = 0;
+                each([&](u64 token, auto &&weight) { mine += token >= least ? weight() : 0; });
+                return block_sum(m, mine);
+            };
+            sum = all();
+            if (WIDE && sum) {
+                // (many tokens may weigh little together: as fine as their sum lets)
+                const int more = min(__builtin_clzll(sum) - 1, FINEST - finer);
+                finer += max(more, 0);
+                if (more > 0 && by_p) sum = all();
+            }
         }
         if (by_p && (by_k || low == m.low)) {
             // of what top_k leaves; in the one bin that decides, what the bins above it leave
-            u64 sum = 0;
-            each([&](u64 token, auto &&weight) { sum += token >= least ? weight() : 0; });
-            sum = block_sum(m, sum);
             const double want = one ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
                                     : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
-            least = cut<true>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
+            least = cut<true, WIDE>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
         // kept weight of the gathered tokens, by chunk
@@ -862,24 +916,41 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
 #pragma unroll
             for (int i = 0; i < LIST / ROW_THREADS; ++i)
                 if (i * ROW_THREADS < n && token[i]) f(token[i], [&] { return w[i]; });
-        });
+        }, std::false_type());
     } else if (scan) {
+        for (int i = tid; i < 1 << WIDE_DIGIT; i += ROW_THREADS) {
+            m.digit_weight[i] = 0;
+            m.digit_count[i] = 0;
+        }
         // (the next logits are on their way)
-        places([&](auto &&f) {
+        auto row = [&](auto &&f) {
             f4 now = four(r.l, 4 * tid, a.V);
             for (int i = 4 * tid; i < a.V; i += 4 * ROW_THREADS) {
                 const f4 next = four(r.l, i + 4 * ROW_THREADS, a.V);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float x = now[j];
-                    if (!(x >= lo && x <= hi)) continue;
-                    const int b = min(r.bin(x), BINS - 1);
-                    const u64 token = token_of(key_of(x), i + j);
-                    if (b >= high && b <= low) f(token, [&] { return r.integer(token, finer, base); });
-                }
+                for (int j = 0; j < 4; ++j)
+                    if (now[j] >= lo && now[j] <= hi) f(now[j], token_of(key_of(now[j]), i + j));
                 now = next;
             }
-        });
+        };
+        if (one && low < BINS - 1) {
+            // one bin: its mantissas are the weights
+            const double bin = r.from - low;
+            const int of_octave = (r.phase - low) & (OCTAVE - 1);
+            places([&](auto &&f) {
+                row([&](float x, u64 token) {
+                    if (x == most ? low == 0 : r.s.bin(x) == bin) f(token, [&] { return r.s.mantissa(x, of_octave) << finer; });
+                });
+            }, std::true_type());
+        } else {
+            places([&](auto &&f) {
+                row([&](float x, u64 token) {
+                    // (with top_k a token a rounding past bin `low` is past the last one kept;
+                    // else this is the last bin, whose weights are none)
+                    f(token, [&] { return r.integer(token, finer, base); });
+                });
+            }, std::true_type());
+        }
     }
     // and of the bins above them
     const int whole = !scan ? BINS : one ? low : 0;
