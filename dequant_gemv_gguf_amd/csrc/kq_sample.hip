@@ -853,13 +853,25 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             least = cut<true, WIDE>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
         __syncthreads();
-        // kept weight of the gathered tokens, by chunk
+        // kept weight of the gathered tokens, by chunk (wide: a thread's tokens of a chunk
+        // follow each other, and all lanes are at the same one)
+        u64 mine = 0;
+        int at = 0;
+        auto put = [&] {
+            if (mine) atomicAdd((unsigned long long *)&m.chunk_list[at], mine);
+            mine = 0;
+        };
         each([&](u64 token, auto &&weight) {
             if (token < least) return;
+            const int c = (int)~(u32)token / CHUNK;
             const u64 w = weight();
-            if (w && r.keeps(token))
-                atomicAdd((unsigned long long *)&m.chunk_list[(int)~(u32)token / CHUNK], w);
+            if (!w || !r.keeps(token)) return;
+            if (WIDE && c != at) put();
+            at = c;
+            mine += w;
+            if (!WIDE) put();
         });
+        put();
         __syncthreads();
     };
     if (listed) {
