@@ -23,7 +23,8 @@
 //    76 us; by a scan of the row 84), the place among them is found digit by digit of the
 //    logits' keys, the chunks' kept weights say which chunk holds the token, and its
 //    logits are gone over once more.  Bins of more than 6144 tokens (thousands of equal
-//    logits, a very high temperature) are not kept: the row is read for every digit.
+//    logits, a very high temperature) are not kept: the row is read for every digit, of
+//    11 bits there (one row of 151937 equal logits 400 us; of 8 bits 730).
 // Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
 // the row's largest.
 #include "kq_step.h"
@@ -822,8 +823,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, which hold them whole; else of the top's, and finer by the bits that the
     // sum of so many of at most 2^36 leaves of 63.
-    const int base = one ? r.octaves(low) : 0, summed = by_k ? min((int)gathered, top_k) : (int)gathered;
-    int finer = finer_for(listed ? LIST : summed);
+    const int base = one ? r.octaves(low) : 0;
+    int finer = finer_for(listed ? LIST : (int)gathered);
     u64 least = 0;                                // top_k and top_p keep the tokens from here on
     // each(f): f(token, weight()) for every gathered token; wide: from the row
     auto places = [&](auto &&each, auto wide) {
@@ -832,19 +833,21 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
         if (by_k && total >= top_k) least = cut<false, WIDE>(m, each, lowest, top, (u64)top_k);
         u64 sum = one && low < BINS - 1 ? m.weight[low] << finer : 0;
-        if (by_k && (WIDE || by_p)) {
-            auto all = [&] {
-                u64 mine = 0;
-                each([&](u64 token, auto &&weight) { mine += token >= least ? weight() : 0; });
-                return block_sum(m, mine);
-            };
-            sum = all();
-            if (WIDE && sum) {
-                // (many tokens may weigh little together: as fine as their sum lets)
-                const int more = min(__builtin_clzll(sum) - 1, FINEST - finer);
-                finer += max(more, 0);
-                if (more > 0 && by_p) sum = all();
-            }
+        if (by_k && WIDE) {
+            // (many tokens may weigh little together: as fine as their sum lets)
+            finer = FINEST;
+            unsigned __int128 mine = 0;
+            each([&](u64 token, auto &&weight) {
+                if (token >= least) mine += weight();
+            });
+            const u64 low48 = block_sum(m, (u64)mine & ((1ull << 48) - 1)), above = block_sum(m, (u64)(mine >> 48)) + (low48 >> 48);
+            const int drop = max(48 + 64 - (above ? __builtin_clzll(above) : 64) - 63, 0);
+            finer -= drop;
+            sum = (u64)(((unsigned __int128)above << 48 | (low48 & ((1ull << 48) - 1))) >> drop);
+        } else if (by_k && by_p) {
+            u64 mine = 0;
+            each([&](u64 token, auto &&weight) { mine += token >= least ? weight() : 0; });
+            sum = block_sum(m, mine);
         }
         if (by_p && (by_k || low == m.low)) {
             // of what top_k leaves; in the one bin that decides, what the bins above it leave
