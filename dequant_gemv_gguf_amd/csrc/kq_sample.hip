@@ -433,7 +433,7 @@ struct Row {
     Scale s;
     u64 best;               // the first token of the order
     double from;            // its bin
-    int V, phase;           // phase: from mod OCTAVE
+    int phase;              // from mod OCTAVE
     double least;           // min_p: the least weight kept
     // bin b (downwards from the top's) is this many octaves below the top's octave
     __device__ __forceinline__ int octaves(int b) const { return (b + OCTAVE - 1 - phase) >> 3; }
@@ -441,8 +441,7 @@ struct Row {
         if (x == logit_of((u32)(best >> 32))) return 0;
         return (int)fmin(from - s.bin(x), (double)BINS);
     }
-    // in units of the top octave's mantissas
-    // (0 past the bin `last`, at most BINS - 2)
+    // in units of the top octave's mantissas; 0 past the bin `last`, at most BINS - 2
     __device__ __forceinline__ double weight(float x, int last) const {
         const int b = bin(x);
         const double w = ldexp(s.mantissa_d(x, (phase - b) & (OCTAVE - 1)) - 0x1p52, -octaves(b));
@@ -632,7 +631,6 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     r.l = a.logits + row * a.ld;
     r.s = scale_of(t, m.steps);
     r.best = best;
-    r.V = a.V;
     const float most = logit_of((u32)(best >> 32));
     r.from = r.s.top_bin(most);
     r.phase = phase_of(r.from);
