@@ -643,19 +643,21 @@ def _step_call(fn, f, stream, tensors, dtypes, strides, struct, args):
 
 
 def kqstep_norm(T, heads, n, x, ldx, add, ldadd, sum, ldsum, weight, eps, y, ldy, y8=None, stream=None):
-    # (a small norm takes 2 us on the GPU: what most calls are, fp32 tensors of one device with whole rows, is looked over at once)
+    # (a small norm takes 2 us on the GPU: what most calls are, fp32 tensors of one device with whole rows, is looked over here, one
+    # after the other: 2.2 us with the call's own 0.6)
     if _torch_c is None:
         _load_torch()
-    C = (_lib or lib()).kqstep_norm
-    given = [t for t in (x, add, sum, weight, y) if t is not None]
-    count = len(given)
+    C, f = (_lib or lib()).kqstep_norm, _float32
     try:
         device = x.get_device()
-        plain = (device >= 0 and list(map(_get_device, given)).count(device) == count and list(map(_dtype, given)).count(_float32) == count and
-                 (list(map(_is_contiguous, given)).count(True) == count or
-                  ((weight is None or weight.is_contiguous()) and
-                   all([t is None or t.is_contiguous() or (t.dim() == 2 and t.stride() == (ld, 1))
-                        for t, ld in ((x, ldx), (add, ldadd), (sum, ldsum), (y, ldy))]))) and
+        plain = (device >= 0 and x.dtype is f and (x.is_contiguous() or (x.dim() == 2 and x.stride() == (ldx, 1))) and
+                 (add is None or (add.get_device() == device and add.dtype is f and
+                                  (add.is_contiguous() or (add.dim() == 2 and add.stride() == (ldadd, 1))))) and
+                 (sum is None or (sum.get_device() == device and sum.dtype is f and
+                                  (sum.is_contiguous() or (sum.dim() == 2 and sum.stride() == (ldsum, 1))))) and
+                 (weight is None or (weight.get_device() == device and weight.dtype is f and weight.is_contiguous())) and
+                 (y is None or (y.get_device() == device and y.dtype is f and
+                                (y.is_contiguous() or (y.dim() == 2 and y.stride() == (ldy, 1))))) and
                  (y8 is None or (y8.get_device() == device and y8.is_contiguous())))
     except (AttributeError, TypeError):                # not all are tensors
         plain = False
@@ -669,7 +671,6 @@ def kqstep_norm(T, heads, n, x, ldx, add, ldadd, sum, ldsum, weight, eps, y, ldy
                None if weight is None else weight.data_ptr(), eps, None if y is None else y.data_ptr(), ldy,
                None if y8 is None else y8.data_ptr(), stream))
         return
-    f = _float32
     _step_call("kqstep_norm", C, stream, (x, add, sum, weight, y, y8), [f, f, f, f, f], (ldx, ldadd, ldsum, None, ldy, None), None,
                lambda a, s: (T, heads, n, a[0], ldx, a[1], ldadd, a[2], ldsum, a[3], eps, a[4], ldy, a[5], s))
 
