@@ -452,11 +452,12 @@ struct Row {
     __device__ __forceinline__ bool keeps(u64 token) const {
         return !(least > 0.0) || token == best || weight(logit_of((u32)(token >> 32)), BINS - 2) >= least;
     }
-    // as an integer, in units of the mantissas `base` octaves below, 2^finer to one
+    // as an integer, in units of the mantissas `base` octaves below, 2^finer to one; at
+    // least 1 (a u of 0 takes the first token that is kept, however little it weighs)
     __device__ __forceinline__ u64 integer(u64 token, int finer, int base) const {
         const float x = logit_of((u32)(token >> 32));
-        const int b = bin(x), down = octaves(b) - base;
-        return b < BINS - 1 && down < 64 ? (mantissa(x, b) << finer) >> down : 0;
+        const int b = bin(x), down = min(octaves(b) - base, 63);
+        return b < BINS - 1 ? max((mantissa(x, b) << finer) >> down, (u64)1) : 0;
     }
 };
 
@@ -1026,7 +1027,63 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
     }
     __syncthreads();
-    // its token
+    // Its token.  Where its chunk keeps few down to bin `low`, these alone, by their
+    // places' upper bits and then one by one; else all of the chunk's.
+    const int64_t chosen = chunk0 + m.n;
+    const int below = low - m.off[m.n], kept_n = low < BINS - 1 && below >= 0 ? a.upto[chosen * BINS + below] : CHUNK;
+    constexpr int EVERY = 2, PIECES = 256, PIECE = CHUNK / PIECES;
+    if (kept_n <= EVERY * ROW_THREADS) {
+        constexpr int FINER = finer_for(EVERY * ROW_THREADS);
+        const int top = r.octaves(m.off[m.n]);    // (of the chunk's own first token)
+        int at[EVERY];
+        u64 w[EVERY];
+#pragma unroll
+        for (int j = 0; j < EVERY; ++j) at[j] = a.order[chosen * CHUNK + min(tid + j * ROW_THREADS, kept_n - 1)];
+#pragma unroll
+        for (int j = 0; j < EVERY; ++j) {
+            w[j] = 0;
+            if (64 * wave + j * ROW_THREADS >= kept_n) continue;
+            const int i = m.n * CHUNK + at[j];
+            const u64 token = token_of(key_of(r.l[i]), i);
+            if (tid + j * ROW_THREADS < kept_n && token >= least && r.keeps(token)) w[j] = r.integer(token, FINER, top);
+            if (w[j]) atomicAdd((unsigned long long *)&m.digit_weight[at[j] / PIECE], w[j]);
+        }
+        if (tid < PIECE) m.digit_weight[PIECES + tid] = 0;
+        __syncthreads();
+        if (wave == 0) {
+            u64 d[PIECES / 64], s = 0;
+#pragma unroll
+            for (int i = 0; i < PIECES / 64; ++i) s += d[i] = m.digit_weight[PIECES / 64 * lane + i];
+            const u64 upto = wave_scan(s), all = last_lane(upto);
+            u64 past = m.picked[0] > 0.0 ? (u64)fmin(ldexp(m.picked[0], FINER + top), 0x1p63) : 0;
+            past = past < all ? past : all - 1;
+            const u64 reach = __ballot(all && upto > past);
+            if (lane == (reach ? __builtin_ctzll(reach) : 0)) {
+                u64 b = upto - s;
+                int i = 0;
+                for (; i < PIECES / 64 - 1 && b + d[i] <= past; ++i) b += d[i];
+                m.found[0] = all ? (u64)(PIECES / 64 * lane + i) : PIECES;
+                m.found[1] = past - b;
+            }
+        }
+        __syncthreads();
+        const int piece = (int)m.found[0];
+#pragma unroll
+        for (int j = 0; j < EVERY; ++j)
+            if (w[j] && at[j] / PIECE == piece) m.digit_weight[PIECES + at[j] % PIECE] = w[j];
+        __syncthreads();
+        if (wave == 0) {
+            const u64 mine = lane < PIECE ? m.digit_weight[PIECES + lane] : 0, upto = wave_scan(mine);
+            const u64 hit = __ballot(mine && upto > m.found[1]);
+            // (weights that differ by a rounding left none: the row's first)
+            if (lane == (hit ? __builtin_ctzll(hit) : 0)) {
+                const int token = hit ? m.n * CHUNK + piece * PIECE + lane : (int)~(u32)best;
+                a.tokens[row] = token;
+                if (a.probs) a.probs[row] = (float)(r.weight(r.l[token], BINS - 2) / m.picked[1]);
+            }
+        }
+        return;
+    }
     constexpr int EACH = CHUNK / ROW_THREADS;
     const int first = m.n * CHUNK + EACH * tid;
     const double at = m.picked[0], sum = m.picked[1];

@@ -168,6 +168,22 @@ def test_settings_out_of_their_ranges():
     assert list(edge) == [0, 0, 0, last, last]
 
 
+@pytest.mark.parametrize("V,k,p", [(100, 0, 1.0), (100, 60, 1.0), (100, 0, 1 - 2.0 ** -24), (9000, 0, 1.0), (9000, 5000, 1.0), (9000, 0, 1 - 2.0 ** -24),
+                                   (30000, 400, 1.0), (30000, 20000, 1.0)])
+def test_u_of_zero_takes_the_first_token_kept(V, k, p):
+    """However little it weighs, down to 64 octaves below the largest."""
+    rng = np.random.default_rng(V + k)
+    octaves = [1, 20, 40, 50, 55, 58, 60, 61, 62]
+    M = len(octaves)
+    l = np.full((M, V), -np.inf, np.float32)
+    for i, o in enumerate(octaves):
+        there = rng.permutation(V - 2)[:min(V - 2, 300 if k < 1000 else 15000)] + 2
+        l[i, there] = rng.uniform(-2, 0, len(there))
+        l[i, V - 1] = 0
+        l[i, 1] = -o * np.log(2)
+    check(l, t=np.ones(M), k=None if not k else np.full(M, k), p=None if p == 1 else np.full(M, p), u=np.zeros(M))
+
+
 @pytest.mark.parametrize("V", [40, 3000, 30000])
 def test_min_p_far_below_the_largest(V):
     """Borders 20 to 30 octaves down, with logits a few 2^-20 of a weight to each side of them: what is kept shows in the probability of
