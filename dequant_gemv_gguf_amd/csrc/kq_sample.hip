@@ -734,7 +734,9 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             one = true;
         }
     }
-    if (low < BINS - 1 && m.counts[low] <= FEW) {
+    // (the last bin's tokens weigh nothing: what ends there leaves all the others)
+    if (low == BINS - 1) low = BINS - 2;
+    if (low < BINS && m.counts[low] <= FEW) {
         // Few tokens, all of them in the chunks' lists: each with those before it (4 threads
         // a token, a quarter of the others each).
         for (int c = wave; c < a.chunks; c += ROW_WAVES) {
@@ -811,14 +813,12 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     // what can lie in these bins, and a little more
     float lo = -3.402823466e38f, hi = __builtin_inff();
     if (r.s.eighths > 0.0 && most < __builtin_inff()) {
-        if (low < BINS - 1) {
-            const double x = (r.from - low) / r.s.eighths;
-            lo = fmaxf(lo, (float)(x - fabs(x) * 0x1p-22) - 1e-37f);
-        }
+        const double x = (r.from - low) / r.s.eighths;
+        lo = fmaxf(lo, (float)(x - fabs(x) * 0x1p-22) - 1e-37f);
         const double y = (r.from - high + 1) / r.s.eighths;
         hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
     }
-    const bool listed = scan && low < BINS - 1 && gathered <= LIST;
+    const bool listed = scan && gathered <= LIST;
     // Weights of gathered tokens as integers: with one bin in units of its octave's
     // mantissas, which hold them whole; else of the top's, and finer by the bits that the
     // sum of so many of at most 2^36 leaves of 63.
@@ -830,8 +830,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         constexpr bool WIDE = decltype(wide)::value;
         // (where the tokens of these bins lie)
         const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
-        if (by_k && total >= top_k) least = cut<false, WIDE>(m, each, lowest, top, (u64)top_k);
-        u64 sum = one && low < BINS - 1 ? m.weight[low] << finer : 0;
+        if (by_k && (int)m.counts[low] >= top_k) least = cut<false, WIDE>(m, each, lowest, top, (u64)top_k);
+        u64 sum = one ? m.weight[low] << finer : 0;
         if (by_k && WIDE) {
             // (many tokens may weigh little together: as fine as their sum lets)
             finer = FINEST;
@@ -947,7 +947,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
                 now = next;
             }
         };
-        if (one && low < BINS - 1) {
+        if (one) {
             // one bin: its mantissas are the weights
             const double bin = r.from - low;
             const int of_octave = (r.phase - low) & (OCTAVE - 1);
@@ -959,8 +959,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         } else {
             places([&](auto &&f) {
                 row([&](float x, u64 token) {
-                    // (with top_k a token a rounding past bin `low` is past the last one kept;
-                    // else this is the last bin, whose weights are none)
+                    // (a token a rounding past bin `low` is past the last one that top_k keeps)
                     f(token, [&] { return r.integer(token, finer, base); });
                 });
             }, std::true_type());
@@ -1032,7 +1031,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     // rows of 128256 22 us, with all of the chunk's 23.4; up to a quarter of them 8 rows
     // are even, 256 of 151937 76.3, up to half 75.5, up to three quarters 75.6).
     const int64_t chosen = chunk0 + m.n;
-    const int below = low - m.off[m.n], kept_n = low < BINS - 1 && below >= 0 ? a.upto[chosen * BINS + below] : CHUNK;
+    const int below = low - m.off[m.n], kept_n = scan && below >= 0 ? a.upto[chosen * BINS + below] : CHUNK;
     constexpr int EVERY = 4, PIECES = 256, PIECE = CHUNK / PIECES;
     if (kept_n <= EVERY * ROW_THREADS) {
         constexpr int FINER = finer_for(EVERY * ROW_THREADS);
