@@ -187,3 +187,32 @@ def test_two_steps_on_two_streams():
     torch.cuda.synchronize()
     for x, y in zip(want, a.outputs() + b.outputs()):
         assert torch.equal(x, y)
+
+
+def test_two_captured_steps_share_workspaces():
+    """Replayed in turn on one stream: a workspace keeps nothing between calls."""
+    a, b = Step(8), Step(3)
+    assert all(x >= y for x, y in zip(a.sizes, b.sizes))
+    b.ws, b.sizes = a.ws, a.sizes
+    graphs = []
+    for s in (a, b):
+        s.run()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.run()
+        graphs.append(g)
+    want = []
+    for s in (a, b):
+        s.run()
+        want.append(s.outputs())
+    for i in range(6):
+        for s in (a, b):
+            for t in [s.y, s.logits, s.probs] + [x["x"] for x in s.b]:
+                t.fill_(float("nan"))
+        for j in ((0, 1) if i % 2 else (1, 0, 1)):
+            graphs[j].replay()
+        torch.cuda.synchronize()
+        for s, w in zip((a, b), want):
+            for x, y in zip(s.outputs(), w):
+                assert torch.equal(x, y), i
