@@ -1136,7 +1136,13 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     if (any && lane == 63 - __builtin_clzll(any)) atomicMax(&m.high, last);
     __syncthreads();
     token = m.low < a.V ? m.low : m.high;
-    if (token < 0 && tid == 0) token = (int)~(u32)best;      // (weights that differ by a rounding left none)
+    if (token < 0) {                              // (weights that differ by a rounding left none: the row's first)
+        if (tid == 0) {
+            a.tokens[row] = best_i;
+            if (a.probs) a.probs[row] = (float)(r.weight(most, 0) / sum);
+        }
+        return;
+    }
     if (token >= first && token < first + EACH) {
         double p = 0.0;
 #pragma unroll

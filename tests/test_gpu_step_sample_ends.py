@@ -1,0 +1,59 @@
+"""GPU: kqstep_sample where its settings and logits are at their ends: min_p that no
+weight reaches, filters over thousands of tokens, logits far from zero at low
+temperatures.  Outputs hold values beforehand that no row may keep."""
+import numpy as np
+import pytest
+
+import step_ref
+
+torch = pytest.importorskip("torch")
+import dequant_gemv_gguf_amd as kq  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def call(l, t=None, k=None, p=None, mp=None, u=0.5):
+    """l [M][V]; settings: one value, or one a row -> tokens, probabilities."""
+    M, V = l.shape
+    each = lambda v, dtype: None if v is None else torch.from_numpy(np.broadcast_to(np.asarray(v, dtype), M).copy()).cuda()  # noqa: E731
+    n = kq.kqstep_sample_workspace_bytes(M, V)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    tokens, probs = torch.full((M,), -9, dtype=torch.int32, device="cuda"), torch.full((M,), 9.0, device="cuda")
+    kq.kqstep_sample(M, V, torch.from_numpy(np.ascontiguousarray(l)).cuda(), V, each(t, np.float32), each(k, np.int32), each(p, np.float32),
+                     each(mp, np.float32), each(u, np.float32), tokens, probs, ws, n)
+    return tokens.cpu().numpy(), probs.cpu().numpy()
+
+
+def check(l, t=None, k=None, p=None, mp=None, u=0.5):
+    M = len(l)
+    tokens, probs = call(l, t, k, p, mp, u)
+    at = lambda v, i, none: none if v is None else np.broadcast_to(v, M)[i]  # noqa: E731
+    for i in range(M):
+        want, prob, kept = step_ref.sample(l[i], at(t, i, 1.0), at(k, i, 0), at(p, i, 2.0), at(mp, i, 0.0), at(u, i, 0.5))
+        assert tokens[i] == want, (i, tokens[i], want, kept)
+        # rounded once (2^-24); weights, and so their sum, within half a step of 36 bits of mantissa (2^-36) and the series' 2^-41 of
+        # themselves, or left out 2^-63 below the largest: both in a quotient, below 2^-34 of it and 2^-62 a token
+        assert abs(probs[i] - prob) <= prob * (2.0 ** -24 + 2.0 ** -34) + kept * 2.0 ** -62, (i, probs[i], prob)
+    return tokens, probs
+
+
+def nearly_flat(rng, M, V):
+    """All weights alike, the first token of the order in the last chunk."""
+    l = (0.1 * rng.standard_normal((M, V))).astype(np.float32)
+    l[:, V - 1000] = 1
+    return l
+
+
+@pytest.mark.parametrize("p", [0.5, 0.999])
+def test_a_row_without_a_weight_of_min_p_gets_its_first_token(p):
+    """Wherever u points: into chunks of thousands of tokens, none of which min_p leaves."""
+    l = nearly_flat(np.random.default_rng(1), 9, 20000)
+    tokens, probs = call(l, p=p, mp=INF, u=np.arange(9) / 9)
+    assert (tokens == 19000).all() and (probs > 0).all() and (probs <= 1).all(), (tokens, probs)
