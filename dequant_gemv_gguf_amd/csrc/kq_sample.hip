@@ -728,7 +728,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         // the bin of the least weight; those above it are kept whole
         const double octave = floor(log2(r.least)) - 35.0, part = floor(OCTAVE * (log2(r.least) - 35.0 - octave));
         const double b = r.phase - (OCTAVE * octave + part);
-        const int edge = b < 0.0 ? 0 : b < BINS ? (int)b : BINS - 1;
+        // (an infinite min_p makes b a NaN: no weight but the first token's stays)
+        const int edge = !(b >= 0.0) ? 0 : b < BINS ? (int)b : BINS - 1;
         if (edge <= low) {
             low = edge;
             one = true;

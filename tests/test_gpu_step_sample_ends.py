@@ -57,3 +57,17 @@ def test_a_row_without_a_weight_of_min_p_gets_its_first_token(p):
     l = nearly_flat(np.random.default_rng(1), 9, 20000)
     tokens, probs = call(l, p=p, mp=INF, u=np.arange(9) / 9)
     assert (tokens == 19000).all() and (probs > 0).all() and (probs <= 1).all(), (tokens, probs)
+
+
+@pytest.mark.parametrize("mp", [INF, 5.0, NAN, -1.0])
+@pytest.mark.parametrize("V", [300, 6000, 20000])
+def test_min_p_out_of_its_range(V, mp):
+    """What no weight reaches leaves the first token alone, with a probability of 1; what is no number filters nothing."""
+    rng = np.random.default_rng(V)
+    M = 8
+    flat = nearly_flat(rng, M, max(V, 1100))[:, -V:]
+    for l in (flat, np.zeros((M, V), np.float32), np.full((M, V), np.float32(INF)), np.where(flat < 0, flat, np.float32(7))):
+        for k, p in ((None, None), (None, 0.3), (None, 0.999), (200, None), (200, 0.9)) + (((3000, 0.9),) if V == 6000 else ()):
+            tokens, probs = check(l, k=k, p=p, mp=mp, u=(np.arange(M) + 0.3) / M)
+            if mp > 0:
+                assert np.array_equal(tokens, l.argmax(1)) and (probs == 1).all()
