@@ -484,6 +484,7 @@ __device__ __forceinline__ u64 cut(RowSpace &m, Each &&each, u64 from, u64 top, 
         auto larger = [](u32 p, u32 q) { return max(p, q); };
         most = wave_all(most, larger);
         least = wave_all(least, larger);
+        __syncthreads();                    // (waves may still read the last block_sum's there)
         if (lane == 0) m.waves[tid >> 6] = (u64)most << 32 | least;
         __syncthreads();
         for (int w = 0; w < ROW_WAVES; ++w) {

@@ -71,3 +71,17 @@ def test_min_p_out_of_its_range(V, mp):
             tokens, probs = check(l, k=k, p=p, mp=mp, u=(np.arange(M) + 0.3) / M)
             if mp > 0:
                 assert np.array_equal(tokens, l.argmax(1)) and (probs == 1).all()
+
+
+@pytest.mark.parametrize("V,k,equal", [(60000, 30000, False), (60000, 59999, False), (151937, 50000, False), (40000, 5000, True), (40000, 39000, True)])
+def test_both_filters_over_more_tokens_than_are_kept(V, k, equal):
+    """top_k, the sum of what it leaves and top_p, each a reduction over the row; the same bits in every run."""
+    rng = np.random.default_rng([V, k])
+    M = 6
+    l = np.zeros((M, V), np.float32) if equal else (2.5 * rng.standard_normal((M, V))).astype(np.float32)
+    kw = dict(t=rng.choice([0.8, 1.0, 3.0], M).astype(np.float32), k=k, p=np.array([0.1, 0.5, 0.9, 0.95, 0.99, 0.999], np.float32),
+              mp=np.array([0, 0, 0, 0, 1e-4, INF], np.float32), u=rng.random(M).astype(np.float32))
+    tokens, probs = check(l, **kw)
+    for _ in range(5):
+        again = call(l, **kw)
+        assert np.array_equal(again[0], tokens) and np.array_equal(again[1], probs)
