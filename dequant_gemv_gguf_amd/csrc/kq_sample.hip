@@ -45,7 +45,7 @@ constexpr int NEAR = 256;                         // tokens of a chunk's list
 constexpr int SPARSE = 1024;                      // tokens of a chunk that can matter, where those are put together first
 constexpr int FEW = 256;                          // tokens that are compared with each other
 constexpr int SLICE = 16384;                      // chunks of a launch, or one row: 390 MB of workspace
-static_assert((u64)CHUNK << 36 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
+static_assert((u64)CHUNK << 37 <= 1ull << COUNT_SHIFT, "a chunk's weights fit a bin's sum");
 
 struct Sample {
     const float *logits, *temperature, *top_p, *min_p, *u;
@@ -77,29 +77,35 @@ __device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 
 
 // Where a logit's weight lies: the bin (counted upwards), its octave, and the
 // mantissa, 2^35 .. 2^36.  (A bin is the nearest whole number to what is 1/2 less than
-// the eighths of an octave: what is left, at most 1/2 either way, the series takes.)
+// the eighths of an octave.)  What is left of the logit is one product and sum, so that
+// it is off by 2^-54 of a bin however far from 0 the logits lie (as the difference of the
+// rounded eighths and the bin it was off by 2^-54 of the eighths: a weight by 2^-27 at
+// l / t of 2^27).
 struct Scale {
-    double eighths;         // of an octave, per logit: 8 log2(e) / t
-    const double *steps;    // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
+    double eighths, quarters;   // of an octave, per logit: 8 log2(e) / t, and half of it
+    const double *steps;        // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
     // (an infinite logit's mantissa is that of the largest number; its bin is given by
     // what it is compared with)
-    __device__ __forceinline__ double at(float l) const {
-        return fma((double)__builtin_amdgcn_fmed3f(l, -3.402823466e38f, 3.402823466e38f), eighths, -0.5);
+    static __device__ __forceinline__ double finite(float l) {
+        return (double)__builtin_amdgcn_fmed3f(l, -3.402823466e38f, 3.402823466e38f);
     }
-    __device__ __forceinline__ double bin(float l) const { return rint(at(l)); }
+    __device__ __forceinline__ double bin(float l) const { return rint(fma(finite(l), eighths, -0.5)); }
     // that of a first token: an infinite one lies above all others
     __device__ __forceinline__ double top_bin(float l) const { return l < __builtin_inff() ? bin(l) : __builtin_inf(); }
     // 2^52 more, in whose low bits it is rounded to an integer.  `of_octave`: the bin's
     // place in its octave
     __device__ __forceinline__ double mantissa_d(float l, int of_octave) const {
-        const double y = at(l), z = y - rint(y);
-        // 2^(z / 8) by the polynomial through six Chebyshev nodes: off by 2^-41
-        double p = 0x1.5d8dfde822453p-25;
-        p = fma(p, z, 0x1.3b324944cbf5dp-19);
-        p = fma(p, z, 0x1.c6b08d5e4bb3bp-14);
-        p = fma(p, z, 0x1.ebfbdfcabe822p-9);
-        p = fma(p, z, 0x1.62e42fefa3aefp-4);
-        p = fma(p, z, 0x1.000000000050cp+0);
+        // half of what is left, from the bin's middle at 1/2: 1/4 .. 3/4, and a rounding of
+        // the bin more.  (Past 2^35 bins only equal logits are in one, and any value does:
+        // 0 .. 1, which costs no instruction and lets sums be 2^(1/16) as large.)
+        const double y = fmin(fmax(fma(finite(l), quarters, fma(bin(l), -0.5, 0.25)), 0.0), 1.0);
+        // 2^((2 y - 1) / 8) by the polynomial through six Chebyshev nodes: off by 2^-41
+        double p = 0x1.5d8dfde822453p-20;
+        p = fma(p, y, 0x1.1fe3316ea9487p-15);
+        p = fma(p, y, 0x1.a0ff35b3145fdp-11);
+        p = fma(p, y, 0x1.c326766be389ep-7);
+        p = fma(p, y, 0x1.456fd368e4058p-3);
+        p = fma(p, y, 0x1.d5818dcc704b1p-1);
         return fma(p, steps[of_octave], 0x1p52);
     }
     // `plus` 2^32 more
@@ -109,7 +115,8 @@ struct Scale {
     }
 };
 __device__ __forceinline__ Scale scale_of(float t, const double *steps) {
-    return Scale{t < __builtin_inff() ? 8.0 * 1.4426950408889634 / (double)t : 0.0, steps};
+    const double quarters = t < __builtin_inff() ? 4.0 * 1.4426950408889634 / (double)t : 0.0;
+    return Scale{2.0 * quarters, quarters, steps};
 }
 __device__ const double STEPS[OCTAVE] = {0x1.0b5586cf9890fp+35, 0x1.2387a6e756238p+35, 0x1.3dea64c123422p+35, 0x1.5ab07dd485429p+35,
                                          0x1.7a11473eb0187p+35, 0x1.9c49182a3f090p+35, 0x1.c199bdd85529cp+35, 0x1.ea4afa2a490dap+35};
@@ -204,7 +211,7 @@ __device__ __forceinline__ int room(int *count, int n) {
 // Whether top_k limits the row (the same in both kernels).
 __device__ __forceinline__ bool limited(int top_k, int V) { return top_k > 0 && top_k < V; }
 
-// Bound: its arithmetic, some 30 instructions a token whose weight is asked for, 14 of
+// Bound: its arithmetic, some 30 instructions a token whose weight is asked for, 15 of
 // them in 64 bits (256 rows of 151937 that all sum weights: 58 us, without the weights
 // 44, greedy 23).  top_k up to the threads of a work-group, and min_p alone, first take
 // out the tokens that cannot matter and count the others, put together in LDS (256 rows
@@ -1058,7 +1065,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
 #pragma unroll
             for (int i = 0; i < PIECES / 64; ++i) s += d[i] = m.digit_weight[PIECES / 64 * lane + i];
             const u64 upto = wave_scan(s), all = last_lane(upto);
-            u64 past = m.picked[0] > 0.0 ? (u64)fmin(ldexp(m.picked[0], FINER + top), 0x1p63) : 0;
+            u64 past = m.picked[0] > 0.0 ? (u64)fmin(ldexp(m.picked[0], FINER + top), 0x1.fffffffffffffp63) : 0;
             past = past < all ? past : all - 1;
             const u64 reach = __ballot(all && upto > past);
             if (lane == (reach ? __builtin_ctzll(reach) : 0)) {

@@ -150,9 +150,10 @@ size_t kqstep_sample_workspace_bytes(int M, int64_t V);
  *   tokens       [M] int32
  *   probs        [M] fp32 the token's part of the kept weight, or NULL
  *   workspace    kqstep_sample_workspace_bytes
- * Weights are computed in 64 bits and rounded to 36 of mantissa; those 64 octaves
- * below the row's largest count as 0.  They are summed as integers, and such sums
- * in 64 bits in a fixed order: the kept weight is off by less than 2^-35 of itself.
+ * Weights are computed in 64 bits and rounded to 36 of mantissa, however far from 0
+ * the logits lie; those 64 octaves below the row's largest count as 0 (from 63 3/4
+ * on some of them).  They are summed as integers, and such sums in 64 bits in a fixed
+ * order: the kept weight is off by less than 2^-35 of itself.
  * 0 <= M <= 65536, 1 <= V <= 2^20. */
 int kqstep_sample(int M, int64_t V, const float *logits, int64_t ld, const float *temperature, const int32_t *top_k,
                   const float *top_p, const float *min_p, const float *u, int32_t *tokens, float *probs, void *workspace,

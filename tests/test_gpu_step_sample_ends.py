@@ -85,3 +85,55 @@ def test_both_filters_over_more_tokens_than_are_kept(V, k, equal):
     for _ in range(5):
         again = call(l, **kw)
         assert np.array_equal(again[0], tokens) and np.array_equal(again[1], probs)
+
+
+@pytest.mark.parametrize("top", [16.0, -11.7, 1e5, 3e-8, -2.0 ** 60, 1e30])
+def test_probabilities_of_logits_far_from_zero(top):
+    """Two tokens a step or a few apart, the lesser one taken, at temperatures that put its probability just above a power of two, where
+    half a step of fp32 is the whole 2^-24 of the tolerance: an error of 2^-28 of a weight shows in one row of a hundred."""
+    rng = np.random.default_rng(int(abs(np.log2(abs(top)))))
+    M = 1000
+    top = np.float32(top)
+    step = float(abs(np.float64(top) - np.float64(np.nextafter(top, np.float32(-INF)))))
+    apart = rng.integers(1, 4, M) * step
+    l = np.stack([np.float64(top) - apart, np.full(M, np.float64(top))], 1).astype(np.float32)
+    assert np.array_equal(l[:, 1].astype(np.float64) - l[:, 0], apart)
+    prob = 2.0 ** -rng.integers(2, 9, M) * (1 + 2.0 ** -11 * rng.random(M))
+    t = (apart / np.log(1 / prob - 1)).astype(np.float32)
+    tokens, _ = check(l, t=t, u=0.0)
+    assert (tokens == 0).all()
+
+
+def steps_below(rng, M, V, top, steps):
+    """Logits up to `steps` fp32 steps below `top`."""
+    step = abs(np.spacing(np.float32(top))) / (2 if np.log2(abs(top)) % 1 == 0 and top > 0 else 1)
+    return (np.float64(top) - step * rng.integers(0, steps, (M, V))).astype(np.float32), float(step)
+
+
+@pytest.mark.parametrize("top", [16.0, -11.7, 1e5, 3e-8, -2.0 ** 60, 1e30])
+@pytest.mark.parametrize("V,M", [(3, 2000), (40, 300), (3000, 20), (30000, 8)])
+def test_weights_do_not_depend_on_where_the_logits_lie(V, M, top):
+    """Logits a few fp32 steps from each other, at temperatures of the order of a step: l / t goes up to 2^27, the weights' ratios are
+    those of (l - max) / t alone."""
+    rng = np.random.default_rng([V, int(abs(np.log2(abs(top))))])
+    l, step = steps_below(rng, M, V, top, 12)
+    t = (step * rng.uniform(0.3, 3.0, M)).astype(np.float32)
+    u = rng.random(M).astype(np.float32)
+    check(l, t=t, u=u)
+    check(l, t=t, u=u, k=max(1, V // 3), p=0.9)
+    check(l, t=t, u=u, mp=0.01)
+
+
+@pytest.mark.parametrize("V,part", [(7, 0.6), (300, 0.6), (8192, 0.49), (9000, 0.6), (30000, 0.6)])
+def test_largest_logits_at_low_temperatures(V, part):
+    """Equal ones share the row, whatever their size; all others weigh nothing."""
+    M = 8
+    rng = np.random.default_rng(V)
+    tops = np.array([3.4e38, 3.4e38, -3.4e38, 1e30, -1e30, 1e15, -1e10, 1e-3], np.float32)
+    l = np.where(rng.random((M, V)) < part, tops[:, None], np.nextafter(tops, np.float32(-INF))[:, None]).astype(np.float32)
+    l[:, 1] = tops
+    l[:, 2] = -INF
+    t = np.array([1e-30, 1, 1e-30, 1e-10, 1e-20, 1e-3, 1e-3, 1e-14], np.float32)
+    for kw in ({}, dict(k=max(1, V // 2)), dict(p=0.5), dict(mp=0.9), dict(k=max(1, V // 4), p=0.7, mp=0.1)):
+        check(l, t=t, u=(rng.integers(0, 1000, M) + 0.37) / 1000, **kw)
+        check(l, t=t, u=0.99937, **kw)
