@@ -736,8 +736,9 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         // the bin of the least weight; those above it are kept whole
         const double octave = floor(log2(r.least)) - 35.0, part = floor(OCTAVE * (log2(r.least) - 35.0 - octave));
         const double b = r.phase - (OCTAVE * octave + part);
-        // (an infinite min_p makes b a NaN: no weight but the first token's stays)
-        const int edge = !(b >= 0.0) ? 0 : b < BINS ? (int)b : BINS - 1;
+        // (equal logits past all bins may weigh a little more than their bin: none of them but
+        // the first is left above 1, nor is one where an infinite min_p makes b a NaN)
+        const int edge = min_p > 1.f || !(b >= 0.0) ? 0 : b < BINS ? (int)b : BINS - 1;
         if (edge <= low) {
             low = edge;
             one = true;

@@ -134,6 +134,6 @@ def test_largest_logits_at_low_temperatures(V, part):
     l[:, 1] = tops
     l[:, 2] = -INF
     t = np.array([1e-30, 1, 1e-30, 1e-10, 1e-20, 1e-3, 1e-3, 1e-14], np.float32)
-    for kw in ({}, dict(k=max(1, V // 2)), dict(p=0.5), dict(mp=0.9), dict(k=max(1, V // 4), p=0.7, mp=0.1)):
+    for kw in ({}, dict(k=max(1, V // 2)), dict(p=0.5), dict(mp=0.9), dict(mp=1.0), dict(mp=1.01), dict(k=max(1, V // 4), p=0.7, mp=0.1)):
         check(l, t=t, u=(rng.integers(0, 1000, M) + 0.37) / 1000, **kw)
         check(l, t=t, u=0.99937, **kw)
