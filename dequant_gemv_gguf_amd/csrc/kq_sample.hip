@@ -730,22 +730,28 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
     }
     __syncthreads();
-    int low = m.low;
-    bool one = !by_k && low < BINS;               // the tokens of bin `low` alone decide
+    int low = m.low, high = low;                  // the tokens of bins high .. low decide
     if (!by_k && r.least > 0.0) {
-        // the bin of the least weight; those above it are kept whole
-        const double octave = floor(log2(r.least)) - 35.0, part = floor(OCTAVE * (log2(r.least) - 35.0 - octave));
-        const double b = r.phase - (OCTAVE * octave + part);
-        // (equal logits past all bins may weigh a little more than their bin: none of them but
-        // the first is left above 1, nor is one where an infinite min_p makes b a NaN)
-        const int edge = min_p > 1.f || !(b >= 0.0) ? 0 : b < BINS ? (int)b : BINS - 1;
-        if (edge <= low) {
-            low = edge;
-            one = true;
+        // The bin of the least weight; those above it are kept whole.  A token's bin is that
+        // of its rounded eighths of an octave, off by up to 2^-53 of them, and its weight by
+        // 2^-35: where the least weight is so near to a border, both bins' tokens decide.
+        // (Equal logits past all bins may weigh a little more than their bin: none of them
+        // but the first is left above 1, nor is one where an infinite min_p makes a bin a NaN.)
+        const double at = OCTAVE * (log2(r.least) - 35.0), near = fmin(0x1p-31 + (fabs(r.from) + BINS) * 0x1p-52, 0x1p-8);
+        auto bin_of = [&](double at) {
+            const double b = r.phase - floor(at);
+            return !(b >= 0.0) ? 0 : b < BINS ? (int)b : BINS - 1;
+        };
+        const int first = min_p > 1.f ? 0 : bin_of(at + near), last = min_p > 1.f ? 0 : bin_of(at - near);
+        if (first <= low) {
+            high = first;
+            low = min(low, last);
         }
     }
+    const bool one = !by_k && low < BINS;         // (mostly one bin)
     // (the last bin's tokens weigh nothing: what ends there leaves all the others)
     if (low == BINS - 1) low = BINS - 2;
+    high = by_k ? 0 : min(high, low);
     if (low < BINS && m.counts[low] <= FEW) {
         // Few tokens, all of them in the chunks' lists: each with those before it (4 threads
         // a token, a quarter of the others each).
@@ -817,7 +823,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         }
         return;
     }
-    const int high = by_k ? 0 : low;              // bins high .. low are gathered
+    // bins high .. low are gathered
     const u32 gathered = low < BINS ? m.counts[low] - (high ? m.counts[high - 1] : 0) : 0;
     const bool scan = low < BINS;
     // what can lie in these bins, and a little more
@@ -829,10 +835,10 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         hi = (float)(y + fabs(y) * 0x1p-22) + 1e-37f;
     }
     const bool listed = scan && gathered <= LIST;
-    // Weights of gathered tokens as integers: with one bin in units of its octave's
-    // mantissas, which hold them whole; else of the top's, and finer by the bits that the
-    // sum of so many of at most 2^36 leaves of 63.
-    const int base = one ? r.octaves(low) : 0;
+    // Weights of gathered tokens as integers: with one bin (or two) in units of its octave's
+    // mantissas, which hold them whole (the second's with a bit more); else of the top's,
+    // and finer by the bits that the sum of so many of at most 2^36 leaves of 63.
+    const int base = one ? r.octaves(high) : 0, down = one ? r.octaves(low) - base : 0;
     int finer = finer_for(listed ? LIST : (int)gathered);
     u64 least = 0;                                // top_k and top_p keep the tokens from here on
     // each(f): f(token, weight()) for every gathered token; wide: from the row
@@ -841,7 +847,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         // (where the tokens of these bins lie)
         const u64 lowest = (u64)key_of(lo) << 32, top = min(best, (u64)key_of(hi) << 32 | 0xFFFFFFFF);
         if (by_k && (int)m.counts[low] >= top_k) least = cut<false, WIDE>(m, each, lowest, top, (u64)top_k);
-        u64 sum = one ? m.weight[low] << finer : 0;
+        u64 sum = one ? (m.weight[low] << finer >> down) + (high < low ? m.weight[high] << finer : 0) : 0;
         if (by_k && WIDE) {
             // (many tokens may weigh little together: as fine as their sum lets)
             finer = FINEST;
@@ -859,8 +865,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             sum = block_sum(m, mine);
         }
         if (by_p && (by_k || low == m.low)) {
-            // of what top_k leaves; in the one bin that decides, what the bins above it leave
-            const double want = one ? ldexp(want_p - (low ? m.upto[low - 1] : 0.0), base + finer)
+            // of what top_k leaves; in the bin that decides, what the bins above it leave
+            const double want = one ? ldexp(want_p - (high ? m.upto[high - 1] : 0.0), base + finer)
                                     : (double)(top_p > 0.f ? top_p : 0.f) * (double)sum;
             least = cut<true, WIDE>(m, each, max(least, lowest), top, want > 1.0 ? (want < (double)sum ? (u64)ceil(want) : sum) : 1);
         }
@@ -946,6 +952,22 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
             m.digit_weight[i] = 0;
             m.digit_count[i] = 0;
         }
+        if (one && high < low) {
+            // two bins: their first and last logits
+            u32 first = key_of(lo), last = key_of(fminf(hi, most));
+            for (u32 end = last; first < end;) {
+                const u32 at = first + (end - first) / 2;
+                if (r.bin(logit_of(at)) <= low) end = at;
+                else first = at + 1;
+            }
+            for (u32 from = first; from < last;) {
+                const u32 at = last - (last - from) / 2;
+                if (r.bin(logit_of(at)) >= high) from = at;
+                else last = at - 1;
+            }
+            lo = logit_of(first);
+            hi = logit_of(last);
+        }
         // (the next logits are on their way)
         auto row = [&](auto &&f) {
             f4 now = four(r.l, 4 * tid, a.V);
@@ -957,7 +979,7 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
                 now = next;
             }
         };
-        if (one) {
+        if (one && high == low) {
             // one bin: its mantissas are the weights
             const double bin = r.from - low;
             const int of_octave = (r.phase - low) & (OCTAVE - 1);
@@ -969,14 +991,14 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
         } else {
             places([&](auto &&f) {
                 row([&](float x, u64 token) {
-                    // (a token a rounding past bin `low` is past the last one that top_k keeps)
+                    // (with top_k a token a rounding past bin `low` is past the last one that it keeps)
                     f(token, [&] { return r.integer(token, finer, base); });
                 });
             }, std::true_type());
         }
     }
     // and of the bins above them
-    const int whole = !scan ? BINS : one ? low : 0;
+    const int whole = !scan ? BINS : one ? high : 0;
     for (int c0 = wave; c0 < a.chunks; c0 += 2 * ROW_WAVES) {
         int off[2];
         u64 h[2][BINS / 64];

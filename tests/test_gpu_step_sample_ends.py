@@ -137,3 +137,27 @@ def test_largest_logits_at_low_temperatures(V, part):
     for kw in ({}, dict(k=max(1, V // 2)), dict(p=0.5), dict(mp=0.9), dict(mp=1.0), dict(mp=1.01), dict(k=max(1, V // 4), p=0.7, mp=0.1)):
         check(l, t=t, u=(rng.integers(0, 1000, M) + 0.37) / 1000, **kw)
         check(l, t=t, u=0.99937, **kw)
+
+
+# The largest logit, and a temperature and a min_p at which the next fp32 number below it weighs just that much or a 2^-26 less, and lies
+# within a rounding of its 64-bit eighths of an octave from a multiple of them.
+BORDERS = [(15.999999046325684, 7.434761783997601e-08, 2.6865993731917115e-06), (15.999950408935547, 1.0194688826459242e-07, 8.656463614897802e-05),
+           (15.999944686889648, 7.419148317922009e-08, 2.6150455596507527e-06), (15.999917030334473, 8.416112962095212e-08, 1.1988899132120423e-05),
+           (15.999894142150879, 8.461003631055064e-08, 1.2731785318464972e-05), (15.999892234802246, 1.070541557623983e-07, 0.00013525680697057396),
+           (15.99988079071045, 7.978613325576589e-08, 6.440637662308291e-06), (15.999874114990234, 7.920611722056492e-08, 5.900860287511023e-06),
+           (15.999845504760742, 1.0317498322365282e-07, 9.676058107288554e-05)]
+
+
+@pytest.mark.parametrize("V", [2, 200, 3000, 6001, 40000])
+def test_min_p_of_a_weight_at_the_border_of_an_eighth_of_an_octave(V):
+    """One token above, all others of that weight: kept or not as a whole."""
+    top, t, mp = (np.array(v, np.float32) for v in zip(*BORDERS))
+    l = np.repeat(np.nextafter(top, np.float32(0))[:, None], V, 1)
+    l[:, V // 2] = top
+    for p in (None, 1 - 2.0 ** -20):
+        for u in (0.0, 0.4, 1 - 2.0 ** -24):
+            check(l, t=t, mp=mp, p=p, u=u)
+    check(l, t=t, mp=mp, k=max(1, V - 1), u=0.4)
+    # and a border that top_p reaches inside the same weight
+    share = 1 / (1 + (V - 1) * np.exp((l[:, (V // 2 + 1) % V].astype(np.float64) - top) / t))
+    check(l, t=t, mp=mp, p=(share + 0.37 * (1 - share)).astype(np.float32), u=0.999)
