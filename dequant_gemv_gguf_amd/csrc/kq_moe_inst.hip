@@ -205,9 +205,11 @@ __device__ __forceinline__ Scores scores_of(const Moe &a, const double *l) {
 // The token's experts, by the whole work-group (`waves` of them), into ids[0 .. k);
 // `meanwhile` runs while the logits are on their way.
 // MANY false: up to 256 experts, which are no more than threads.  An expert's place is the
-// number of those that come before it; a thread counts them over a part of the
-// experts.  A key ends in the expert's own number, so that one comparison does: logits
-// that differ by less than 2^-44 of their size count as the same.
+// number of those with greater keys; a thread counts them over a part of the experts.
+// Equal keys share a place, which the lower expert has, and leave one empty behind it:
+// only then are those of the same key in front of each counted too.  (With the expert's
+// number in a key's low bits there are none, but logits that differ by less than 2^-44 of
+// their size counted as the same.)
 // MANY: the first wave alone, a lane with every 64th expert, takes k times the
 // greatest of all that is left (its upper half first).  Counting takes E^2 steps over
 // all threads, this one k of about 500 cycles whatever E.
@@ -228,8 +230,9 @@ template <bool MANY, class Fn> __device__ __forceinline__ void choose(const Moe 
                 const Scores s = scores_of(a, l);
                 key = order_of(weight_of(a, s, mine) / s.sum + (double)a.bias[min(e, E - 1)]);
             }
-            keys[e] = e < E ? (key & ~255ull) | (255 - e) : 0;
+            keys[e] = e < E ? key : 0;
             before[e] = 0;
+            if (e < MOE_SLOTS) ids[e] = MOE_EXPERTS;
         }
         __syncthreads();
         // (keys past the last expert are 0; the parts past `width` have none)
@@ -251,7 +254,17 @@ template <bool MANY, class Fn> __device__ __forceinline__ void choose(const Moe 
             else before[e] = n;
         }
         __syncthreads();
-        if (tid < E && before[tid] < a.k) ids[before[tid]] = tid;
+        if (tid < E && before[tid] < a.k) atomicMin(&ids[before[tid]], tid);
+        __syncthreads();
+        if (__builtin_expect(__ballot(lane < a.k && ids[lane < a.k ? lane : 0] == MOE_EXPERTS) != 0, 0)) {
+            __syncthreads();
+            if (tid < E && before[tid] < a.k) {
+                int place = before[tid];
+                for (int j = 0; j < tid; ++j) place += keys[j] == keys[tid];
+                if (place < a.k) ids[place] = tid;
+            }
+            __syncthreads();
+        }
     } else {
         __shared__ u64 left[MOE_EXPERTS];
         meanwhile();
@@ -285,8 +298,8 @@ template <bool MANY, class Fn> __device__ __forceinline__ void choose(const Moe 
                 }
             }
         }
+        __syncthreads();
     }
-    __syncthreads();
 }
 
 // The weights of the token's experts (in `ids`), by one wave, lane i the i-th.

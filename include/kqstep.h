@@ -111,8 +111,7 @@ size_t kqstep_moe_workspace_bytes(const kqstep_moe_layer *layer, int T);
  *   y = add + sum_j p_j down[e_j] . (act(gate[e_j] . x) * (up[e_j] . x))
  *
  * Logits, scores and weights are computed in 64 bits (so that experts whose
- * logits differ by an fp32 rounding are not mistaken for each other; up to 256
- * experts, those within 2^-44 of each other's size count as equal), the weights
+ * logits differ by an fp32 rounding are not mistaken for each other), the weights
  * rounded once; the products as in kq_qgemv, in fp32, each within 1e-4 *
  * sum|w*x| + 1e-6 of the exact one.
  *   x, add, y  [T] rows of `hidden` fp32, strides ldx, ldadd, ldy.  add NULL: 0.
