@@ -84,21 +84,18 @@ __device__ __forceinline__ u64 token_of(u32 key, int i) { return (u64)key << 32 
 struct Scale {
     double eighths, quarters;   // of an octave, per logit: 8 log2(e) / t, and half of it
     const double *steps;        // 2^(35 + (i + 1/2) / 8), i < 8, in LDS
-    // (an infinite logit's mantissa is that of the largest number; its bin is given by
-    // what it is compared with)
-    static __device__ __forceinline__ double finite(float l) {
-        return (double)__builtin_amdgcn_fmed3f(l, -3.402823466e38f, 3.402823466e38f);
-    }
-    __device__ __forceinline__ double bin(float l) const { return rint(fma(finite(l), eighths, -0.5)); }
+    // (an infinite logit's bin is given by what it is compared with)
+    __device__ __forceinline__ double bin(float l) const { return rint(fma((double)l, eighths, -0.5)); }
     // that of a first token: an infinite one lies above all others
     __device__ __forceinline__ double top_bin(float l) const { return l < __builtin_inff() ? bin(l) : __builtin_inf(); }
     // 2^52 more, in whose low bits it is rounded to an integer.  `of_octave`: the bin's
     // place in its octave
     __device__ __forceinline__ double mantissa_d(float l, int of_octave) const {
         // half of what is left, from the bin's middle at 1/2: 1/4 .. 3/4, and a rounding of
-        // the bin more.  (Past 2^35 bins only equal logits are in one, and any value does:
-        // 0 .. 1, which costs no instruction and lets sums be 2^(1/16) as large.)
-        const double y = fmin(fmax(fma(finite(l), quarters, fma(bin(l), -0.5, 0.25)), 0.0), 1.0);
+        // the bin more.  (Past 2^35 bins, or where it is no number, only equal logits are in
+        // one, and any value does: 0 .. 1, which costs no instruction and lets sums be
+        // 2^(1/16) as large.)
+        const double y = fmin(fmax(fma((double)l, quarters, fma(bin(l), -0.5, 0.25)), 0.0), 1.0);
         // 2^((2 y - 1) / 8) by the polynomial through six Chebyshev nodes: off by 2^-41
         double p = 0x1.5d8dfde822453p-20;
         p = fma(p, y, 0x1.1fe3316ea9487p-15);
