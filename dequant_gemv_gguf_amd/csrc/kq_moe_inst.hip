@@ -4,7 +4,7 @@
 // Bound: HBM (a token's experts' weights, read once) and, from three tokens on, the
 // vector units' work on them (8 of 128 experts of 2048 x 768, Q4_K and Q6_K, one token:
 // 16 us; eight tokens 47, 3.4 TB/s of the distinct experts' bytes; three tokens, 6 of 160
-// of 5120 x 1536, Q5_K and Q4_K: 85, 3.1 TB/s, the vector units busy half the time with
+// of 5120 x 1536, Q5_K and Q4_K: 84, 3.1 TB/s, the vector units busy half the time with
 // three waves a SIMD); for one token the chain of logits, choice, weights.
 // A work-group takes one token and a tile of rows, a wave one expert's rows of the
 // tile: it streams them through registers.  The activations are put into LDS once for
@@ -14,7 +14,7 @@
 // on their way: the loop itself reads no LDS.
 // An expert that several tokens chose is read once per token, but their
 // work-groups of one tile sit on one XCD and go through it side by side, so that
-// its L2 serves the second read.
+// its L2 serves the second read; it is unpacked for each.
 #include "kq_moe.h"
 
 namespace kq {
@@ -25,8 +25,10 @@ namespace step {
 constexpr int MOE_WAVES = 8;
 template <int T> constexpr int GATE_RESIDENT() { return BIG_UNIT<T>() || T == T_Q2_K ? 12 : 16; }
 template <int T> constexpr int DOWN_RESIDENT() { return BIG_UNIT<T>() ? 12 : 16; }
-// Units of a lane on their way in a wave.  (Two in the down kernel took a quarter of the
-// waves' registers and were slower: eight tokens 49.7 -> 48.3 us with one.)
+// Units of a lane on their way in a wave, of all formats.  (Two in the down kernel took a
+// quarter of the waves' registers and were slower: eight tokens 49.7 -> 48.3 us with one.
+// Four in gate and up: five tokens of Q8_0 16.8 -> 19.9, four 48.7 -> 50.2, six of Q2_K
+// 48.9 -> 53.6.)
 constexpr int GATE_DEPTH = 2, DOWN_DEPTH = 1;
 constexpr int MOE_LDS = 54 * 1024 / 4;         // floats of LDS that a launch asks for, at most (64 KB with the kernels' own)
 constexpr int MOE_RESULTS = 2048;              // of them for the rows' sums

@@ -26,7 +26,8 @@
 //    logits, a very high temperature) are not kept: the row is read for every digit, of
 //    11 bits there (one row of 151937 equal logits 400 us; of 8 bits 730).
 // Weights are 2^(l log2(e) / t) with 36 bits of mantissa, relative to the octave of
-// the row's largest.
+// the row's largest: a chunk's 8192 of them and their count are one 64-bit word, and a
+// probability, rounded to 2^-24, has 2^12 steps of them to a step of its own.
 #include "kq_step.h"
 
 #include <cmath>
@@ -1057,8 +1058,8 @@ __global__ __launch_bounds__(ROW_THREADS) void row_kernel(const Sample a) {
     __syncthreads();
     // Its token.  Where its chunk keeps up to half of its tokens down to bin `low`, these
     // alone, by their places' upper bits and then one by one; else all of the chunk's (8
-    // rows of 128256 22 us, with all of the chunk's 23.4; up to a quarter of them 8 rows
-    // are even, 256 of 151937 76.3, up to half 75.5, up to three quarters 75.6).
+    // rows of 128256 22 us, with all of the chunk's 23.4; with a quarter, half or three
+    // quarters as the limit they are even, and 256 of 151937 within 1 %).
     const int64_t chosen = chunk0 + m.n;
     const int below = low - m.off[m.n], kept_n = scan && below >= 0 ? a.upto[chosen * BINS + below] : CHUNK;
     constexpr int EVERY = 4, PIECES = 256, PIECE = CHUNK / PIECES;
